@@ -367,6 +367,112 @@ CONV3D_API conv3d_status_t conv3d_bwd_weight_cached(const void* x, const void* p
                                                     void* workspace, size_t ws_bytes,
                                                     struct CUstream_st* stream);
 
+/*
+ * Channel-wise operators: what stands beside the convolutions in a block that
+ * mixes the channels of each pixel by itself.  Activations are matrices
+ * [rows, C], one row a pixel (rows = N*D*H*W of an NDHWC tensor) or token, and
+ * C (or K and N) a multiple of 8; 16-bit tensors, fp32 statistics and sums, one
+ * round-to-nearest-even to the dtype.  Any number of rows from 1 up.  The pages
+ * name the operators next to their convolutions (Metal FlashAttention post:
+ * GEMM and layer norm shaders with backward passes; LoRA post: training on
+ * device, where activation memory is short); the interface is this library's.
+ *
+ * 8-bit activation checkpoint.  A training step keeps activations for its
+ * backward pass; a checkpoint keeps one in 1.03 bytes a value.  Blocks of 32
+ * consecutive channels of a row share one exponent byte b and hold signed 8-bit
+ * codes k, each standing for k * 2^(b-133):
+ *   codes     int8  [rows, 32 * ceil(C/32)], zero behind channel C
+ *   exponents uint8 [rows, ceil(C/32)],  b = max(7, biased exponent of the
+ *             block's largest magnitude), or 255 when the block holds an infinity
+ *             or NaN: then all 32 read back as NaN (their codes are unspecified).
+ *   k = clamp(round_half_even(v / 2^(b-133)), -127, 127)
+ * so a value is off by at most half a step (a step where it clamps, 127.5 to
+ * 128 steps): at most 1/64 of the block's largest magnitude, and every code is
+ * exact in bf16.  Both buffers 16-byte aligned.
+ */
+typedef enum {
+  CONV3D_ACT_NONE = 0,
+  CONV3D_ACT_SILU = 1, /* v / (1 + e^-v) */
+  CONV3D_ACT_GELU = 2  /* v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+} conv3d_act_t;
+
+/*
+ * conv3d_layernorm_fwd -- y = xh * gamma + beta, xh = (x - mean) * rstd, mean and
+ * rstd = 1/sqrt(var + eps) (biased) over the C channels of each row, C <= 8192.
+ * gamma, beta: [C] of the dtype or NULL (1, 0).  y may be exactly x.  Optional
+ * outputs for the backward pass: mean, rstd (fp32 [rows]) and the 8-bit
+ * checkpoint of xh (codes and exponents, both or neither).  One read of x.
+ */
+CONV3D_API conv3d_status_t conv3d_layernorm_fwd(const void* x, const void* gamma, const void* beta,
+                                                void* y, float* mean, float* rstd, void* codes,
+                                                void* exponents, long long rows, int C, float eps,
+                                                conv3d_dtype_t dtype, struct CUstream_st* stream);
+
+/*
+ * conv3d_layernorm_bwd -- with g = dy * gamma:
+ *   dx = rstd * (g - mean_c(g) - xh * mean_c(g * xh)) + dres
+ *   dgamma = sum over rows of dy * xh,  dbeta = sum over rows of dy
+ * from x with mean, or from the checkpoint of xh (codes, exponents; x and mean
+ * NULL).  dres ([rows, C], e.g. the gradient of a skip connection) may be NULL;
+ * dgamma and dbeta ([C]) may each be NULL.  dx may be exactly dy, x or dres.
+ * Partial sums in the workspace (conv3d_layernorm_bwd_workspace_bytes(), device,
+ * 256-byte aligned, not needed without dgamma and dbeta) are added in a fixed
+ * order: the same inputs give the same bits.
+ */
+CONV3D_API conv3d_status_t conv3d_layernorm_bwd(const void* dy, const void* x, const float* mean,
+                                                const void* codes, const void* exponents,
+                                                const float* rstd, const void* gamma,
+                                                const void* dres, void* dx, void* dgamma, void* dbeta,
+                                                long long rows, int C, conv3d_dtype_t dtype,
+                                                void* workspace, size_t ws_bytes,
+                                                struct CUstream_st* stream);
+CONV3D_API size_t conv3d_layernorm_bwd_workspace_bytes(long long rows, int C);
+
+/* conv3d_act8_pack -- the checkpoint of x [rows, C] (C <= 2^24). */
+CONV3D_API conv3d_status_t conv3d_act8_pack(const void* x, void* codes, void* exponents,
+                                            long long rows, int C, conv3d_dtype_t dtype,
+                                            struct CUstream_st* stream);
+
+/* conv3d_act8_unpack -- y = act(v * gamma + beta) of a checkpoint's values v:
+ * the activation recomputed for the backward pass (the normalised value through
+ * the norm's affine map, a pre-activation through its activation, or, with NULL
+ * gamma and beta and CONV3D_ACT_NONE, the values themselves, exact in bf16). */
+CONV3D_API conv3d_status_t conv3d_act8_unpack(const void* codes, const void* exponents,
+                                              const void* gamma, const void* beta, conv3d_act_t act,
+                                              void* y, long long rows, int C, conv3d_dtype_t dtype,
+                                              struct CUstream_st* stream);
+
+/* conv3d_act8_bwd -- dx = dy * act'(v) of a checkpoint's values v.  dx may be exactly dy. */
+CONV3D_API conv3d_status_t conv3d_act8_bwd(const void* dy, const void* codes, const void* exponents,
+                                           conv3d_act_t act, void* dx, long long rows, int C,
+                                           conv3d_dtype_t dtype, struct CUstream_st* stream);
+
+/*
+ * conv3d_linear_fwd -- y = act(x w^T + bias) + residual, x [rows, K], w [N, K]
+ * (a 1x1x1 convolution's weight), bias [N] or NULL, residual [rows, N] or NULL, y
+ * [rows, N]; the sum, the activation and the residual in fp32, one rounding.
+ * codes and exponents (both or neither): the 8-bit checkpoint of the
+ * pre-activation x w^T + bias, coded from fp32.  y may be exactly the residual.
+ * Needs no workspace; the same inputs give the same bits.
+ */
+CONV3D_API conv3d_status_t conv3d_linear_fwd(const void* x, const void* w, const void* bias,
+                                             const void* residual, void* y, void* codes,
+                                             void* exponents, long long rows, int K, int N,
+                                             conv3d_act_t act, conv3d_dtype_t dtype,
+                                             struct CUstream_st* stream);
+
+/*
+ * conv3d_linear_bwd_data -- dx = (dy w) * act'(v), dy [rows, N], w [N, K], dx
+ * [rows, K], v the checkpoint [rows, K] of what the activation that produced x
+ * was applied to (x = act(v)); CONV3D_ACT_NONE: dx = dy w, codes and exponents
+ * unused.  w is read as it lies; no workspace.  The weight's and the bias's
+ * gradients are conv3d_bwd_weight's with kernel {1,1,1}, D = H = 1, W = rows.
+ */
+CONV3D_API conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void* codes,
+                                                  const void* exponents, conv3d_act_t act, void* dx,
+                                                  long long rows, int K, int N, conv3d_dtype_t dtype,
+                                                  struct CUstream_st* stream);
+
 /* Device scratch bytes conv3d_fwd_ws needs for this problem: the folded
  * first-frame weight for CONV3D_TPAD_CAUSAL_REPLICATE with D == 1 and kt > 1,
  * 0 otherwise (also 0 for invalid sizes or a NULL kernel). */

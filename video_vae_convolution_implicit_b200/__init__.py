@@ -14,11 +14,18 @@ in front of a decoder convolution (groupnorm_stats / groupnorm_silu), the
 backward pass (conv3d_bwd_data, conv3d_bwd_weight) and a torch.autograd
 wrapper over both directions (Conv3dFunction / conv3d_autograd).  Each call has
 a raw-pointer twin (``*_ptr``) that returns the library's status code.
+
+Channel-wise operators on [..., C] tensors, a row per pixel or token: layer norm
+(layernorm, layernorm_bwd), 8-bit activation checkpoints (Act8, act8_pack,
+act8_unpack, act8_bwd), the channel product with its epilogue (linear,
+linear_bwd_data, linear_bwd_weight) and the channel MLP block made of them
+(channel_mlp, channel_mlp_bwd), each with a torch.autograd wrapper.
 """
 from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -32,6 +39,12 @@ __all__ = [
     "conv3d_bwd_weight", "conv3d_bwd_weight_ptr", "bwd_weight_workspace_bytes",
     "conv3d_bwd_data_cached", "conv3d_bwd_weight_cached",
     "Conv3dFunction", "conv3d_autograd",
+    "ACT_NONE", "ACT_SILU", "ACT_GELU", "Act8", "act8_pack", "act8_unpack", "act8_bwd",
+    "layernorm", "layernorm_bwd", "layernorm_bwd_workspace_bytes", "LayerNormFunction",
+    "layernorm_autograd", "linear", "linear_bwd_data", "linear_bwd_weight", "LinearFunction",
+    "linear_autograd", "ChannelMlpSaved", "channel_mlp", "channel_mlp_bwd", "ChannelMlpFunction",
+    "channel_mlp_autograd", "layernorm_fwd_ptr", "layernorm_bwd_ptr", "act8_pack_ptr",
+    "act8_unpack_ptr", "act8_bwd_ptr", "linear_fwd_ptr", "linear_bwd_data_ptr",
     "poll_status", "selftest_wait_timeout", "release", "test_arm_stall",
 ]
 
@@ -41,6 +54,9 @@ TPAD_ZERO = 0
 TPAD_CAUSAL_REPLICATE = 1
 TPAD_CAUSAL_ZERO = 2
 TPAD_CAUSAL_CACHED = 3
+ACT_NONE = 0
+ACT_SILU = 1
+ACT_GELU = 2
 
 
 class Status:
@@ -121,6 +137,23 @@ _lib.conv3d_fwd_gn.argtypes = ([_vp, _vp, _vp, _vp, _c, _c, _c] + [_vp] * 4 + [_
                                 + [_c, _c, _vp, _c, ctypes.c_float, _vp])
 _lib.conv3d_test_arm_stall.restype = _c
 _lib.conv3d_test_arm_stall.argtypes = [_c, _c]
+_ll = ctypes.c_longlong
+_lib.conv3d_layernorm_fwd.restype = _c
+_lib.conv3d_layernorm_fwd.argtypes = [_vp] * 8 + [_ll, _c, ctypes.c_float, _c, _vp]
+_lib.conv3d_layernorm_bwd.restype = _c
+_lib.conv3d_layernorm_bwd.argtypes = [_vp] * 11 + [_ll, _c, _c, _vp, ctypes.c_size_t, _vp]
+_lib.conv3d_layernorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+_lib.conv3d_layernorm_bwd_workspace_bytes.argtypes = [_ll, _c]
+_lib.conv3d_act8_pack.restype = _c
+_lib.conv3d_act8_pack.argtypes = [_vp] * 3 + [_ll, _c, _c, _vp]
+_lib.conv3d_act8_unpack.restype = _c
+_lib.conv3d_act8_unpack.argtypes = [_vp] * 4 + [_c, _vp, _ll, _c, _c, _vp]
+_lib.conv3d_act8_bwd.restype = _c
+_lib.conv3d_act8_bwd.argtypes = [_vp] * 3 + [_c, _vp, _ll, _c, _c, _vp]
+_lib.conv3d_linear_fwd.restype = _c
+_lib.conv3d_linear_fwd.argtypes = [_vp] * 7 + [_ll, _c, _c, _c, _c, _vp]
+_lib.conv3d_linear_bwd_data.restype = _c
+_lib.conv3d_linear_bwd_data.argtypes = [_vp] * 4 + [_c, _vp, _ll, _c, _c, _c, _vp]
 
 
 def raw_library() -> ctypes.CDLL:
@@ -498,37 +531,501 @@ def conv3d_bwd_weight_cached(x: torch.Tensor, prev: torch.Tensor | None, dy: tor
 class Conv3dFunction(torch.autograd.Function):
     """torch.autograd wrapper: forward through conv3d_fwd, backward through
     conv3d_bwd_data (dx; temporal stride 1) and conv3d_bwd_weight (dw, dbias).
-    The residual's gradient is dy itself.  Marshalling only: every product runs
-    in the library's kernels, none in torch."""
+    The residual's gradient is dy itself.  With checkpoint8 the input is kept as
+    an 8-bit checkpoint (Act8), which only dw reads.  Marshalling only: every
+    product runs in the library's kernels, none in torch."""
 
     @staticmethod
-    def forward(ctx, x, w, bias, residual, stride, pad, tpad):
+    def forward(ctx, x, w, bias, residual, stride, pad, tpad, checkpoint8=False):
         y = conv3d(x, w, bias, residual, stride, pad, tpad)
-        ctx.save_for_backward(x, w)
+        if checkpoint8:
+            a = act8_pack(x)
+            ctx.save_for_backward(w, a.codes, a.exponents)
+        else:
+            ctx.save_for_backward(w, x)
         ctx.conf = (tuple(stride), tuple(pad), tpad, bias is not None, residual is not None)
+        ctx.x_shape = tuple(x.shape)
         return y
 
     @staticmethod
     def backward(ctx, dy):
-        x, w = ctx.saved_tensors
+        w, *saved = ctx.saved_tensors
         stride, pad, tpad, has_bias, has_res = ctx.conf
         dy = dy.contiguous()
         dx = dw = db = dres = None
         if ctx.needs_input_grad[0]:
             if stride[0] != 1:
                 raise NotImplementedError("the input gradient supports temporal stride 1 only")
-            dx = conv3d_bwd_data(dy, w, x.shape, pad, tpad, stride=stride)
+            dx = conv3d_bwd_data(dy, w, ctx.x_shape, pad, tpad, stride=stride)
         if ctx.needs_input_grad[1] or (has_bias and ctx.needs_input_grad[2]):
+            x = saved[0] if len(saved) == 1 else act8_unpack(Act8(*saved, ctx.x_shape[-1]), w.dtype)
             dw, db = conv3d_bwd_weight(x, dy, tuple(w.shape[1:4]), stride, pad, tpad,
                                        with_bias=has_bias)
             if not ctx.needs_input_grad[1]:
                 dw = None
         if has_res and ctx.needs_input_grad[3]:
             dres = dy
-        return dx, dw, db, dres, None, None, None
+        return dx, dw, db, dres, None, None, None, None
 
 
 def conv3d_autograd(x, w, bias=None, residual=None, stride=(1, 1, 1), pad=(0, 1, 1),
-                    tpad=TPAD_CAUSAL_REPLICATE):
-    """y = conv3d(x, w) + bias + residual with gradients for x, w, bias and residual."""
-    return Conv3dFunction.apply(x, w, bias, residual, tuple(stride), tuple(pad), tpad)
+                    tpad=TPAD_CAUSAL_REPLICATE, checkpoint8=False):
+    """y = conv3d(x, w) + bias + residual with gradients for x, w, bias and residual.
+    checkpoint8: keep x for the weight gradient in 8 bits (1.03 bytes a value)."""
+    return Conv3dFunction.apply(x, w, bias, residual, tuple(stride), tuple(pad), tpad, checkpoint8)
+
+
+# ---------------------------------------------------------------- channel-wise operators
+#
+# Tensors are [..., C], contiguous, bf16 or fp16; every leading extent counts as
+# rows.  All tensors of a call live on one CUDA device, which need not be the
+# current one; the default stream is that device's current stream.
+
+
+def layernorm_fwd_ptr(x, gamma, beta, y, mean, rstd, codes, exponents, rows, C, eps, dtype, stream) -> int:
+    """Raw-pointer call of conv3d_layernorm_fwd; returns the status code."""
+    return _lib.conv3d_layernorm_fwd(x, gamma, beta, y, mean, rstd, codes, exponents, rows, C, eps, dtype, stream)
+
+
+def layernorm_bwd_ptr(dy, x, mean, codes, exponents, rstd, gamma, dres, dx, dgamma, dbeta, rows, C, dtype,
+                      workspace, ws_bytes, stream) -> int:
+    """Raw-pointer call of conv3d_layernorm_bwd; returns the status code."""
+    return _lib.conv3d_layernorm_bwd(dy, x, mean, codes, exponents, rstd, gamma, dres, dx, dgamma, dbeta, rows, C,
+                                     dtype, workspace, ws_bytes, stream)
+
+
+def layernorm_bwd_workspace_bytes(rows: int, C: int) -> int:
+    return int(_lib.conv3d_layernorm_bwd_workspace_bytes(rows, C))
+
+
+def act8_pack_ptr(x, codes, exponents, rows, C, dtype, stream) -> int:
+    """Raw-pointer call of conv3d_act8_pack; returns the status code."""
+    return _lib.conv3d_act8_pack(x, codes, exponents, rows, C, dtype, stream)
+
+
+def act8_unpack_ptr(codes, exponents, gamma, beta, act, y, rows, C, dtype, stream) -> int:
+    """Raw-pointer call of conv3d_act8_unpack; returns the status code."""
+    return _lib.conv3d_act8_unpack(codes, exponents, gamma, beta, act, y, rows, C, dtype, stream)
+
+
+def act8_bwd_ptr(dy, codes, exponents, act, dx, rows, C, dtype, stream) -> int:
+    """Raw-pointer call of conv3d_act8_bwd; returns the status code."""
+    return _lib.conv3d_act8_bwd(dy, codes, exponents, act, dx, rows, C, dtype, stream)
+
+
+def linear_fwd_ptr(x, w, bias, residual, y, codes, exponents, rows, K, N, act, dtype, stream) -> int:
+    """Raw-pointer call of conv3d_linear_fwd; returns the status code."""
+    return _lib.conv3d_linear_fwd(x, w, bias, residual, y, codes, exponents, rows, K, N, act, dtype, stream)
+
+
+def linear_bwd_data_ptr(dy, w, codes, exponents, act, dx, rows, K, N, dtype, stream) -> int:
+    """Raw-pointer call of conv3d_linear_bwd_data; returns the status code."""
+    return _lib.conv3d_linear_bwd_data(dy, w, codes, exponents, act, dx, rows, K, N, dtype, stream)
+
+
+class Act8(NamedTuple):
+    """An 8-bit activation checkpoint of a [..., C] tensor: int8 codes
+    [..., 32 * ceil(C/32)] and uint8 exponents [..., ceil(C/32)] (conv3d.h)."""
+    codes: torch.Tensor
+    exponents: torch.Tensor
+    channels: int
+
+    @staticmethod
+    def empty(shape, device) -> "Act8":
+        blocks = -(-shape[-1] // 32)
+        lead = tuple(shape[:-1])
+        return Act8(torch.empty((*lead, blocks * 32), dtype=torch.int8, device=device),
+                    torch.empty((*lead, blocks), dtype=torch.uint8, device=device), int(shape[-1]))
+
+
+class _On:
+    """Makes the tensors' device current for a call, where it is not already."""
+    __slots__ = ("guard",)
+
+    def __init__(self, t):
+        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _tensor(name, t, like, shape, dtype=None):
+    """Checks one operand: a contiguous CUDA tensor on ``like``'s device."""
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
+    if t.dtype != (like.dtype if dtype is None else dtype):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype if dtype is None else dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _main(name, t):
+    """Checks a call's leading operand; returns (rows, channels)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() < 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [..., C] tensor")
+    C = t.shape[-1]
+    return (t.numel() // C if C else 0), C
+
+
+def _act8(name, a, shape, device):
+    """Checks a checkpoint of a tensor of ``shape``."""
+    if a.channels != shape[-1]:
+        raise ValueError(f"{name} holds {a.channels} channels, expected {shape[-1]}")
+    lead, blocks = tuple(shape[:-1]), -(-shape[-1] // 32)
+    for part, t, dt, n in (("codes", a.codes, torch.int8, blocks * 32), ("exponents", a.exponents, torch.uint8, blocks)):
+        if t.device != device or t.dtype != dt or tuple(t.shape) != (*lead, n) or not t.is_contiguous():
+            raise ValueError(f"{name}.{part} must be a contiguous {dt} tensor {(*lead, n)} on {device}")
+
+
+def _stream_on(t, stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return _stream_handle(stream)
+
+
+def act8_pack(x: torch.Tensor, stream=None) -> Act8:
+    """The 8-bit checkpoint of x [..., C]."""
+    rows, C = _main("x", x)
+    a = Act8.empty(x.shape, x.device)
+    with _On(x):
+        _check(_lib.conv3d_act8_pack(x.data_ptr(), a.codes.data_ptr(), a.exponents.data_ptr(), rows, C,
+                                     _dtype_code(x.dtype), _stream_on(x, stream)))
+    return a
+
+
+def act8_unpack(a: Act8, dtype: torch.dtype, gamma=None, beta=None, act: int = ACT_NONE,
+                y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """act(v * gamma + beta) of the checkpoint's values v, as a ``dtype`` tensor."""
+    shape = (*a.codes.shape[:-1], a.channels)
+    _act8("a", a, shape, a.codes.device)
+    if not a.codes.is_cuda:
+        raise ValueError("a must hold CUDA tensors")
+    if y is None:
+        y = torch.empty(shape, dtype=dtype, device=a.codes.device)
+    else:
+        _tensor("y", y, a.codes, shape, dtype)
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        if t is not None:
+            _tensor(name, t, y, (a.channels,))
+    with _On(y):
+        _check(_lib.conv3d_act8_unpack(a.codes.data_ptr(), a.exponents.data_ptr(), _ptr(gamma), _ptr(beta), act,
+                                       y.data_ptr(), y.numel() // a.channels, a.channels, _dtype_code(dtype),
+                                       _stream_on(y, stream)))
+    return y
+
+
+def act8_bwd(dy: torch.Tensor, a: Act8, act: int, dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dy * act'(v) of the checkpoint's values v (``dx`` may be ``dy``)."""
+    rows, C = _main("dy", dy)
+    _act8("a", a, dy.shape, dy.device)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    elif dx is not dy:
+        _tensor("dx", dx, dy, dy.shape)
+    with _On(dy):
+        _check(_lib.conv3d_act8_bwd(dy.data_ptr(), a.codes.data_ptr(), a.exponents.data_ptr(), act, dx.data_ptr(),
+                                    rows, C, _dtype_code(dy.dtype), _stream_on(dy, stream)))
+    return dx
+
+
+def layernorm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-6, with_stats: bool = False,
+              checkpoint8: bool = False, y: torch.Tensor | None = None, stream=None):
+    """y = (x - mean) * rstd * gamma + beta over the last axis of x [..., C].
+
+    Returns y; with ``with_stats`` (y, mean, rstd), fp32 [...]; with
+    ``checkpoint8`` (y, xhat, rstd), xhat the :class:`Act8` of (x - mean) * rstd:
+    either is what :func:`layernorm_bwd` needs.  ``y`` may be ``x``.
+    """
+    rows, C = _main("x", x)
+    if with_stats and checkpoint8:
+        raise ValueError("with_stats and checkpoint8 exclude each other")
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        if t is not None:
+            _tensor(name, t, x, (C,))
+    if y is None:
+        y = torch.empty_like(x)
+    elif y is not x:
+        _tensor("y", y, x, x.shape)
+    mean = rstd = a = None
+    if with_stats or checkpoint8:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    if with_stats:
+        mean = torch.empty_like(rstd)
+    if checkpoint8:
+        a = Act8.empty(x.shape, x.device)
+    with _On(x):
+        _check(_lib.conv3d_layernorm_fwd(x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(mean), _ptr(rstd),
+                                         None if a is None else a.codes.data_ptr(),
+                                         None if a is None else a.exponents.data_ptr(), rows, C, eps,
+                                         _dtype_code(x.dtype), _stream_on(x, stream)))
+    if checkpoint8:
+        return y, a, rstd
+    return (y, mean, rstd) if with_stats else y
+
+
+def layernorm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, mean: torch.Tensor | None = None, gamma=None,
+                  dres=None, with_params: bool = True, dx: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """(dx, dgamma, dbeta) of :func:`layernorm`; dgamma and dbeta are None without ``with_params``.
+
+    saved: x (then ``mean`` is needed) or the :class:`Act8` of the normalised x.
+    dres: added to dx (the gradient of a skip connection around the norm).
+    """
+    rows, C = _main("dy", dy)
+    lead = dy.shape[:-1]
+    _tensor("rstd", rstd, dy, lead, torch.float32)
+    x = codes = exponents = None
+    if isinstance(saved, Act8):
+        if mean is not None:
+            raise ValueError("mean belongs to x: a checkpoint holds the normalised values")
+        _act8("saved", saved, dy.shape, dy.device)
+        codes, exponents = saved.codes, saved.exponents
+    else:
+        x = saved
+        _tensor("saved", x, dy, dy.shape)
+        if mean is None:
+            raise ValueError("x needs its mean")
+        _tensor("mean", mean, dy, lead, torch.float32)
+    if gamma is not None:
+        _tensor("gamma", gamma, dy, (C,))
+    if dres is not None:
+        _tensor("dres", dres, dy, dy.shape)
+    if dx is None:
+        dx = torch.empty_like(dy)
+    elif dx is not dy:
+        _tensor("dx", dx, dy, dy.shape)
+    dgamma = dbeta = None
+    ws_bytes = 0
+    if with_params:
+        dgamma = torch.empty((C,), dtype=dy.dtype, device=dy.device)
+        dbeta = torch.empty((C,), dtype=dy.dtype, device=dy.device)
+        if workspace is None:
+            workspace = torch.empty((layernorm_bwd_workspace_bytes(rows, C),), dtype=torch.uint8, device=dy.device)
+        elif not workspace.is_cuda or workspace.device != dy.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous CUDA tensor on {dy.device}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    with _On(dy):
+        _check(_lib.conv3d_layernorm_bwd(dy.data_ptr(), _ptr(x), _ptr(mean), _ptr(codes), _ptr(exponents),
+                                         rstd.data_ptr(), _ptr(gamma), _ptr(dres), dx.data_ptr(), _ptr(dgamma),
+                                         _ptr(dbeta), rows, C, _dtype_code(dy.dtype),
+                                         workspace.data_ptr() if with_params else None, ws_bytes,
+                                         _stream_on(dy, stream)))
+    return dx, dgamma, dbeta
+
+
+def _weight(w, like, K, N=None):
+    """Checks a [N, K] weight (or a 1x1x1 convolution's [N, 1, 1, 1, K]); returns N."""
+    if w.dim() not in (2, 5) or w.shape[-1] != K or (N is not None and w.shape[0] != N) or w.numel() != w.shape[0] * K:
+        raise ValueError(f"w must be [N, {K}] or [N, 1, 1, 1, {K}]" + ("" if N is None else f" with N = {N}") +
+                         f", got {tuple(w.shape)}")
+    _tensor("w", w, like, w.shape)
+    return w.shape[0]
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: int = ACT_NONE,
+           checkpoint8: bool = False, y: torch.Tensor | None = None, stream=None):
+    """y = act(x w^T + bias) + residual for x [..., K], w [N, K] (or [N, 1, 1, 1, K]).
+
+    With ``checkpoint8`` returns (y, pre): pre is the :class:`Act8` of x w^T + bias.
+    ``y`` may be ``residual``.
+    """
+    rows, K = _main("x", x)
+    N = _weight(w, x, K)
+    shape = (*x.shape[:-1], N)
+    if bias is not None:
+        _tensor("bias", bias, x, (N,))
+    if residual is not None:
+        _tensor("residual", residual, x, shape)
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    elif y is not residual:
+        _tensor("y", y, x, shape)
+    a = Act8.empty(shape, x.device) if checkpoint8 else None
+    with _On(x):
+        _check(_lib.conv3d_linear_fwd(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
+                                      None if a is None else a.codes.data_ptr(),
+                                      None if a is None else a.exponents.data_ptr(), rows, K, N, act,
+                                      _dtype_code(x.dtype), _stream_on(x, stream)))
+    return (y, a) if checkpoint8 else y
+
+
+def linear_bwd_data(dy: torch.Tensor, w: torch.Tensor, pre: Act8 | None = None, act: int = ACT_NONE,
+                    dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """dx = (dy w) * act'(pre) for dy [..., N], w [N, K]: the gradient of x, or, with the
+    checkpoint ``pre`` of what ``act`` was applied to (x = act(pre)), of that argument."""
+    rows, N = _main("dy", dy)
+    K = w.shape[-1] if w.dim() else 0
+    _weight(w, dy, K, N)
+    shape = (*dy.shape[:-1], K)
+    if act != ACT_NONE and pre is None:
+        raise ValueError("the derivative of an activation needs the checkpoint of its argument")
+    if pre is not None:
+        _act8("pre", pre, shape, dy.device)
+    if dx is None:
+        dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+    else:
+        _tensor("dx", dx, dy, shape)
+    with _On(dy):
+        _check(_lib.conv3d_linear_bwd_data(dy.data_ptr(), w.data_ptr(), None if pre is None else pre.codes.data_ptr(),
+                                           None if pre is None else pre.exponents.data_ptr(), act, dx.data_ptr(),
+                                           rows, K, N, _dtype_code(dy.dtype), _stream_on(dy, stream)))
+    return dx
+
+
+def linear_bwd_weight(x: torch.Tensor, dy: torch.Tensor, with_bias: bool = True,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """(dw [N, K], dbias [N]) of :func:`linear` without activation: the weight
+    gradient of a 1x1x1 convolution over the rows as pixels (conv3d_bwd_weight)."""
+    rows, K = _main("x", x)
+    N = dy.shape[-1] if dy.dim() else 0
+    _tensor("dy", dy, x, (*x.shape[:-1], N))
+    if rows < 1 or rows > 0x7FFFFFFF:
+        raise ValueError(f"rows must be in [1, 2^31), got {rows}")
+    with _On(x):
+        dw, db = conv3d_bwd_weight(x.view(1, 1, 1, rows, K), dy.view(1, 1, 1, rows, N), (1, 1, 1), (1, 1, 1),
+                                   (0, 0, 0), TPAD_ZERO, with_bias, workspace, _stream_on(x, stream))
+    return dw.view(N, K), db
+
+
+class ChannelMlpSaved(NamedTuple):
+    """What :func:`channel_mlp` keeps for its backward pass, beside the weights:
+    the checkpoints of the normalised input and of the pre-activation."""
+    xhat: Act8
+    rstd: torch.Tensor
+    pre: Act8
+
+
+def channel_mlp(x: torch.Tensor, gamma, beta, w1: torch.Tensor, b1, w2: torch.Tensor, b2, act: int = ACT_GELU,
+                eps: float = 1e-6, save: bool = False, stream=None):
+    """y = x + act(layernorm(x) w1^T + b1) w2^T + b2 over the channels of x [..., C];
+    w1 [H, C], w2 [C, H].  With ``save`` returns (y, :class:`ChannelMlpSaved`): about
+    1.03 (C + H) bytes a row in place of the 16-bit activations (2 (2C + 2H))."""
+    if not save:
+        n = layernorm(x, gamma, beta, eps, stream=stream)
+        return linear(linear(n, w1, b1, None, act, stream=stream), w2, b2, x, stream=stream)
+    n, xhat, rstd = layernorm(x, gamma, beta, eps, checkpoint8=True, stream=stream)
+    h, pre = linear(n, w1, b1, None, act, checkpoint8=True, stream=stream)
+    return linear(h, w2, b2, x, stream=stream), ChannelMlpSaved(xhat, rstd, pre)
+
+
+def channel_mlp_bwd(dy: torch.Tensor, saved: ChannelMlpSaved, gamma, beta, w1: torch.Tensor, w2: torch.Tensor,
+                    act: int = ACT_GELU, stream=None):
+    """(dx, dgamma, dbeta, dw1, db1, dw2, db2) of :func:`channel_mlp` from its checkpoints.
+
+    The two inputs that the weight gradients need are recomputed from the
+    checkpoints (one pass each); act' rides in the epilogue of dy w2 and the skip
+    connection's gradient in the layer norm's.
+    """
+    _main("dy", dy)
+    h = act8_unpack(saved.pre, dy.dtype, None, None, act, stream=stream)
+    dw2, db2 = linear_bwd_weight(h, dy, stream=stream)
+    dpre = linear_bwd_data(dy, w2, saved.pre, act, dx=h, stream=stream)   # h is read by then
+    n = act8_unpack(saved.xhat, dy.dtype, gamma, beta, stream=stream)
+    dw1, db1 = linear_bwd_weight(n, dpre, stream=stream)
+    dn = linear_bwd_data(dpre, w1, dx=n, stream=stream)
+    dx, dgamma, dbeta = layernorm_bwd(dn, saved.xhat, saved.rstd, gamma=gamma, dres=dy, dx=dn, stream=stream)
+    return dx, dgamma, dbeta, dw1, db1, dw2, db2
+
+
+class LayerNormFunction(torch.autograd.Function):
+    """torch.autograd wrapper of layernorm; with checkpoint8 it keeps the 8-bit
+    normalised input instead of x."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, eps, checkpoint8):
+        if checkpoint8:
+            y, a, rstd = layernorm(x, gamma, beta, eps, checkpoint8=True)
+            ctx.save_for_backward(gamma, rstd, a.codes, a.exponents)
+        else:
+            y, mean, rstd = layernorm(x, gamma, beta, eps, with_stats=True)
+            ctx.save_for_backward(gamma, rstd, x, mean)
+        ctx.conf = (checkpoint8, x.shape[-1])
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        gamma, rstd, s0, s1 = ctx.saved_tensors
+        checkpoint8, C = ctx.conf
+        saved, mean = (Act8(s0, s1, C), None) if checkpoint8 else (s0, s1)
+        need = ctx.needs_input_grad
+        dx, dgamma, dbeta = layernorm_bwd(dy.contiguous(), saved, rstd, mean, gamma, with_params=need[1] or need[2])
+        return dx if need[0] else None, dgamma if need[1] else None, dbeta if need[2] else None, None, None
+
+
+def layernorm_autograd(x, gamma=None, beta=None, eps: float = 1e-6, checkpoint8: bool = False):
+    """layernorm with gradients for x, gamma and beta."""
+    return LayerNormFunction.apply(x, gamma, beta, eps, checkpoint8)
+
+
+class LinearFunction(torch.autograd.Function):
+    """torch.autograd wrapper of linear.  With an activation the pre-activation
+    is kept as an 8-bit checkpoint."""
+
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, act):
+        if act != ACT_NONE:
+            y, a = linear(x, w, bias, residual, act, checkpoint8=True)
+            ctx.save_for_backward(x, w, a.codes, a.exponents)
+        else:
+            y = linear(x, w, bias, residual, act)
+            ctx.save_for_backward(x, w)
+        ctx.conf = (act, bias is not None, residual is not None)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, *a = ctx.saved_tensors
+        act, has_bias, has_res = ctx.conf
+        dy = dy.contiguous()
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if need[0] or need[1] or (has_bias and need[2]):
+            dpre = act8_bwd(dy, Act8(a[0], a[1], w.shape[0]), act) if act != ACT_NONE else dy
+            if need[0]:
+                dx = linear_bwd_data(dpre, w)
+            if need[1] or (has_bias and need[2]):
+                dw, db = linear_bwd_weight(x, dpre, with_bias=has_bias)
+                dw = dw.view(w.shape) if need[1] else None
+        return dx, dw, db if has_bias and need[2] else None, dy if has_res and need[3] else None, None
+
+
+def linear_autograd(x, w, bias=None, residual=None, act: int = ACT_NONE):
+    """y = act(x w^T + bias) + residual with gradients for x, w, bias and residual."""
+    return LinearFunction.apply(x, w, bias, residual, act)
+
+
+class ChannelMlpFunction(torch.autograd.Function):
+    """torch.autograd wrapper of channel_mlp: between forward and backward it keeps
+    the two checkpoints, rstd and the weights, no 16-bit activation."""
+
+    @staticmethod
+    def forward(ctx, x, gamma, beta, w1, b1, w2, b2, act, eps):
+        y, s = channel_mlp(x, gamma, beta, w1, b1, w2, b2, act, eps, save=True)
+        ctx.save_for_backward(gamma, beta, w1, w2, s.xhat.codes, s.xhat.exponents, s.rstd, s.pre.codes,
+                              s.pre.exponents)
+        ctx.conf = (act, x.shape[-1], w1.shape[0], b1 is not None, b2 is not None)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        gamma, beta, w1, w2, qc, qe, rstd, pc, pe = ctx.saved_tensors
+        act, C, H, has_b1, has_b2 = ctx.conf
+        dx, dg, dbt, dw1, db1, dw2, db2 = channel_mlp_bwd(
+            dy.contiguous(), ChannelMlpSaved(Act8(qc, qe, C), rstd, Act8(pc, pe, H)), gamma, beta, w1, w2, act)
+        grads = (dx, dg if gamma is not None else None, dbt if beta is not None else None, dw1.view(w1.shape),
+                 db1 if has_b1 else None, dw2.view(w2.shape), db2 if has_b2 else None)
+        return tuple(g if need else None for g, need in zip(grads, ctx.needs_input_grad)) + (None, None)
+
+
+def channel_mlp_autograd(x, gamma, beta, w1, b1, w2, b2, act: int = ACT_GELU, eps: float = 1e-6):
+    """channel_mlp with gradients for x, gamma, beta, w1, b1, w2 and b2."""
+    return ChannelMlpFunction.apply(x, gamma, beta, w1, b1, w2, b2, act, eps)

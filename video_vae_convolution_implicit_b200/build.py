@@ -1,4 +1,8 @@
-"""Build libconv3d.so (the CUDA library) in-tree with nvcc for sm_100a."""
+"""Build libconv3d.so (the CUDA library) in-tree with nvcc for sm_100a.
+
+The translation units are compiled side by side into build/ (one object each,
+recompiled when it or a header is newer) and linked.
+"""
 from __future__ import annotations
 
 import os
@@ -8,23 +12,47 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+OBJ = os.path.join(ROOT, "build")
 LIB = os.path.join(PKG, "libconv3d.so")
-SOURCES = [os.path.join(CSRC, "conv3d_api.cu"), os.path.join(CSRC, "groupnorm.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("conv3d_kernel.cuh", "wgrad_kernel.cuh", "ptx.cuh")] + [
-    os.path.join(ROOT, "include", "conv3d.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("conv3d_api.cu", "groupnorm.cu", "channel_ops.cu", "linear.cu")]
+# the headers that each unit includes (besides the public one)
+HEADERS = {
+    "conv3d_api.cu": ("conv3d_kernel.cuh", "wgrad_kernel.cuh", "pipeline.cuh", "ptx.cuh", "internal.h"),
+    "groupnorm.cu": (),
+    "channel_ops.cu": ("act8.cuh", "ptx.cuh", "internal.h"),
+    "linear.cu": ("linear_kernel.cuh", "act8.cuh", "pipeline.cuh", "ptx.cuh", "internal.h"),
+}
+FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+         "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
+         "-I", os.path.join(ROOT, "include"), "-I", CSRC]
 
 
-def nvcc_command(out: str = LIB, extra=()) -> list[str]:
-    return ["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo",
-            "-std=c++17", "--shared", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-            "-I", os.path.join(ROOT, "include"), "-I", CSRC, *extra, "-o", out, *SOURCES]
+def _deps(src: str) -> list[str]:
+    own = [os.path.join(CSRC, h) for h in HEADERS[os.path.basename(src)]]
+    return [src, os.path.join(ROOT, "include", "conv3d.h"), *own]
+
+
+def _newer(deps: list[str], than: str) -> bool:
+    return not os.path.exists(than) or any(os.path.getmtime(d) > os.path.getmtime(than) for d in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    stale = not os.path.exists(LIB) or any(os.path.getmtime(d) > os.path.getmtime(LIB) for d in DEPS)
-    if force or stale:
-        cmd = nvcc_command(extra=("-Xptxas", "-v") if verbose else ())
-        subprocess.run(cmd, check=True)
+    if not force and not _newer([d for s in SOURCES for d in _deps(s)], LIB):
+        return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    extra = ["-Xptxas", "-v"] if verbose else []
+    running, objects = [], []
+    for src in SOURCES:
+        obj = os.path.join(OBJ, os.path.basename(src) + ".o")
+        objects.append(obj)
+        if force or _newer(_deps(src), obj):
+            cmd = ["nvcc", *FLAGS, *extra, "-c", "-o", obj, src]
+            running.append((cmd, subprocess.Popen(cmd)))
+    failed = [cmd for cmd, p in running if p.wait() != 0]
+    if failed:
+        raise subprocess.CalledProcessError(1, failed[0])
+    subprocess.run(["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "--shared", "-o", LIB, *objects],
+                   check=True)
     return LIB
 
 

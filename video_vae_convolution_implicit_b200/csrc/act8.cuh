@@ -1,0 +1,160 @@
+// act8.cuh -- device arithmetic shared by the channel-wise operators: 16-bit
+// conversions, the activations and their derivatives, and the 8-bit
+// checkpoint code.
+//
+// Checkpoint code.  32 consecutive channels of a row share one exponent byte
+// b = max(7, biased exponent of the block's largest magnitude), and a value v
+// is kept as the integer k = clamp(rint(v * 2^(133-b)), -127, 127), which
+// stands for k * 2^(b-133): seven bits and a sign under a shared power of two
+// (the layout of the open MX formats' 8-bit integers).  A power-of-two step
+// makes the scaling exact, so one rounding (half a step, at most 1/128 of the
+// block's largest magnitude) is all that is lost, the same code comes out of
+// any precision that holds v, and every code is exactly representable in
+// bf16.  Against e4m3 with the same exponent byte (3 fraction bits: up to 1/16
+// of each value) the error of a block of normal deviates is about four times
+// smaller.  b = 255 marks a block with an infinity or NaN; all of it reads
+// back as NaN, so a diverged activation cannot pass as a finite one.  b >= 7
+// keeps 2^(133-b) and the step normal numbers; smaller values lose at most
+// 2^-127.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace conv3d {
+
+constexpr int kActNone = 0, kActSilu = 1, kActGelu = 2;   // conv3d_act_t
+
+template <bool kBF16>
+struct Val16 {
+  static __device__ __forceinline__ float lo(uint32_t w) {
+    if constexpr (kBF16) return __uint_as_float(w << 16);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(w & 0xFFFFu)));
+  }
+  static __device__ __forceinline__ float hi(uint32_t w) {
+    if constexpr (kBF16) return __uint_as_float(w & 0xFFFF0000u);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16)));
+  }
+  // two values rounded to nearest even, the first in the low half
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    if constexpr (kBF16) {
+      __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      return *reinterpret_cast<uint32_t*>(&h);
+    }
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
+    f[0] = lo(q.x); f[1] = hi(q.x); f[2] = lo(q.y); f[3] = hi(q.y);
+    f[4] = lo(q.z); f[5] = hi(q.z); f[6] = lo(q.w); f[7] = hi(q.w);
+  }
+  static __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+  }
+};
+
+// ------------------------------------------------------------------ activations
+
+// One special-function operation per activation: the hardware tanh, whose
+// error is about 2^-11 of a result of magnitude at most 1.  silu(v) = h + h
+// tanh(h), h = v/2; gelu(v) = h + h tanh(u(v)), u = sqrt(2/pi) (v + 0.044715
+// v^3).  The absolute error is at most |v| 2^-12, under half a bf16 step of v.
+__device__ __forceinline__ float tanh_hw(float x) {
+  float t;
+  asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(x));
+  return t;
+}
+
+constexpr float kGeluA = 0.7978845608028654f;             // sqrt(2 / pi)
+constexpr float kGeluC = 0.7978845608028654f * 0.044715f;
+
+template <int kAct>
+__device__ __forceinline__ float act_value(float v) {
+  if constexpr (kAct == kActSilu) {
+    const float h = 0.5f * v;
+    return fmaf(h, tanh_hw(h), h);
+  } else if constexpr (kAct == kActGelu) {
+    const float u = v * fmaf(kGeluC, v * v, kGeluA);
+    const float h = 0.5f * v;
+    return fmaf(h, tanh_hw(u), h);
+  } else {
+    return v;
+  }
+}
+
+// silu'(v) = s + v s (1 - s) with s = (1 + t)/2, t = tanh(v/2):
+//   = (1 + t)/2 + (v/4) (1 - t^2).
+// gelu'(v) = (1 + t)/2 + (v/2) (1 - t^2) u'(v), t = tanh(u(v)).
+template <int kAct>
+__device__ __forceinline__ float act_slope(float v) {
+  if constexpr (kAct == kActSilu) {
+    const float t = tanh_hw(0.5f * v);
+    const float c = 0.25f * v;
+    return fmaf(c, fmaf(-t, t, 1.0f), fmaf(0.5f, t, 0.5f));
+  } else if constexpr (kAct == kActGelu) {
+    const float v2 = v * v;
+    const float t = tanh_hw(v * fmaf(kGeluC, v2, kGeluA));
+    const float c = 0.5f * v * fmaf(3.0f * kGeluC, v2, kGeluA);
+    return fmaf(c, fmaf(-t, t, 1.0f), fmaf(0.5f, t, 0.5f));
+  } else {
+    return 1.0f;
+  }
+}
+
+// An infinite v makes u infinite and 1 - t^2 zero, and their product NaN; the
+// limits are used instead where |v| is so large that t has saturated.
+template <int kAct>
+__device__ __forceinline__ float act_slope_safe(float v) {
+  if constexpr (kAct == kActNone) return 1.0f;
+  const float c = fminf(fmaxf(v, -64.0f), 64.0f);
+  const float s = act_slope<kAct>(c);
+  return v == v ? s : v;
+}
+
+// ------------------------------------------------------------------ checkpoint code
+
+// Magnitude as an unsigned integer: ordered like the magnitudes, with
+// infinities and NaN above every finite one.
+__device__ __forceinline__ uint32_t a8_mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Exponent byte of a block whose largest magnitude has the bits `mag`.
+__device__ __forceinline__ uint32_t a8_exponent(uint32_t mag) {
+  const uint32_t b = mag >> 23;
+  return b < 7u ? 7u : b;
+}
+
+// 2^(133-b); 0 for a block marked as not finite.
+__device__ __forceinline__ float a8_inv_step(uint32_t b) {
+  return b == 255u ? 0.0f : __uint_as_float((260u - b) << 23);
+}
+
+// 2^(b-133); NaN for a block marked as not finite.
+__device__ __forceinline__ float a8_step(uint32_t b) {
+  return __uint_as_float(b == 255u ? 0x7FFFFFFFu : (b - 6u) << 23);
+}
+
+// Codes of four values, the first in the low byte.  v * inv + 1.5 * 2^23
+// rounds v * inv (exact: inv is a power of two) to the nearest integer, ties to
+// even, and leaves it in the low bits of the sum in two's complement.
+__device__ __forceinline__ uint32_t a8_code4(float a, float b, float c, float d, float inv) {
+  constexpr float kMagic = 12582912.0f;
+  const float lo = kMagic - 127.0f, hi = kMagic + 127.0f;
+  const uint32_t ia = __float_as_uint(fminf(fmaxf(fmaf(a, inv, kMagic), lo), hi));
+  const uint32_t ib = __float_as_uint(fminf(fmaxf(fmaf(b, inv, kMagic), lo), hi));
+  const uint32_t ic = __float_as_uint(fminf(fmaxf(fmaf(c, inv, kMagic), lo), hi));
+  const uint32_t id = __float_as_uint(fminf(fmaxf(fmaf(d, inv, kMagic), lo), hi));
+  return __byte_perm(__byte_perm(ia, ib, 0x0040), __byte_perm(ic, id, 0x0040), 0x5410);
+}
+
+// Values of four codes: the byte k + 128 under the exponent of 2^23 is the
+// float 2^23 + 128 + k, from which the subtraction leaves k exactly.
+__device__ __forceinline__ void a8_decode4(uint32_t w, float step, float* v) {
+  w ^= 0x80808080u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = (__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + i)) - 8388736.0f) * step;
+}
+
+}  // namespace conv3d

@@ -1,0 +1,854 @@
+// channel_ops.cu -- layer norm over the channels of each pixel (forward and
+// backward) and the 8-bit activation checkpoints (written, read back through an
+// affine map and an activation, and multiplied into a gradient).
+//
+// Every operator here reads and writes each element once with a handful of
+// operations between, so HBM bounds all of them: the layouts below keep whole
+// rows in registers (statistics in two passes over registers, one over memory)
+// and several 16-byte loads in flight per thread.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "act8.cuh"
+#include "conv3d.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace conv3d_channel {
+
+using namespace conv3d;
+using namespace conv3d_internal;
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------ row groups
+
+// A row belongs to a group of G threads: G = 8, 16 or 32 neighbouring lanes of
+// a warp, or the whole block of 256.  Thread `l` of the group holds the
+// 8-channel vectors l, l + G, ..., V of them.
+
+// Sums of N values over the threads of a group, in every thread.  Block-wide
+// groups pass through `red` ([2][8][N] floats), whose halves alternate (`flip`)
+// so that one barrier per sum is enough: a thread writes a half again only
+// after the barrier of the sum in between, which every reader of the half has
+// passed.
+template <int G, int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) {
+#pragma unroll
+  for (int o = (G < 32 ? G : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], o);
+  if constexpr (G > 32) {
+    float* r = red + flip * (8 * N);
+    flip ^= 1;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int n = 0; n < N; ++n) r[(threadIdx.x >> 5) * N + n] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) s += r[w * N + n];
+      v[n] = s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ layer norm, forward
+
+struct LnFwdParams {
+  const uint16_t* x;
+  const uint16_t* gamma;   // [C] or null (1)
+  const uint16_t* beta;    // [C] or null (0)
+  uint16_t* y;
+  float* mean;             // [rows] or null
+  float* rstd;             // [rows] or null
+  uint8_t* q;              // checkpoint of (x - mean) * rstd (kCkpt)
+  uint8_t* scales;
+  long long rows;
+  int C;
+  float eps;
+};
+
+// y = xh * gamma + beta, xh = (x - mean) / sqrt(var + eps).  A group loads R
+// rows at a time (R * V 16-byte loads in flight per thread), so the
+// reductions of the rows overlap; mean first, then the squared deviations from
+// it, both from registers: no cancellation however far the row is off centre.
+// The checkpoint's 32-channel blocks are four neighbouring threads' vectors.
+template <bool kBF16, int G, int V, int R, bool kCkpt>
+__global__ void __launch_bounds__(kThreads, 2) layernorm_fwd_kernel(const LnFwdParams p) {
+  using T = Val16<kBF16>;
+  __shared__ float red[G > 32 ? 2 * 8 * R : 1];
+  int flip = 0;
+  constexpr int kPerWarp = G < 32 ? 32 / G : 1;         // groups per warp
+  const int l = threadIdx.x % G;
+  const int vecs = p.C / 8;
+  const int nb = (p.C + 31) / 32;
+  const float inv_c = 1.0f / static_cast<float>(p.C);
+  uint4 ga[V], be[V];
+  griddep_wait();
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = l + i * G;
+    if (p.gamma && c < vecs) ga[i] = __ldg(reinterpret_cast<const uint4*>(p.gamma) + c);
+    if (p.beta && c < vecs) be[i] = __ldg(reinterpret_cast<const uint4*>(p.beta) + c);
+  }
+  // every warp (block-wide groups: every block) takes kPerWarp * R consecutive rows a step
+  constexpr int kStep = kPerWarp * R;
+  const long long walker = G > 32 ? blockIdx.x
+                                  : blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
+  const long long walkers = static_cast<long long>(gridDim.x) * (G > 32 ? 1 : kThreads / 32);
+  const int sub = G < 32 ? (threadIdx.x % 32) / G : 0;
+  for (long long row0 = walker * kStep; row0 < p.rows; row0 += walkers * kStep) {
+    uint4 raw[R][V];
+    long long row[R];
+    float s[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      row[r] = row0 + r * kPerWarp + sub;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = l + i * G;
+        raw[r][i] = make_uint4(0, 0, 0, 0);
+        if (c < vecs && row[r] < p.rows)
+          raw[r][i] = *reinterpret_cast<const uint4*>(p.x + row[r] * p.C + c * 8);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      s[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float f[8];
+        T::unpack8(raw[r][i], f);
+        s[r] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+      }
+    }
+    group_sum<G, R>(s, red, flip);
+    float mean[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = s[r] * inv_c;
+      s[r] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float f[8];
+        T::unpack8(raw[r][i], f);
+        float a = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float d = f[e] - mean[r];
+          a = fmaf(d, d, a);
+        }
+        if (l + i * G < vecs) s[r] += a;
+      }
+    }
+    group_sum<G, R>(s, red, flip);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float rstd = rsqrtf(fmaf(s[r], inv_c, p.eps));
+      const bool live = row[r] < p.rows;
+      if (l == 0 && live) {
+        if (p.mean) p.mean[row[r]] = mean[r];
+        if (p.rstd) p.rstd[row[r]] = rstd;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = l + i * G;
+        float f[8], gm[8], bt[8];
+        T::unpack8(raw[r][i], f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e] - mean[r], rstd);
+        if constexpr (kCkpt) {
+          uint32_t mag = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mag = max(mag, c < vecs ? a8_mag(f[e]) : 0u);
+          mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+          mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
+          const uint32_t b = a8_exponent(mag);
+          const float inv = a8_inv_step(b);
+          if (c < nb * 4 && live) {
+            uint2 k = make_uint2(0, 0);   // zero codes behind the last channel
+            if (c < vecs)
+              k = make_uint2(a8_code4(f[0], f[1], f[2], f[3], inv), a8_code4(f[4], f[5], f[6], f[7], inv));
+            *reinterpret_cast<uint2*>(p.q + (row[r] * nb * 4 + c) * 8) = k;
+            if ((c & 3) == 0) p.scales[row[r] * nb + (c >> 2)] = static_cast<uint8_t>(b);
+          }
+        }
+        if (c < vecs && live) {
+          if (p.gamma) T::unpack8(ga[i], gm);
+          if (p.beta) T::unpack8(be[i], bt);
+          // (a fused multiply-add by name, so that every variant rounds alike)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], p.gamma ? gm[e] : 1.0f, p.beta ? bt[e] : 0.0f);
+          *reinterpret_cast<uint4*>(p.y + row[r] * p.C + c * 8) = T::pack8(f);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ layer norm, backward
+
+struct LnBwdParams {
+  const uint16_t* dy;
+  const uint16_t* x;        // with mean, or
+  const uint8_t* q;         // the checkpoint of xh
+  const uint8_t* scales;
+  const float* mean;
+  const float* rstd;
+  const uint16_t* gamma;    // [C] or null (1)
+  const uint16_t* dres;     // added to dx, or null
+  uint16_t* dx;
+  float* part;              // [blocks][2][C] partial {dgamma, dbeta}, or null
+  long long rows;
+  int C;
+};
+
+// dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dres, g = dy * gamma, and
+// each thread's share of dgamma = sum dy * xh and dbeta = sum dy for its own
+// channels, kept in fp32 registers over all of its rows; at the end the
+// block's groups are added in a fixed tree and the block writes one partial,
+// which layernorm_param_kernel adds up in block order: no atomics, so the
+// result does not depend on timing.
+template <bool kBF16, int G, int V, int R, bool kCkpt>
+__global__ void __launch_bounds__(kThreads, 1) layernorm_bwd_kernel(const LnBwdParams p) {
+  using T = Val16<kBF16>;
+  constexpr int kPerWarp = G < 32 ? 32 / G : 1;
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ float fold[];                       // [kWarps / 2][2][C] (groups within a warp)
+  __shared__ float red[G > 32 ? 2 * 8 * 2 * R : 1];
+  int flip = 0;
+  const int l = threadIdx.x % G;
+  const int vecs = p.C / 8;
+  const int nb = (p.C + 31) / 32;
+  const float inv_c = 1.0f / static_cast<float>(p.C);
+  float dg[V][8], db[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.0f;
+  griddep_wait();
+  uint4 ga[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = l + i * G;
+    ga[i] = make_uint4(0, 0, 0, 0);
+    if (p.gamma && c < vecs) ga[i] = __ldg(reinterpret_cast<const uint4*>(p.gamma) + c);
+  }
+  constexpr int kStep = kPerWarp * R;
+  const long long walker = G > 32 ? blockIdx.x : blockIdx.x * static_cast<long long>(kWarps) + threadIdx.x / 32;
+  const long long walkers = static_cast<long long>(gridDim.x) * (G > 32 ? 1 : kWarps);
+  const int sub = G < 32 ? (threadIdx.x % 32) / G : 0;
+  for (long long row0 = walker * kStep; row0 < p.rows; row0 += walkers * kStep) {
+    uint4 rdy[R][V], rx[R][V], rres[R][V];
+    uint2 rq[R][V];
+    uint32_t rb[R][V];
+    float mean[R], rstd[R];
+    long long row[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      row[r] = row0 + r * kPerWarp + sub;
+      const bool live = row[r] < p.rows;
+      rstd[r] = live ? __ldg(p.rstd + row[r]) : 0.0f;
+      mean[r] = 0.0f;
+      if constexpr (!kCkpt) mean[r] = live ? __ldg(p.mean + row[r]) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = l + i * G;
+        const bool in = live && c < vecs;
+        rdy[r][i] = make_uint4(0, 0, 0, 0);
+        if (in) rdy[r][i] = *reinterpret_cast<const uint4*>(p.dy + row[r] * p.C + c * 8);
+        if constexpr (kCkpt) {
+          rq[r][i] = make_uint2(0, 0);
+          rb[r][i] = 7u;
+          if (in) {
+            rq[r][i] = __ldg(reinterpret_cast<const uint2*>(p.q + (row[r] * nb * 4 + c) * 8));
+            rb[r][i] = __ldg(p.scales + row[r] * nb + (c >> 2));
+          }
+        } else {
+          rx[r][i] = make_uint4(0, 0, 0, 0);
+          if (in) rx[r][i] = *reinterpret_cast<const uint4*>(p.x + row[r] * p.C + c * 8);
+        }
+        if (p.dres != nullptr) {
+          rres[r][i] = make_uint4(0, 0, 0, 0);
+          if (in) rres[r][i] = *reinterpret_cast<const uint4*>(p.dres + row[r] * p.C + c * 8);
+        }
+      }
+    }
+    // xh of a vector, from x or from its codes (zero behind the last channel or row)
+    auto normalised = [&](int r, int i, float (&xh)[8]) {
+      if constexpr (kCkpt) {
+        const float step = a8_step(rb[r][i]);
+        a8_decode4(rq[r][i].x, step, xh);
+        a8_decode4(rq[r][i].y, step, xh + 4);
+      } else {
+        T::unpack8(rx[r][i], xh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xh[e] = l + i * G < vecs ? (xh[e] - mean[r]) * rstd[r] : 0.0f;
+      }
+    };
+    float c12[2 * R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float a = 0.0f, b = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float dy[8], xh[8], gm[8];
+        T::unpack8(rdy[r][i], dy);
+        normalised(r, i, xh);
+        if (p.gamma) T::unpack8(ga[i], gm);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float g = p.gamma ? dy[e] * gm[e] : dy[e];
+          a += g;
+          b = fmaf(g, xh[e], b);
+          db[i][e] += dy[e];
+          dg[i][e] = fmaf(dy[e], xh[e], dg[i][e]);
+        }
+      }
+      c12[2 * r] = a;
+      c12[2 * r + 1] = b;
+    }
+    group_sum<G, 2 * R>(c12, red, flip);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float c1 = c12[2 * r] * inv_c, c2 = c12[2 * r + 1] * inv_c;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = l + i * G;
+        float dy[8], xh[8], gm[8], add[8];
+        T::unpack8(rdy[r][i], dy);
+        normalised(r, i, xh);
+        if (p.gamma) T::unpack8(ga[i], gm);
+        if (p.dres != nullptr) T::unpack8(rres[r][i], add);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float g = p.gamma ? dy[e] * gm[e] : dy[e];
+          dy[e] = rstd[r] * (g - fmaf(xh[e], c2, c1));
+          if (p.dres != nullptr) dy[e] += add[e];
+        }
+        if (row[r] < p.rows && c < vecs)
+          *reinterpret_cast<uint4*>(p.dx + row[r] * p.C + c * 8) = T::pack8(dy);
+      }
+    }
+  }
+  if (p.part == nullptr) return;
+  float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * p.C;
+  if constexpr (G <= 32) {
+    // lanes that hold the same channels, then the warps by halves
+#pragma unroll
+    for (int o = G; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dg[i][e] += __shfl_xor_sync(0xFFFFFFFFu, dg[i][e], o);
+          db[i][e] += __shfl_xor_sync(0xFFFFFFFFu, db[i][e], o);
+        }
+    const int warp = threadIdx.x / 32;
+    const bool holds = threadIdx.x % 32 < G;
+    for (int half = kWarps / 2; half > 0; half >>= 1) {
+      if (holds && warp >= half && warp < 2 * half)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (l + i * G < vecs)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float* f = fold + (static_cast<size_t>(warp - half) * 2) * p.C + (l + i * G) * 8 + e;
+              f[0] = dg[i][e];
+              f[p.C] = db[i][e];
+            }
+      __syncthreads();
+      if (holds && warp < half)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (l + i * G < vecs)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float* f = fold + (static_cast<size_t>(warp) * 2) * p.C + (l + i * G) * 8 + e;
+              dg[i][e] += f[0];
+              db[i][e] += f[p.C];
+            }
+      __syncthreads();
+    }
+    if (warp != 0 || !holds) return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = l + i * G;
+    if (c < vecs) {
+      float4* o = reinterpret_cast<float4*>(out + c * 8);
+      o[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+      o[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+      o = reinterpret_cast<float4*>(out + p.C + c * 8);
+      o[0] = make_float4(db[i][0], db[i][1], db[i][2], db[i][3]);
+      o[1] = make_float4(db[i][4], db[i][5], db[i][6], db[i][7]);
+    }
+  }
+}
+
+// Adds the blocks' partials of 32 of the 2C sums per block: warp w takes the
+// partials w, w + 32, ... in order, then the 32 warps' sums are added in order.
+template <bool kBF16>
+__global__ void __launch_bounds__(1024) layernorm_param_kernel(const float* __restrict__ part, int blocks,
+                                                               int C, uint16_t* dgamma, uint16_t* dbeta) {
+  __shared__ float s[32][33];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31);
+  const int w = threadIdx.x >> 5;
+  griddep_wait();
+  float a = 0.0f;
+  if (col < 2 * C) {
+#pragma unroll 4
+    for (int b = w; b < blocks; b += 32) a += __ldcg(part + static_cast<size_t>(b) * 2 * C + col);
+  }
+  s[w][threadIdx.x & 31] = a;
+  __syncthreads();
+  if (w == 0 && col < 2 * C) {
+    a = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) a += s[k][threadIdx.x];
+    const uint16_t v = static_cast<uint16_t>(Val16<kBF16>::pack(a, 0.0f) & 0xFFFFu);
+    if (col < C) {
+      if (dgamma) dgamma[col] = v;
+    } else if (dbeta) {
+      dbeta[col - C] = v;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ 8-bit checkpoints
+
+// The streaming kernels walk 16-channel units, two neighbouring threads a
+// 32-channel block: unit u of the flat index is row u / units, channels
+// 16 * (u % units) ..  A thread's first unit is found by division and the next
+// ones by adding the grid stride's quotient and remainder.
+struct UnitWalk {
+  long long row, drow;
+  int v, dv, units;
+  __device__ __forceinline__ UnitWalk(long long u, long long stride, int units_) : units(units_) {
+    row = u / units;
+    v = static_cast<int>(u - row * units);
+    drow = stride / units;
+    dv = static_cast<int>(stride - drow * units);
+  }
+  __device__ __forceinline__ void next() {
+    row += drow;
+    v += dv;
+    if (v >= units) {
+      v -= units;
+      ++row;
+    }
+  }
+};
+
+constexpr int kUnroll = 4;   // units in flight per thread
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kThreads) act8_pack_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ q,
+                                                             uint8_t* __restrict__ scales, long long total,
+                                                             int units, int C) {
+  using T = Val16<kBF16>;
+  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
+  long long u = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
+  UnitWalk w(u, stride, units);
+  griddep_wait();
+  // a warp's units end together (total is even and its lanes are consecutive), so the
+  // exchange below always has both threads of a block
+  for (long long u0 = u - (threadIdx.x & 31); u0 < total; u0 += kUnroll * stride) {
+    uint4 a[kUnroll], b[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k, w.next()) {
+      const long long uk = u0 + (threadIdx.x & 31) + k * stride;
+      const uint16_t* src = x + w.row * C + w.v * 16;
+      a[k] = b[k] = make_uint4(0, 0, 0, 0);
+      if (uk < total && w.v * 16 < C) a[k] = *reinterpret_cast<const uint4*>(src);
+      if (uk < total && w.v * 16 + 8 < C) b[k] = *reinterpret_cast<const uint4*>(src + 8);
+    }
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      const long long uk = u0 + (threadIdx.x & 31) + k * stride;
+      float f[8], g[8];
+      T::unpack8(a[k], f);
+      T::unpack8(b[k], g);
+      uint32_t mag = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mag = max(mag, max(a8_mag(f[e]), a8_mag(g[e])));
+      mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
+      const uint32_t eb = a8_exponent(mag);
+      const float inv = a8_inv_step(eb);
+      if (uk < total) {
+        *reinterpret_cast<uint4*>(q + uk * 16) =
+            make_uint4(a8_code4(f[0], f[1], f[2], f[3], inv), a8_code4(f[4], f[5], f[6], f[7], inv),
+                       a8_code4(g[0], g[1], g[2], g[3], inv), a8_code4(g[4], g[5], g[6], g[7], inv));
+        if ((uk & 1) == 0) scales[uk >> 1] = static_cast<uint8_t>(eb);
+      }
+    }
+  }
+}
+
+struct ReadParams {
+  const uint8_t* q;
+  const uint8_t* scales;
+  const uint16_t* gamma;   // unpack: [C] or null
+  const uint16_t* beta;
+  const uint16_t* dy;      // gradient: out = dy * act'(v); unpack: null
+  uint16_t* out;
+  long long total;
+  int units, C;
+};
+
+// unpack: out = act(v * gamma + beta); gradient (kGrad): out = dy * act'(v).
+template <bool kBF16, int kAct, bool kGrad>
+__global__ void __launch_bounds__(kThreads) act8_read_kernel(const ReadParams p) {
+  using T = Val16<kBF16>;
+  const long long stride = static_cast<long long>(gridDim.x) * kThreads;
+  long long u = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
+  UnitWalk w(u, stride, p.units);
+  griddep_wait();
+  for (; u < p.total; u += kUnroll * stride) {
+    uint4 k[kUnroll], d0[kUnroll], d1[kUnroll];
+    uint32_t eb[kUnroll];
+    long long off[kUnroll];
+    int c0[kUnroll];
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j, w.next()) {
+      const long long uj = u + j * stride;
+      c0[j] = w.v * 16;
+      off[j] = w.row * p.C + c0[j];
+      if (uj < p.total) {
+        k[j] = __ldg(reinterpret_cast<const uint4*>(p.q) + uj);
+        eb[j] = __ldg(p.scales + (uj >> 1));
+        if constexpr (kGrad) {
+          if (c0[j] < p.C) d0[j] = *reinterpret_cast<const uint4*>(p.dy + off[j]);
+          if (c0[j] + 8 < p.C) d1[j] = *reinterpret_cast<const uint4*>(p.dy + off[j] + 8);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kUnroll; ++j) {
+      if (u + j * stride >= p.total) break;
+      const float step = a8_step(eb[j]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0[j] + 8 * h;
+        if (c >= p.C) break;
+        float v[8];
+        a8_decode4(h ? k[j].z : k[j].x, step, v);
+        a8_decode4(h ? k[j].w : k[j].y, step, v + 4);
+        if constexpr (kGrad) {
+          float d[8];
+          T::unpack8(h ? d1[j] : d0[j], d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = d[e] * act_slope_safe<kAct>(v[e]);
+        } else {
+          if (p.gamma || p.beta) {
+            float g[8], b[8];
+            if (p.gamma) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma + c)), g);
+            if (p.beta) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta + c)), b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], p.gamma ? g[e] : 1.0f, p.beta ? b[e] : 0.0f);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = act_value<kAct>(v[e]);
+        }
+        *reinterpret_cast<uint4*>(p.out + off[j] + 8 * h) = T::pack8(v);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int kMaxLnChannels = 8192;
+// Blocks of the backward kernel: two per SM of a 148-SM part; each leaves one
+// partial of 2C floats.
+constexpr int kLnBwdBlocks = 296;
+
+conv3d_status_t check_sizes(long long rows, int C, conv3d_dtype_t dtype, int max_c) {
+  if (rows < 1 || C < 1) {
+    set_error("sizes must be >= 1");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (dtype != CONV3D_F16 && dtype != CONV3D_BF16) {
+    set_error("unknown dtype %d", static_cast<int>(dtype));
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (C % 8 != 0 || C > max_c) {
+    set_error("channels must be a multiple of 8 and at most %d (got %d)", max_c, C);
+    return CONV3D_ERR_UNSUPPORTED;
+  }
+  if (rows > LLONG_MAX / 4 / C) {
+    set_error("problem too large");
+    return CONV3D_ERR_UNSUPPORTED;
+  }
+  return CONV3D_OK;
+}
+
+conv3d_status_t misaligned() {
+  set_error("tensor pointers must be 16-byte aligned, and mean and rstd 4-byte aligned");
+  return CONV3D_ERR_ALIGNMENT;
+}
+
+conv3d_status_t overlapping(const char* what) {
+  set_error("%s", what);
+  return CONV3D_ERR_INVALID_ARG;
+}
+
+unsigned blocks_for(long long work, long long per_block, long long cap) {
+  long long b = (work + per_block - 1) / per_block;
+  if (b > cap) b = cap;
+  return static_cast<unsigned>(b < 1 ? 1 : b);
+}
+
+// Rows per step of a block (block-wide groups) or of its 8 warps.
+constexpr int rows_per_step(int G, int R) { return G > 32 ? R : (kThreads / 32) * (32 / G) * R; }
+
+template <bool kBF16, int G, int V, int R>
+cudaError_t run_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
+  const unsigned blocks = blocks_for(p.rows, rows_per_step(G, R), static_cast<long long>(sms) * (V >= 4 ? 3 : 4));
+  if (p.q) return launch(layernorm_fwd_kernel<kBF16, G, V, R, true>, blocks, kThreads, 0, 1, stream, p);
+  return launch(layernorm_fwd_kernel<kBF16, G, V, R, false>, blocks, kThreads, 0, 1, stream, p);
+}
+
+// The narrowest group and vector count that hold a row, with about four
+// 16-byte loads in flight per thread.
+template <bool kBF16>
+cudaError_t dispatch_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
+  const int vecs = p.C / 8;
+  if (vecs <= 8) return run_fwd<kBF16, 8, 1, 4>(p, sms, stream);
+  if (vecs <= 16) return run_fwd<kBF16, 16, 1, 4>(p, sms, stream);
+  if (vecs <= 32) return run_fwd<kBF16, 32, 1, 4>(p, sms, stream);
+  if (vecs <= 64) return run_fwd<kBF16, 32, 2, 2>(p, sms, stream);
+  if (vecs <= 128) return run_fwd<kBF16, 32, 4, 1>(p, sms, stream);
+  if (vecs <= 256) return run_fwd<kBF16, 256, 1, 2>(p, sms, stream);
+  if (vecs <= 512) return run_fwd<kBF16, 256, 2, 1>(p, sms, stream);
+  return run_fwd<kBF16, 256, 4, 1>(p, sms, stream);
+}
+
+template <bool kBF16, int G, int V, int R>
+cudaError_t run_bwd(const LnBwdParams& p, unsigned blocks, cudaStream_t stream) {
+  const size_t smem = G > 32 ? 0 : static_cast<size_t>(kThreads / 64) * 2 * p.C * sizeof(float);
+  if (p.q) return launch(layernorm_bwd_kernel<kBF16, G, V, R, true>, blocks, kThreads, smem, 1, stream, p);
+  return launch(layernorm_bwd_kernel<kBF16, G, V, R, false>, blocks, kThreads, smem, 1, stream, p);
+}
+
+unsigned bwd_blocks(long long rows, int C) {
+  const int vecs = C / 8;
+  const int per = vecs <= 8    ? rows_per_step(8, 2)
+                  : vecs <= 16 ? rows_per_step(16, 2)
+                  : vecs <= 32 ? rows_per_step(32, 2)
+                  : vecs <= 128 ? rows_per_step(32, 1)
+                                : rows_per_step(256, 1);
+  return blocks_for(rows, per, kLnBwdBlocks);
+}
+
+template <bool kBF16>
+cudaError_t dispatch_bwd(const LnBwdParams& p, unsigned blocks, cudaStream_t stream) {
+  const int vecs = p.C / 8;
+  if (vecs <= 8) return run_bwd<kBF16, 8, 1, 2>(p, blocks, stream);
+  if (vecs <= 16) return run_bwd<kBF16, 16, 1, 2>(p, blocks, stream);
+  if (vecs <= 32) return run_bwd<kBF16, 32, 1, 2>(p, blocks, stream);
+  if (vecs <= 64) return run_bwd<kBF16, 32, 2, 1>(p, blocks, stream);
+  if (vecs <= 128) return run_bwd<kBF16, 32, 4, 1>(p, blocks, stream);
+  if (vecs <= 256) return run_bwd<kBF16, 256, 1, 1>(p, blocks, stream);
+  if (vecs <= 512) return run_bwd<kBF16, 256, 2, 1>(p, blocks, stream);
+  return run_bwd<kBF16, 256, 4, 1>(p, blocks, stream);
+}
+
+template <bool kBF16, bool kGrad>
+cudaError_t dispatch_read(int act, unsigned blocks, cudaStream_t stream, const ReadParams& p) {
+  if (act == kActSilu) return launch(act8_read_kernel<kBF16, kActSilu, kGrad>, blocks, kThreads, 0, 1, stream, p);
+  if (act == kActGelu) return launch(act8_read_kernel<kBF16, kActGelu, kGrad>, blocks, kThreads, 0, 1, stream, p);
+  return launch(act8_read_kernel<kBF16, kActNone, kGrad>, blocks, kThreads, 0, 1, stream, p);
+}
+
+constexpr int kMaxAct8Channels = 1 << 24;
+
+// Units of 16 channels per row and in all.
+void unit_count(long long rows, int C, int& units, long long& total) {
+  units = 2 * ((C + 31) / 32);
+  total = rows * units;
+}
+
+}  // namespace conv3d_channel
+
+using namespace conv3d_channel;
+
+extern "C" {
+
+conv3d_status_t conv3d_layernorm_fwd(const void* x, const void* gamma, const void* beta, void* y,
+                                     float* mean, float* rstd, void* codes, void* exponents,
+                                     long long rows, int C, float eps, conv3d_dtype_t dtype,
+                                     struct CUstream_st* stream) {
+  conv3d_status_t st = check_sizes(rows, C, dtype, kMaxLnChannels);
+  if (st != CONV3D_OK) return st;
+  if (!x || !y || !(eps >= 0.0f) || (codes == nullptr) != (exponents == nullptr)) {
+    set_error("x and y must be non-null, eps >= 0, and codes and exponents given together");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(gamma, 16) || !aligned(beta, 16) ||
+      !aligned(codes, 16) || !aligned(exponents, 16) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return misaligned();
+  const size_t n = static_cast<size_t>(rows) * C * 2, cb = act8_code_bytes(rows, C),
+               sb = act8_scale_bytes(rows, C), rb = static_cast<size_t>(rows) * 4, pb = C * 2ull;
+  if ((y != x && overlaps(y, n, x, n)) || overlaps(y, n, gamma, pb) || overlaps(y, n, beta, pb) ||
+      overlaps(codes, cb, x, n) || overlaps(codes, cb, y, n) || overlaps(exponents, sb, x, n) ||
+      overlaps(exponents, sb, y, n) || overlaps(codes, cb, exponents, sb) || overlaps(mean, rb, y, n) ||
+      overlaps(rstd, rb, y, n) || overlaps(mean, rb, x, n) || overlaps(rstd, rb, x, n) ||
+      overlaps(mean, rb, rstd, rb) || overlaps(mean, rb, codes, cb) || overlaps(rstd, rb, codes, cb) ||
+      overlaps(mean, rb, exponents, sb) || overlaps(rstd, rb, exponents, sb))
+    return overlapping("y must be exactly x or not overlap it; the other outputs must overlap nothing");
+  Device dev;
+  if ((st = current_device(dev)) != CONV3D_OK) return st;
+  LnFwdParams p{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(gamma),
+                static_cast<const uint16_t*>(beta), static_cast<uint16_t*>(y), mean, rstd,
+                static_cast<uint8_t*>(codes), static_cast<uint8_t*>(exponents), rows, C, eps};
+  const cudaError_t e = dtype == CONV3D_BF16 ? dispatch_fwd<true>(p, dev.num_sms, stream)
+                                             : dispatch_fwd<false>(p, dev.num_sms, stream);
+  return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "layer norm launch");
+}
+
+size_t conv3d_layernorm_bwd_workspace_bytes(long long rows, int C) {
+  if (rows < 1 || C < 8 || C > kMaxLnChannels) return 0;
+  const size_t b = static_cast<size_t>(bwd_blocks(rows, C)) * 2 * C * sizeof(float);
+  return (b + 255) & ~static_cast<size_t>(255);
+}
+
+conv3d_status_t conv3d_layernorm_bwd(const void* dy, const void* x, const float* mean,
+                                     const void* codes, const void* exponents, const float* rstd,
+                                     const void* gamma, const void* dres, void* dx, void* dgamma,
+                                     void* dbeta, long long rows, int C, conv3d_dtype_t dtype,
+                                     void* workspace, size_t ws_bytes, struct CUstream_st* stream) {
+  conv3d_status_t st = check_sizes(rows, C, dtype, kMaxLnChannels);
+  if (st != CONV3D_OK) return st;
+  if (!dy || !dx || !rstd) {
+    set_error("dy, dx and rstd must be non-null");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  const bool from_x = x != nullptr && mean != nullptr, from_codes = codes != nullptr && exponents != nullptr;
+  if (from_x == from_codes || (x != nullptr) != (mean != nullptr) ||
+      (codes != nullptr) != (exponents != nullptr)) {
+    set_error("either x and mean or codes and exponents must be given");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(codes, 16) || !aligned(exponents, 16) ||
+      !aligned(gamma, 16) || !aligned(dres, 16) || !aligned(dx, 16) || !aligned(dgamma, 16) ||
+      !aligned(dbeta, 16) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return misaligned();
+  const bool params = dgamma != nullptr || dbeta != nullptr;
+  const size_t need = params ? conv3d_layernorm_bwd_workspace_bytes(rows, C) : 0;
+  if (params && (workspace == nullptr || ws_bytes < need)) {
+    set_error("workspace of %zu bytes required", need);
+    return CONV3D_ERR_WORKSPACE;
+  }
+  if (params && !aligned(workspace, 256)) {
+    set_error("workspace must be 256-byte aligned");
+    return CONV3D_ERR_ALIGNMENT;
+  }
+  const size_t n = static_cast<size_t>(rows) * C * 2, cb = act8_code_bytes(rows, C),
+               sb = act8_scale_bytes(rows, C), rb = static_cast<size_t>(rows) * 4, pb = C * 2ull;
+  const struct { const void* p; size_t n; } outs[] = {{dx, n}, {dgamma, pb}, {dbeta, pb}, {params ? workspace : nullptr, need}},
+                                            ins[] = {{dy, n}, {x, n}, {codes, cb}, {exponents, sb}, {mean, rb},
+                                                     {rstd, rb}, {gamma, pb}, {dres, n}};
+  for (const auto& o : outs) {
+    for (const auto& i : ins)
+      if (overlaps(o.p, o.n, i.p, i.n) && !(o.p == dx && (i.p == dy || i.p == dres || i.p == x) && o.p == i.p))
+        return overlapping("dx must be exactly dy, x or dres or overlap none of them; the other outputs must overlap nothing");
+    for (const auto& q : outs)
+      if (&o != &q && overlaps(o.p, o.n, q.p, q.n))
+        return overlapping("dx, dgamma, dbeta and the workspace must not overlap");
+  }
+  Device dev;
+  if ((st = current_device(dev)) != CONV3D_OK) return st;
+  const unsigned blocks = bwd_blocks(rows, C);
+  LnBwdParams p{static_cast<const uint16_t*>(dy), static_cast<const uint16_t*>(x),
+                static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(exponents), mean, rstd,
+                static_cast<const uint16_t*>(gamma), static_cast<const uint16_t*>(dres),
+                static_cast<uint16_t*>(dx), params ? static_cast<float*>(workspace) : nullptr, rows, C};
+  cudaError_t e = dtype == CONV3D_BF16 ? dispatch_bwd<true>(p, blocks, stream) : dispatch_bwd<false>(p, blocks, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "layer norm gradient launch");
+  if (!params) return CONV3D_OK;
+  const unsigned cols = static_cast<unsigned>((2 * C + 31) / 32);
+  uint16_t* g16 = static_cast<uint16_t*>(dgamma);
+  uint16_t* b16 = static_cast<uint16_t*>(dbeta);
+  e = dtype == CONV3D_BF16 ? launch(layernorm_param_kernel<true>, cols, 1024, 0, 1, stream, p.part, static_cast<int>(blocks), C, g16, b16)
+                           : launch(layernorm_param_kernel<false>, cols, 1024, 0, 1, stream, p.part, static_cast<int>(blocks), C, g16, b16);
+  return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "layer norm parameter gradient launch");
+}
+
+conv3d_status_t conv3d_act8_pack(const void* x, void* codes, void* exponents, long long rows, int C,
+                                 conv3d_dtype_t dtype, struct CUstream_st* stream) {
+  conv3d_status_t st = check_sizes(rows, C, dtype, kMaxAct8Channels);
+  if (st != CONV3D_OK) return st;
+  if (!x || !codes || !exponents) {
+    set_error("x, codes and exponents must be non-null");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(exponents, 16)) return misaligned();
+  const size_t n = static_cast<size_t>(rows) * C * 2, cb = act8_code_bytes(rows, C), sb = act8_scale_bytes(rows, C);
+  if (overlaps(codes, cb, x, n) || overlaps(exponents, sb, x, n) || overlaps(codes, cb, exponents, sb))
+    return overlapping("x, codes and exponents must not overlap");
+  Device dev;
+  if ((st = current_device(dev)) != CONV3D_OK) return st;
+  int units;
+  long long total;
+  unit_count(rows, C, units, total);
+  const unsigned blocks = blocks_for(total, kThreads * kUnroll, dev.num_sms * 6LL);
+  const uint16_t* x16 = static_cast<const uint16_t*>(x);
+  uint8_t* q = static_cast<uint8_t*>(codes);
+  uint8_t* s = static_cast<uint8_t*>(exponents);
+  const cudaError_t e = dtype == CONV3D_BF16
+                            ? launch(act8_pack_kernel<true>, blocks, kThreads, 0, 1, stream, x16, q, s, total, units, C)
+                            : launch(act8_pack_kernel<false>, blocks, kThreads, 0, 1, stream, x16, q, s, total, units, C);
+  return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "checkpoint launch");
+}
+
+static conv3d_status_t act8_read(const void* codes, const void* exponents, const void* gamma, const void* beta,
+                                 const void* dy, bool grad, conv3d_act_t act, void* out, long long rows, int C,
+                                 conv3d_dtype_t dtype, cudaStream_t stream) {
+  conv3d_status_t st = check_sizes(rows, C, dtype, kMaxAct8Channels);
+  if (st != CONV3D_OK) return st;
+  if (!codes || !exponents || !out || (grad && !dy) || act < CONV3D_ACT_NONE || act > CONV3D_ACT_GELU) {
+    set_error("a tensor pointer is null or the activation %d unknown", static_cast<int>(act));
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(codes, 16) || !aligned(exponents, 16) || !aligned(gamma, 16) || !aligned(beta, 16) ||
+      !aligned(dy, 16) || !aligned(out, 16))
+    return misaligned();
+  const size_t n = static_cast<size_t>(rows) * C * 2, cb = act8_code_bytes(rows, C), sb = act8_scale_bytes(rows, C),
+               pb = static_cast<size_t>(C) * 2;
+  if (overlaps(out, n, codes, cb) || overlaps(out, n, exponents, sb) || overlaps(out, n, gamma, pb) ||
+      overlaps(out, n, beta, pb) || (dy != out && overlaps(out, n, dy, n)))
+    return overlapping("the output must not overlap the inputs (the gradient's may be exactly dy)");
+  Device dev;
+  if ((st = current_device(dev)) != CONV3D_OK) return st;
+  ReadParams p{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(exponents),
+               static_cast<const uint16_t*>(gamma), static_cast<const uint16_t*>(beta),
+               static_cast<const uint16_t*>(dy), static_cast<uint16_t*>(out), 0, 0, C};
+  unit_count(rows, C, p.units, p.total);
+  const unsigned blocks = blocks_for(p.total, kThreads * kUnroll, dev.num_sms * 6LL);
+  const bool bf16 = dtype == CONV3D_BF16;
+  const cudaError_t e = grad ? (bf16 ? dispatch_read<true, true>(act, blocks, stream, p)
+                                     : dispatch_read<false, true>(act, blocks, stream, p))
+                             : (bf16 ? dispatch_read<true, false>(act, blocks, stream, p)
+                                     : dispatch_read<false, false>(act, blocks, stream, p));
+  return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "checkpoint read launch");
+}
+
+conv3d_status_t conv3d_act8_unpack(const void* codes, const void* exponents, const void* gamma,
+                                   const void* beta, conv3d_act_t act, void* y, long long rows, int C,
+                                   conv3d_dtype_t dtype, struct CUstream_st* stream) {
+  return act8_read(codes, exponents, gamma, beta, nullptr, false, act, y, rows, C, dtype, stream);
+}
+
+conv3d_status_t conv3d_act8_bwd(const void* dy, const void* codes, const void* exponents,
+                                conv3d_act_t act, void* dx, long long rows, int C,
+                                conv3d_dtype_t dtype, struct CUstream_st* stream) {
+  return act8_read(codes, exponents, nullptr, nullptr, dy, true, act, dx, rows, C, dtype, stream);
+}
+
+}  // extern "C"

@@ -19,6 +19,7 @@
 
 #include "conv3d.h"
 #include "conv3d_kernel.cuh"
+#include "internal.h"
 #include "wgrad_kernel.cuh"
 
 // GroupNorm finalize (groupnorm.cu): {sum, sum of squares} -> {mean, rstd}.
@@ -2524,3 +2525,52 @@ conv3d_status_t conv3d_selftest_wait_timeout(int timeout_ms) {
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ for the other translation units
+
+namespace conv3d_internal {
+
+conv3d_status_t current_device(Device& out) {
+  DeviceState* s = nullptr;
+  int dev = 0;
+  const conv3d_status_t st = device_state(s, dev);
+  if (st == CONV3D_OK) out = Device{s->num_sms, s->max_smem_optin, s->status};
+  return st;
+}
+
+void set_error(const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+  va_end(ap);
+}
+
+conv3d_status_t cuda_fail(cudaError_t e, const char* what) { return ::cuda_fail(e, what); }
+cudaError_t launched() { return conv3d_count_launches(1); }
+bool pdl_enabled() { return ::pdl_enabled(); }
+bool plan_log() { return ::plan_log(); }
+bool take_stall(unsigned long long& timeout_ns) { return ::take_stall(timeout_ns); }
+unsigned long long wait_limit_ns() { return kDefaultTimeoutNs; }
+
+conv3d_status_t encode_matrix(CUtensorMap& map, CUtensorMapDataType type, const void* base,
+                              unsigned long long cols, unsigned long long rows,
+                              unsigned long long pitch_bytes, unsigned box_cols, unsigned box_rows,
+                              CUtensorMapSwizzle swizzle, const char* what) {
+  const conv3d_status_t st = load_entry_points();
+  if (st != CONV3D_OK) return st;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {pitch_bytes};
+  const cuuint32_t box[2] = {box_cols, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = encode_tiled_cached(&map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("cuTensorMapEncodeTiled (%s) failed (%d)", what, static_cast<int>(r));
+    return CONV3D_ERR_CUDA;
+  }
+  return CONV3D_OK;
+}
+
+}  // namespace conv3d_internal

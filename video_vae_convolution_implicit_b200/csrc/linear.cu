@@ -1,0 +1,309 @@
+// linear.cu -- host side of the channel product (linear_kernel.cuh): argument
+// checks, the choice between the two kernels, tensor maps and launches.
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <climits>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+
+#include "conv3d.h"
+#include "internal.h"
+#include "linear_kernel.cuh"
+
+namespace conv3d_linear {
+
+using namespace conv3d;
+using namespace conv3d_internal;
+
+constexpr int kReserve = 1024 + 8 * (2 * MAX_STAGES + 2 + 2 + 1 + 2 * kLinEpiWarps);   // alignment, barriers
+
+// One product: C [M, N] = A [M, K] B^T, B = w [N, K] (forward) or w^T with w [K, N] (gradient).
+struct Product {
+  const void* a;
+  const void* w;
+  const void* bias;
+  const void* residual;
+  void* out;
+  void* codes;
+  void* exponents;
+  int M, K, N;
+  bool bwd;
+  int act;
+  conv3d_dtype_t dtype;
+};
+
+struct Plan {
+  bool pair;
+  int BN, split, stages;
+  size_t smem;
+};
+
+int env_int(const char* name) {
+  const char* v = getenv(name);
+  return v ? atoi(v) : 0;
+}
+
+uint32_t pow2(int v) {
+  uint32_t p = 32;
+  while (p < static_cast<uint32_t>(v)) p <<= 1;
+  return p;
+}
+
+// Pair tiles of 256 rows when they fill most of the SM pairs; otherwise the
+// rows kernel, split along the contraction while that fills idle SMs and
+// leaves every piece a k-block.
+Plan choose(const Product& P, const Device& dev) {
+  Plan L{};
+  const long long mt = (P.M + 255) / 256;
+  const int kblocks = (P.K + BK - 1) / BK;
+  const int pairs = dev.num_sms / 2;
+  const long long tiles256 = mt * ((P.N + 255) / 256), tiles128 = mt * ((P.N + 127) / 128);
+  const int forced = env_int("CONV3D_LINEAR");   // tuning and tests: 1 rows kernel, 128 or 256 pair tiles
+  L.pair = P.M > 128 && tiles128 * 3 >= pairs * 2;
+  L.BN = tiles256 * 3 >= pairs * 2 && P.N > 128 ? 256 : 128;
+  if (forced == 1) L.pair = false;
+  if (forced == 128 || forced == 256) {
+    L.pair = true;
+    L.BN = forced;
+  }
+  if (L.pair) {
+    L.split = 1;
+    const size_t stage = kLinABytes + static_cast<size_t>(L.BN / 2) * BK * 2;
+    const bool q = P.codes != nullptr;
+    const size_t epi = kLinEpiWarps * 2 *
+                       (kLinOutBytes + (P.residual ? kLinOutBytes : 0) + (q ? kLinCodeBytes : 0));
+    const size_t room = dev.max_smem_optin - 64 - kReserve - epi;
+    L.stages = static_cast<int>(room / stage < MAX_STAGES ? room / stage : MAX_STAGES);
+    L.smem = kReserve + epi + L.stages * stage;
+    return L;
+  }
+  L.BN = 16;
+  while (L.BN < 128 && L.BN < P.M) L.BN *= 2;
+  const long long tiles = static_cast<long long>((P.N + 127) / 128) * ((P.M + L.BN - 1) / L.BN);
+  L.split = 1;
+  while (L.split < 8 && tiles * L.split * 2 <= dev.num_sms && L.split * 2 <= kblocks) L.split *= 2;
+  const int forced_split = env_int("CONV3D_LINEAR_SPLIT");   // tuning and tests
+  if (forced_split >= 1 && forced_split <= 8) L.split = forced_split <= kblocks ? forced_split : kblocks;
+  const int per = (kblocks + L.split - 1) / L.split;
+  const size_t stage = kLinABytes + static_cast<size_t>(L.BN) * BK * 2;
+  L.stages = per < 6 ? per : 6;
+  size_t ring = L.stages * stage;
+  const size_t part = static_cast<size_t>(L.BN) * BM * 4;
+  if (ring < part) ring = part;
+  L.smem = kReserve + ring;
+  return L;
+}
+
+// Sets a kernel's dynamic shared memory limit once per device.
+template <typename K>
+conv3d_status_t allow_smem(K kern, std::atomic<unsigned long long>& done, int bytes) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return CONV3D_OK;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  done.fetch_or(bit, std::memory_order_release);
+  return CONV3D_OK;
+}
+
+template <bool kBF16, bool kBwd, int kAct, bool kQ>
+conv3d_status_t run(const Product& P, cudaStream_t stream) {
+  Device dev;
+  conv3d_status_t st = current_device(dev);
+  if (st != CONV3D_OK) return st;
+  const Plan L = choose(P, dev);
+  const CUtensorMapDataType dt = kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const unsigned long long K = P.K, N = P.N, M = P.M;
+  LinearParams p{};
+  p.M = P.M;
+  p.N = P.N;
+  p.kblocks = (P.K + BK - 1) / BK;
+  p.BN = L.BN;
+  p.split = L.split;
+  p.stages = L.stages;
+  p.bias = static_cast<const uint16_t*>(P.bias);
+  p.residual = static_cast<const uint16_t*>(P.residual);
+  p.out = static_cast<uint16_t*>(P.out);
+  p.codes = static_cast<uint8_t*>(P.codes);
+  p.exponents = static_cast<uint8_t*>(P.exponents);
+  p.blocks = (P.N + 31) / 32;
+  p.has_aux = P.residual != nullptr;
+  p.status = dev.status;
+  p.timeout_ns = wait_limit_ns();
+  p.test_stall = take_stall(p.timeout_ns) ? 1 : 0;
+  CUtensorMap map_a, map_w;
+  if (plan_log())
+    fprintf(stderr, "libconv3d: channel product %s %s, %d x %d x %d, tiles of %d, %d pieces, %d stages, %zu B shared\n",
+            kBwd ? "gradient" : "forward", L.pair ? "CTA pair" : "few rows", P.M, P.N, P.K, L.BN, L.split, L.stages,
+            L.smem);
+  if (L.pair) {
+    if ((st = encode_matrix(map_a, dt, P.a, K, M, K * 2, BK, BM, sw, "rows")) != CONV3D_OK) return st;
+    st = kBwd ? encode_matrix(map_w, dt, P.w, N, K, N * 2, 64, BK, sw, "weight")
+              : encode_matrix(map_w, dt, P.w, K, N, K * 2, BK, L.BN / 2, sw, "weight");
+    if (st != CONV3D_OK) return st;
+    CUtensorMap map_out, map_aux, map_codes;
+    if ((st = encode_matrix(map_out, dt, P.out, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, "output")) != CONV3D_OK)
+      return st;
+    map_aux = map_codes = map_out;   // not read unless replaced below
+    if (P.residual && (st = encode_matrix(map_aux, dt, P.residual, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
+                                          "residual")) != CONV3D_OK)
+      return st;
+    const unsigned long long cols = static_cast<unsigned long long>(p.blocks) * 32;
+    if (kQ && (st = encode_matrix(map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, P.codes, cols, M, cols, 32, 32,
+                                  CU_TENSOR_MAP_SWIZZLE_32B, "codes")) != CONV3D_OK)
+      return st;
+    p.tiles_n = (P.N + L.BN - 1) / L.BN;
+    const long long tiles = static_cast<long long>(p.tiles_n) * ((P.M + 2 * BM - 1) / (2 * BM));
+    if (tiles > INT_MAX / 2) {
+      set_error("problem too large for 32-bit tile indexing");
+      return CONV3D_ERR_UNSUPPORTED;
+    }
+    p.num_tiles = static_cast<int>(tiles);
+    p.tmem_cols = pow2(2 * L.BN);
+    p.idesc = idesc_f16(kBF16, 2 * BM, L.BN) | (kBwd ? 1u << 16 : 0u);   // bit 16: B is MN-major
+    static std::atomic<unsigned long long> ready{0};
+    auto kern = linear_pair_kernel<kBF16, kBwd, kAct, kQ>;
+    if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
+    const int pairs = dev.num_sms / 2;
+    const unsigned grid = 2u * static_cast<unsigned>(p.num_tiles < pairs ? p.num_tiles : pairs);
+    const cudaError_t e = launch(kern, grid, kLinThreads, L.smem, 2, stream, map_a, map_w, map_out, map_aux, map_codes, p);
+    return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "channel product launch");
+  }
+  st = kBwd ? encode_matrix(map_w, dt, P.w, N, K, N * 2, 64, BK, sw, "weight")
+            : encode_matrix(map_w, dt, P.w, K, N, K * 2, BK, BM, sw, "weight");
+  if (st != CONV3D_OK) return st;
+  if ((st = encode_matrix(map_a, dt, P.a, K, M, K * 2, BK, L.BN, sw, "rows")) != CONV3D_OK) return st;
+  p.tiles_n = (P.N + BM - 1) / BM;
+  const long long ctas = static_cast<long long>(p.tiles_n) * ((P.M + L.BN - 1) / L.BN) * L.split;
+  if (ctas > INT_MAX / 2) {
+    set_error("problem too large for 32-bit tile indexing");
+    return CONV3D_ERR_UNSUPPORTED;
+  }
+  p.tmem_cols = pow2(L.BN);
+  p.idesc = idesc_f16(kBF16, BM, L.BN) | (kBwd ? 1u << 15 : 0u);   // bit 15: A (here w) is MN-major
+  static std::atomic<unsigned long long> ready{0};
+  auto kern = linear_rows_kernel<kBF16, kBwd, kAct, kQ>;
+  if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
+  const cudaError_t e = launch(kern, static_cast<unsigned>(ctas), kLinRowsThreads, L.smem, static_cast<unsigned>(L.split),
+                               stream, map_w, map_a, p);
+  return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "channel product launch");
+}
+
+template <bool kBF16>
+conv3d_status_t dispatch(const Product& P, cudaStream_t stream) {
+  const bool q = P.codes != nullptr;
+  if (P.bwd) {
+    if (!q) return run<kBF16, true, kActNone, false>(P, stream);
+    return P.act == kActSilu ? run<kBF16, true, kActSilu, true>(P, stream) : run<kBF16, true, kActGelu, true>(P, stream);
+  }
+  switch (P.act) {
+    case kActSilu:
+      return q ? run<kBF16, false, kActSilu, true>(P, stream) : run<kBF16, false, kActSilu, false>(P, stream);
+    case kActGelu:
+      return q ? run<kBF16, false, kActGelu, true>(P, stream) : run<kBF16, false, kActGelu, false>(P, stream);
+    default:
+      return q ? run<kBF16, false, kActNone, true>(P, stream) : run<kBF16, false, kActNone, false>(P, stream);
+  }
+}
+
+conv3d_status_t check(long long rows, int K, int N, conv3d_act_t act, conv3d_dtype_t dtype) {
+  if (rows < 1 || K < 1 || N < 1) {
+    set_error("sizes must be >= 1");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (dtype != CONV3D_F16 && dtype != CONV3D_BF16) {
+    set_error("unknown dtype %d", static_cast<int>(dtype));
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (act < CONV3D_ACT_NONE || act > CONV3D_ACT_GELU) {
+    set_error("unknown activation %d", static_cast<int>(act));
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (K % 8 != 0 || N % 8 != 0) {
+    set_error("K and N must be multiples of 8 (got %d, %d)", K, N);
+    return CONV3D_ERR_UNSUPPORTED;
+  }
+  if (rows > INT_MAX - 512 || K > INT_MAX - 512 || N > INT_MAX - 512) {
+    set_error("problem too large for 32-bit tile indexing");
+    return CONV3D_ERR_UNSUPPORTED;
+  }
+  return CONV3D_OK;
+}
+
+conv3d_status_t misaligned() {
+  set_error("tensor pointers must be 16-byte aligned");
+  return CONV3D_ERR_ALIGNMENT;
+}
+
+}  // namespace conv3d_linear
+
+using namespace conv3d_linear;
+
+extern "C" {
+
+conv3d_status_t conv3d_linear_fwd(const void* x, const void* w, const void* bias, const void* residual,
+                                  void* y, void* codes, void* exponents, long long rows, int K, int N,
+                                  conv3d_act_t act, conv3d_dtype_t dtype, struct CUstream_st* stream) {
+  conv3d_status_t st = check(rows, K, N, act, dtype);
+  if (st != CONV3D_OK) return st;
+  if (!x || !w || !y || (codes == nullptr) != (exponents == nullptr)) {
+    set_error("x, w and y must be non-null, and codes and exponents given together");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 16) || !aligned(residual, 16) || !aligned(y, 16) ||
+      !aligned(codes, 16) || !aligned(exponents, 16))
+    return misaligned();
+  const size_t xb = static_cast<size_t>(rows) * K * 2, wb = static_cast<size_t>(N) * K * 2,
+               yb = static_cast<size_t>(rows) * N * 2, cb = act8_code_bytes(rows, N), sb = act8_scale_bytes(rows, N),
+               bb = static_cast<size_t>(N) * 2;
+  const struct { const void* p; size_t n; } outs[] = {{y, yb}, {codes, cb}, {exponents, sb}},
+                                            ins[] = {{x, xb}, {w, wb}, {bias, bb}, {residual, yb}};
+  for (const auto& o : outs) {
+    for (const auto& i : ins)
+      if (overlaps(o.p, o.n, i.p, i.n) && !(o.p == y && i.p == residual && y == residual)) {
+        set_error("the outputs must not overlap the inputs (y may be exactly the residual)");
+        return CONV3D_ERR_INVALID_ARG;
+      }
+    for (const auto& q : outs)
+      if (&o != &q && overlaps(o.p, o.n, q.p, q.n)) {
+        set_error("y, codes and exponents must not overlap");
+        return CONV3D_ERR_INVALID_ARG;
+      }
+  }
+  const Product P{x, w, bias, residual, y, codes, exponents, static_cast<int>(rows), K, N, false, act, dtype};
+  return dtype == CONV3D_BF16 ? dispatch<true>(P, stream) : dispatch<false>(P, stream);
+}
+
+conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void* codes,
+                                       const void* exponents, conv3d_act_t act, void* dx, long long rows,
+                                       int K, int N, conv3d_dtype_t dtype, struct CUstream_st* stream) {
+  conv3d_status_t st = check(rows, K, N, act, dtype);
+  if (st != CONV3D_OK) return st;
+  if (!dy || !w || !dx || (codes == nullptr) != (exponents == nullptr)) {
+    set_error("dy, w and dx must be non-null, and codes and exponents given together");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (act != CONV3D_ACT_NONE && !codes) {
+    set_error("the derivative of an activation needs the checkpoint of its argument");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(codes, 16) || !aligned(exponents, 16) || !aligned(dx, 16))
+    return misaligned();
+  const size_t n = static_cast<size_t>(rows) * K * 2;
+  if (overlaps(dx, n, dy, static_cast<size_t>(rows) * N * 2) || overlaps(dx, n, w, static_cast<size_t>(N) * K * 2) ||
+      overlaps(dx, n, codes, act8_code_bytes(rows, K)) || overlaps(dx, n, exponents, act8_scale_bytes(rows, K))) {
+    set_error("dx must not overlap the inputs");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  const bool q = act != CONV3D_ACT_NONE;   // without an activation the derivative is 1
+  const Product P{dy, w, nullptr, nullptr, dx, q ? const_cast<void*>(codes) : nullptr,
+                  q ? const_cast<void*>(exponents) : nullptr, static_cast<int>(rows), N, K, true, act, dtype};
+  return dtype == CONV3D_BF16 ? dispatch<true>(P, stream) : dispatch<false>(P, stream);
+}
+
+}  // extern "C"
