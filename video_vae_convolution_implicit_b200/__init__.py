@@ -638,102 +638,110 @@ class Act8(NamedTuple):
                     torch.empty((*lead, blocks), dtype=torch.uint8, device=device), int(shape[-1]))
 
 
-class _On:
-    """Makes the tensors' device current for a call, where it is not already."""
-    __slots__ = ("guard",)
-
-    def __init__(self, t):
-        self.guard = None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+# The current stream of a device as a raw handle.  The direct accessor takes 0.1 us where building a
+# torch.cuda.Stream takes 2.2, as long as the whole of a small kernel.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _tensor(name, t, like, shape, dtype=None):
-    """Checks one operand: a contiguous CUDA tensor on ``like``'s device."""
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
-    if t.dtype != (like.dtype if dtype is None else dtype):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {like.dtype if dtype is None else dtype}")
+def _call(fn, device, stream, *args) -> None:
+    """Runs the library call ``fn(*args, stream)`` with ``device`` current, and checks its status."""
+    s = _raw_stream(device) if stream is None else _stream_handle(stream)
+    if device == torch.cuda.current_device():
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, s)
+    if status:
+        _check(status)
+
+
+def _refuse(name, t, device, dtype, shape):
+    """Says what is wrong with an operand that failed the check of :func:`_tensor`."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _tensor(name, t, device, dtype, shape):
+    """Checks one operand (a contiguous tensor on CUDA device ``device``); returns its address."""
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(name, t, device, dtype, shape)
+    return t.data_ptr()
 
 
 def _main(name, t):
-    """Checks a call's leading operand; returns (rows, channels)."""
-    if not t.is_cuda:
+    """Checks a call's leading operand; returns (rows, channels, device, dtype, dtype code)."""
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() < 1 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [..., C] tensor")
+    dtype = t.dtype
     C = t.shape[-1]
-    return (t.numel() // C if C else 0), C
+    return t.numel() // C if C else 0, C, device, dtype, BF16 if dtype is torch.bfloat16 else _dtype_code(dtype)
 
 
 def _act8(name, a, shape, device):
-    """Checks a checkpoint of a tensor of ``shape``."""
-    if a.channels != shape[-1]:
-        raise ValueError(f"{name} holds {a.channels} channels, expected {shape[-1]}")
-    lead, blocks = tuple(shape[:-1]), -(-shape[-1] // 32)
-    for part, t, dt, n in (("codes", a.codes, torch.int8, blocks * 32), ("exponents", a.exponents, torch.uint8, blocks)):
-        if t.device != device or t.dtype != dt or tuple(t.shape) != (*lead, n) or not t.is_contiguous():
-            raise ValueError(f"{name}.{part} must be a contiguous {dt} tensor {(*lead, n)} on {device}")
+    """Checks a checkpoint of a tensor of ``shape``; returns the two addresses."""
+    codes, exponents, C = a
+    if C != shape[-1]:
+        raise ValueError(f"{name} holds {C} channels, expected {shape[-1]}")
+    lead, blocks = shape[:-1], -(-C // 32)
+    return (_tensor(f"{name}.codes", codes, device, torch.int8, (*lead, blocks * 32)),
+            _tensor(f"{name}.exponents", exponents, device, torch.uint8, (*lead, blocks)))
 
 
-def _stream_on(t, stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
-    return _stream_handle(stream)
+def _new_act8(like, shape):
+    blocks = -(-shape[-1] // 32)
+    lead = shape[:-1]
+    return Act8(like.new_empty((*lead, blocks * 32), dtype=torch.int8),
+                like.new_empty((*lead, blocks), dtype=torch.uint8), shape[-1])
 
 
 def act8_pack(x: torch.Tensor, stream=None) -> Act8:
     """The 8-bit checkpoint of x [..., C]."""
-    rows, C = _main("x", x)
-    a = Act8.empty(x.shape, x.device)
-    with _On(x):
-        _check(_lib.conv3d_act8_pack(x.data_ptr(), a.codes.data_ptr(), a.exponents.data_ptr(), rows, C,
-                                     _dtype_code(x.dtype), _stream_on(x, stream)))
+    rows, C, device, _, code = _main("x", x)
+    a = _new_act8(x, x.shape)
+    _call(_lib.conv3d_act8_pack, device, stream, x.data_ptr(), a.codes.data_ptr(), a.exponents.data_ptr(), rows, C,
+          code)
     return a
 
 
 def act8_unpack(a: Act8, dtype: torch.dtype, gamma=None, beta=None, act: int = ACT_NONE,
                 y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """act(v * gamma + beta) of the checkpoint's values v, as a ``dtype`` tensor."""
-    shape = (*a.codes.shape[:-1], a.channels)
-    _act8("a", a, shape, a.codes.device)
-    if not a.codes.is_cuda:
+    C = a.channels
+    shape = (*a.codes.shape[:-1], C)
+    device = a.codes.get_device()
+    if device < 0:
         raise ValueError("a must hold CUDA tensors")
+    codes, exponents = _act8("a", a, shape, device)
+    code = _dtype_code(dtype)
     if y is None:
-        y = torch.empty(shape, dtype=dtype, device=a.codes.device)
+        y = a.codes.new_empty(shape, dtype=dtype)
     else:
-        _tensor("y", y, a.codes, shape, dtype)
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None:
-            _tensor(name, t, y, (a.channels,))
-    with _On(y):
-        _check(_lib.conv3d_act8_unpack(a.codes.data_ptr(), a.exponents.data_ptr(), _ptr(gamma), _ptr(beta), act,
-                                       y.data_ptr(), y.numel() // a.channels, a.channels, _dtype_code(dtype),
-                                       _stream_on(y, stream)))
+        _tensor("y", y, device, dtype, shape)
+    g = None if gamma is None else _tensor("gamma", gamma, device, dtype, (C,))
+    b = None if beta is None else _tensor("beta", beta, device, dtype, (C,))
+    _call(_lib.conv3d_act8_unpack, device, stream, codes, exponents, g, b, act, y.data_ptr(),
+          y.numel() // C if C else 0, C, code)
     return y
 
 
 def act8_bwd(dy: torch.Tensor, a: Act8, act: int, dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dy * act'(v) of the checkpoint's values v (``dx`` may be ``dy``)."""
-    rows, C = _main("dy", dy)
-    _act8("a", a, dy.shape, dy.device)
+    rows, C, device, dtype, code = _main("dy", dy)
+    codes, exponents = _act8("a", a, dy.shape, device)
     if dx is None:
         dx = torch.empty_like(dy)
-    elif dx is not dy:
-        _tensor("dx", dx, dy, dy.shape)
-    with _On(dy):
-        _check(_lib.conv3d_act8_bwd(dy.data_ptr(), a.codes.data_ptr(), a.exponents.data_ptr(), act, dx.data_ptr(),
-                                    rows, C, _dtype_code(dy.dtype), _stream_on(dy, stream)))
+    else:
+        _tensor("dx", dx, device, dtype, dy.shape)
+    _call(_lib.conv3d_act8_bwd, device, stream, dy.data_ptr(), codes, exponents, act, dx.data_ptr(), rows, C, code)
     return dx
 
 
@@ -745,31 +753,30 @@ def layernorm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-6, with_st
     ``checkpoint8`` (y, xhat, rstd), xhat the :class:`Act8` of (x - mean) * rstd:
     either is what :func:`layernorm_bwd` needs.  ``y`` may be ``x``.
     """
-    rows, C = _main("x", x)
-    if with_stats and checkpoint8:
-        raise ValueError("with_stats and checkpoint8 exclude each other")
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None:
-            _tensor(name, t, x, (C,))
+    rows, C, device, dtype, code = _main("x", x)
+    g = None if gamma is None else _tensor("gamma", gamma, device, dtype, (C,))
+    b = None if beta is None else _tensor("beta", beta, device, dtype, (C,))
     if y is None:
         y = torch.empty_like(x)
-    elif y is not x:
-        _tensor("y", y, x, x.shape)
-    mean = rstd = a = None
-    if with_stats or checkpoint8:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        _tensor("y", y, device, dtype, x.shape)
+    fn = _lib.conv3d_layernorm_fwd
     if with_stats:
+        if checkpoint8:
+            raise ValueError("with_stats and checkpoint8 exclude each other")
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
         mean = torch.empty_like(rstd)
+        _call(fn, device, stream, x.data_ptr(), g, b, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), None, None, rows,
+              C, eps, code)
+        return y, mean, rstd
     if checkpoint8:
-        a = Act8.empty(x.shape, x.device)
-    with _On(x):
-        _check(_lib.conv3d_layernorm_fwd(x.data_ptr(), _ptr(gamma), _ptr(beta), y.data_ptr(), _ptr(mean), _ptr(rstd),
-                                         None if a is None else a.codes.data_ptr(),
-                                         None if a is None else a.exponents.data_ptr(), rows, C, eps,
-                                         _dtype_code(x.dtype), _stream_on(x, stream)))
-    if checkpoint8:
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        a = _new_act8(x, x.shape)
+        _call(fn, device, stream, x.data_ptr(), g, b, y.data_ptr(), None, rstd.data_ptr(), a.codes.data_ptr(),
+              a.exponents.data_ptr(), rows, C, eps, code)
         return y, a, rstd
-    return (y, mean, rstd) if with_stats else y
+    _call(fn, device, stream, x.data_ptr(), g, b, y.data_ptr(), None, None, None, None, rows, C, eps, code)
+    return y
 
 
 def layernorm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, mean: torch.Tensor | None = None, gamma=None,
@@ -779,56 +786,52 @@ def layernorm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, mean: torch.Tenso
 
     saved: x (then ``mean`` is needed) or the :class:`Act8` of the normalised x.
     dres: added to dx (the gradient of a skip connection around the norm).
+    ``dx`` may be ``dy``, ``dres`` or x.
     """
-    rows, C = _main("dy", dy)
-    lead = dy.shape[:-1]
-    _tensor("rstd", rstd, dy, lead, torch.float32)
-    x = codes = exponents = None
+    rows, C, device, dtype, code = _main("dy", dy)
+    shape = dy.shape
+    lead = shape[:-1]
+    r = _tensor("rstd", rstd, device, torch.float32, lead)
+    x = m = codes = exponents = None
     if isinstance(saved, Act8):
         if mean is not None:
             raise ValueError("mean belongs to x: a checkpoint holds the normalised values")
-        _act8("saved", saved, dy.shape, dy.device)
-        codes, exponents = saved.codes, saved.exponents
+        codes, exponents = _act8("saved", saved, shape, device)
     else:
-        x = saved
-        _tensor("saved", x, dy, dy.shape)
+        x = _tensor("saved", saved, device, dtype, shape)
         if mean is None:
             raise ValueError("x needs its mean")
-        _tensor("mean", mean, dy, lead, torch.float32)
-    if gamma is not None:
-        _tensor("gamma", gamma, dy, (C,))
-    if dres is not None:
-        _tensor("dres", dres, dy, dy.shape)
+        m = _tensor("mean", mean, device, torch.float32, lead)
+    g = None if gamma is None else _tensor("gamma", gamma, device, dtype, (C,))
+    s = None if dres is None else _tensor("dres", dres, device, dtype, shape)
     if dx is None:
         dx = torch.empty_like(dy)
-    elif dx is not dy:
-        _tensor("dx", dx, dy, dy.shape)
-    dgamma = dbeta = None
-    ws_bytes = 0
-    if with_params:
-        dgamma = torch.empty((C,), dtype=dy.dtype, device=dy.device)
-        dbeta = torch.empty((C,), dtype=dy.dtype, device=dy.device)
-        if workspace is None:
-            workspace = torch.empty((layernorm_bwd_workspace_bytes(rows, C),), dtype=torch.uint8, device=dy.device)
-        elif not workspace.is_cuda or workspace.device != dy.device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous CUDA tensor on {dy.device}")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    with _On(dy):
-        _check(_lib.conv3d_layernorm_bwd(dy.data_ptr(), _ptr(x), _ptr(mean), _ptr(codes), _ptr(exponents),
-                                         rstd.data_ptr(), _ptr(gamma), _ptr(dres), dx.data_ptr(), _ptr(dgamma),
-                                         _ptr(dbeta), rows, C, _dtype_code(dy.dtype),
-                                         workspace.data_ptr() if with_params else None, ws_bytes,
-                                         _stream_on(dy, stream)))
+    else:
+        _tensor("dx", dx, device, dtype, shape)
+    if not with_params:
+        _call(_lib.conv3d_layernorm_bwd, device, stream, dy.data_ptr(), x, m, codes, exponents, r, g, s, dx.data_ptr(),
+              None, None, rows, C, code, None, 0)
+        return dx, None, None
+    dgamma = dy.new_empty((C,))
+    dbeta = torch.empty_like(dgamma)
+    if workspace is None:
+        workspace = dy.new_empty((layernorm_bwd_workspace_bytes(rows, C),), dtype=torch.uint8)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on device {device}")
+    _call(_lib.conv3d_layernorm_bwd, device, stream, dy.data_ptr(), x, m, codes, exponents, r, g, s, dx.data_ptr(),
+          dgamma.data_ptr(), dbeta.data_ptr(), rows, C, code, workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
     return dx, dgamma, dbeta
 
 
-def _weight(w, like, K, N=None):
-    """Checks a [N, K] weight (or a 1x1x1 convolution's [N, 1, 1, 1, K]); returns N."""
-    if w.dim() not in (2, 5) or w.shape[-1] != K or (N is not None and w.shape[0] != N) or w.numel() != w.shape[0] * K:
+def _weight(w, device, dtype, K, N=None):
+    """Checks a [N, K] weight (or a 1x1x1 convolution's [N, 1, 1, 1, K]); returns (N, address)."""
+    shape = w.shape
+    if len(shape) not in (2, 5) or shape[-1] != K or (N is not None and shape[0] != N) or (
+            len(shape) == 5 and shape[1:4] != (1, 1, 1)):
         raise ValueError(f"w must be [N, {K}] or [N, 1, 1, 1, {K}]" + ("" if N is None else f" with N = {N}") +
-                         f", got {tuple(w.shape)}")
-    _tensor("w", w, like, w.shape)
-    return w.shape[0]
+                         f", got {tuple(shape)}")
+    return shape[0], _tensor("w", w, device, dtype, shape)
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: int = ACT_NONE,
@@ -838,46 +841,44 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: int 
     With ``checkpoint8`` returns (y, pre): pre is the :class:`Act8` of x w^T + bias.
     ``y`` may be ``residual``.
     """
-    rows, K = _main("x", x)
-    N = _weight(w, x, K)
+    rows, K, device, dtype, code = _main("x", x)
+    N, wp = _weight(w, device, dtype, K)
     shape = (*x.shape[:-1], N)
-    if bias is not None:
-        _tensor("bias", bias, x, (N,))
-    if residual is not None:
-        _tensor("residual", residual, x, shape)
+    b = None if bias is None else _tensor("bias", bias, device, dtype, (N,))
+    r = None if residual is None else _tensor("residual", residual, device, dtype, shape)
     if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    elif y is not residual:
-        _tensor("y", y, x, shape)
-    a = Act8.empty(shape, x.device) if checkpoint8 else None
-    with _On(x):
-        _check(_lib.conv3d_linear_fwd(x.data_ptr(), w.data_ptr(), _ptr(bias), _ptr(residual), y.data_ptr(),
-                                      None if a is None else a.codes.data_ptr(),
-                                      None if a is None else a.exponents.data_ptr(), rows, K, N, act,
-                                      _dtype_code(x.dtype), _stream_on(x, stream)))
-    return (y, a) if checkpoint8 else y
+        y = x.new_empty(shape)
+    else:
+        _tensor("y", y, device, dtype, shape)
+    if checkpoint8:
+        a = _new_act8(x, shape)
+        _call(_lib.conv3d_linear_fwd, device, stream, x.data_ptr(), wp, b, r, y.data_ptr(), a.codes.data_ptr(),
+              a.exponents.data_ptr(), rows, K, N, act, code)
+        return y, a
+    _call(_lib.conv3d_linear_fwd, device, stream, x.data_ptr(), wp, b, r, y.data_ptr(), None, None, rows, K, N, act,
+          code)
+    return y
 
 
 def linear_bwd_data(dy: torch.Tensor, w: torch.Tensor, pre: Act8 | None = None, act: int = ACT_NONE,
                     dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dx = (dy w) * act'(pre) for dy [..., N], w [N, K]: the gradient of x, or, with the
     checkpoint ``pre`` of what ``act`` was applied to (x = act(pre)), of that argument."""
-    rows, N = _main("dy", dy)
+    rows, N, device, dtype, code = _main("dy", dy)
     K = w.shape[-1] if w.dim() else 0
-    _weight(w, dy, K, N)
+    _, wp = _weight(w, device, dtype, K, N)
     shape = (*dy.shape[:-1], K)
-    if act != ACT_NONE and pre is None:
-        raise ValueError("the derivative of an activation needs the checkpoint of its argument")
+    codes = exponents = None
     if pre is not None:
-        _act8("pre", pre, shape, dy.device)
+        codes, exponents = _act8("pre", pre, shape, device)
+    elif act != ACT_NONE:
+        raise ValueError("the derivative of an activation needs the checkpoint of its argument")
     if dx is None:
-        dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        dx = dy.new_empty(shape)
     else:
-        _tensor("dx", dx, dy, shape)
-    with _On(dy):
-        _check(_lib.conv3d_linear_bwd_data(dy.data_ptr(), w.data_ptr(), None if pre is None else pre.codes.data_ptr(),
-                                           None if pre is None else pre.exponents.data_ptr(), act, dx.data_ptr(),
-                                           rows, K, N, _dtype_code(dy.dtype), _stream_on(dy, stream)))
+        _tensor("dx", dx, device, dtype, shape)
+    _call(_lib.conv3d_linear_bwd_data, device, stream, dy.data_ptr(), wp, codes, exponents, act, dx.data_ptr(), rows, K,
+          N, code)
     return dx
 
 
@@ -885,15 +886,21 @@ def linear_bwd_weight(x: torch.Tensor, dy: torch.Tensor, with_bias: bool = True,
                       workspace: torch.Tensor | None = None, stream=None):
     """(dw [N, K], dbias [N]) of :func:`linear` without activation: the weight
     gradient of a 1x1x1 convolution over the rows as pixels (conv3d_bwd_weight)."""
-    rows, K = _main("x", x)
+    rows, K, device, dtype, code = _main("x", x)
     N = dy.shape[-1] if dy.dim() else 0
-    _tensor("dy", dy, x, (*x.shape[:-1], N))
+    d = _tensor("dy", dy, device, dtype, (*x.shape[:-1], N))
     if rows < 1 or rows > 0x7FFFFFFF:
         raise ValueError(f"rows must be in [1, 2^31), got {rows}")
-    with _On(x):
-        dw, db = conv3d_bwd_weight(x.view(1, 1, 1, rows, K), dy.view(1, 1, 1, rows, N), (1, 1, 1), (1, 1, 1),
-                                   (0, 0, 0), TPAD_ZERO, with_bias, workspace, _stream_on(x, stream))
-    return dw.view(N, K), db
+    dw = x.new_empty((N, K))
+    db = x.new_empty((N,)) if with_bias else None
+    one = _i3(1, 1, 1)
+    if workspace is None:
+        workspace = x.new_empty((bwd_weight_workspace_bytes(K, N, (1, 1, 1)),), dtype=torch.uint8)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on device {device}")
+    _call(_lib.conv3d_bwd_weight, device, stream, x.data_ptr(), d, dw.data_ptr(), _ptr(db), 1, K, 1, 1, rows, N, one,
+          one, _i3(0, 0, 0), TPAD_ZERO, code, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return dw, db
 
 
 class ChannelMlpSaved(NamedTuple):

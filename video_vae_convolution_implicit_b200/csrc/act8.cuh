@@ -119,6 +119,21 @@ __device__ __forceinline__ float act_slope_safe(float v) {
 // infinities and NaN above every finite one.
 __device__ __forceinline__ uint32_t a8_mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
+// The larger of a magnitude m and |v|, NaN if either is.
+__device__ __forceinline__ float a8_max(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
+
+// The largest magnitude of 8 values, as bits.
+__device__ __forceinline__ uint32_t a8_mag8(const float (&f)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = a8_max(m, f[e]);
+  return __float_as_uint(m);
+}
+
 // Exponent byte of a block whose largest magnitude has the bits `mag`.
 __device__ __forceinline__ uint32_t a8_exponent(uint32_t mag) {
   const uint32_t b = mag >> 23;

@@ -8,6 +8,7 @@
 // and several 16-byte loads in flight per thread.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -26,14 +27,21 @@ constexpr int kThreads = 256;
 // ------------------------------------------------------------------ row groups
 
 // A row belongs to a group of G threads: G = 8, 16 or 32 neighbouring lanes of
-// a warp, or the whole block of 256.  Thread `l` of the group holds the
-// 8-channel vectors l, l + G, ..., V of them.
+// a warp, or the whole block.  Thread `l` of the group holds the 8-channel
+// vectors l, l + G, ..., V of them.  A walker (a warp, or a block-wide group's
+// block) takes kPerWarp * R consecutive rows a step.
+//
+// Rows stream through a shared-memory ring by cp.async, D steps deep, each
+// thread filling and reading its own slots only, so no barrier is needed: the
+// bytes in flight are bounded by shared memory and not by registers (measured
+// on B200 with the loads in registers: the backward pass of 104448 x 512 from
+// 8 bits at 2.5 TB/s).
 
 // Sums of N values over the threads of a group, in every thread.  Block-wide
-// groups pass through `red` ([2][8][N] floats), whose halves alternate (`flip`)
-// so that one barrier per sum is enough: a thread writes a half again only
-// after the barrier of the sum in between, which every reader of the half has
-// passed.
+// groups pass through `red` ([2][T/32][N] floats), whose halves alternate
+// (`flip`) so that one barrier per sum is enough: a thread writes a half again
+// only after the barrier of the sum in between, which every reader of the half
+// has passed.
 template <int G, int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) {
 #pragma unroll
@@ -41,7 +49,8 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) 
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], o);
   if constexpr (G > 32) {
-    float* r = red + flip * (8 * N);
+    constexpr int kWarps = G / 32;
+    float* r = red + flip * (kWarps * N);
     flip ^= 1;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -51,11 +60,65 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float* red, int& flip) 
     for (int n = 0; n < N; ++n) {
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) s += r[w * N + n];
+      for (int w = 0; w < kWarps; ++w) s += r[w * N + n];
       v[n] = s;
     }
   }
 }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first `bytes` of a 4-byte word; the rest of it is filled with zeros.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes = 4) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// A cached 16-byte load that stays where it is written: rows of two and more
+// vectors a thread read gamma and beta again at each use (from L1) rather than
+// hold them unpacked in registers.
+__device__ __forceinline__ uint4 ld_again(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// The rows of one walker.
+template <int G, int R, int T>
+struct Walk {
+  static constexpr int kPerWarp = G < 32 ? 32 / G : 1;
+  static constexpr int kStep = kPerWarp * R;
+  long long first, stride;   // first row of step 0 (this thread's, r = 0) and rows between steps
+  long long steps;
+  __device__ __forceinline__ explicit Walk(long long rows) {
+    const long long walker = G > 32 ? blockIdx.x : blockIdx.x * static_cast<long long>(T / 32) + threadIdx.x / 32;
+    const long long walkers = static_cast<long long>(gridDim.x) * (G > 32 ? 1 : T / 32);
+    const int sub = G < 32 ? (threadIdx.x % 32) / G : 0;
+    first = walker * kStep + sub;
+    stride = walkers * kStep;
+    const long long left = rows - walker * kStep;
+    steps = left > 0 ? (left + stride - 1) / stride : 0;
+  }
+  __device__ __forceinline__ long long row(long long step, int r) const { return first + step * stride + r * kPerWarp; }
+};
 
 // ------------------------------------------------------------------ layer norm, forward
 
@@ -73,60 +136,61 @@ struct LnFwdParams {
   float eps;
 };
 
-// y = xh * gamma + beta, xh = (x - mean) / sqrt(var + eps).  A group loads R
-// rows at a time (R * V 16-byte loads in flight per thread), so the
-// reductions of the rows overlap; mean first, then the squared deviations from
-// it, both from registers: no cancellation however far the row is off centre.
-// The checkpoint's 32-channel blocks are four neighbouring threads' vectors.
-template <bool kBF16, int G, int V, int R, bool kCkpt>
-__global__ void __launch_bounds__(kThreads, 2) layernorm_fwd_kernel(const LnFwdParams p) {
-  using T = Val16<kBF16>;
-  __shared__ float red[G > 32 ? 2 * 8 * R : 1];
+// y = xh * gamma + beta, xh = (x - mean) / sqrt(var + eps): the mean first, then
+// the squared deviations from it, both from registers: no cancellation however
+// far the row is off centre.  The checkpoint's 32-channel blocks are four
+// neighbouring threads' vectors.  T threads a block, `kOcc` blocks an SM.
+template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
+__global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParams p) {
+  using H = Val16<kBF16>;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ float red[G > 32 ? 2 * (T / 32) * R : 1];
   int flip = 0;
-  constexpr int kPerWarp = G < 32 ? 32 / G : 1;         // groups per warp
   const int l = threadIdx.x % G;
   const int vecs = p.C / 8;
   const int nb = (p.C + 31) / 32;
   const float inv_c = 1.0f / static_cast<float>(p.C);
-  uint4 ga[V], be[V];
+  const Walk<G, R, T> walk(p.rows);
+  const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16u;
+  constexpr uint32_t kSlot = R * V * T * 16;
   griddep_wait();
+  auto fetch = [&](long long k, int slot) {
+    if (k < walk.steps)
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int c = l + i * G;
-    if (p.gamma && c < vecs) ga[i] = __ldg(reinterpret_cast<const uint4*>(p.gamma) + c);
-    if (p.beta && c < vecs) be[i] = __ldg(reinterpret_cast<const uint4*>(p.beta) + c);
-  }
-  // every warp (block-wide groups: every block) takes kPerWarp * R consecutive rows a step
-  constexpr int kStep = kPerWarp * R;
-  const long long walker = G > 32 ? blockIdx.x
-                                  : blockIdx.x * static_cast<long long>(kThreads / 32) + threadIdx.x / 32;
-  const long long walkers = static_cast<long long>(gridDim.x) * (G > 32 ? 1 : kThreads / 32);
-  const int sub = G < 32 ? (threadIdx.x % 32) / G : 0;
-  for (long long row0 = walker * kStep; row0 < p.rows; row0 += walkers * kStep) {
-    uint4 raw[R][V];
-    long long row[R];
-    float s[R];
+      for (int r = 0; r < R; ++r) {
+        const long long row = walk.row(k, r);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      row[r] = row0 + r * kPerWarp + sub;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = l + i * G;
-        raw[r][i] = make_uint4(0, 0, 0, 0);
-        if (c < vecs && row[r] < p.rows)
-          raw[r][i] = *reinterpret_cast<const uint4*>(p.x + row[r] * p.C + c * 8);
+        for (int i = 0; i < V; ++i)
+          if (l + i * G < vecs && row < p.rows)
+            cp_async16(ring + slot * kSlot + (r * V + i) * (T * 16), p.x + row * p.C + (l + i * G) * 8);
       }
-    }
+    cp_async_commit();   // one group per step, empty ones included, so the count stays fixed
+  };
+#pragma unroll
+  for (int k = 0; k < D - 1; ++k) fetch(k, k);
+  uint4 ga, be;   // V == 1
+  if (V == 1 && p.gamma && l < vecs) ga = __ldg(reinterpret_cast<const uint4*>(p.gamma) + l);
+  if (V == 1 && p.beta && l < vecs) be = __ldg(reinterpret_cast<const uint4*>(p.beta) + l);
+  int slot = 0;
+  for (long long k = 0; k < walk.steps; ++k) {
+    // the slot of the step before this one was read into registers then: refill it
+    fetch(k + D - 1, slot == 0 ? D - 1 : slot - 1);
+    cp_async_wait<D - 1>();
+    float d[R][V][8], s[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const bool live = walk.row(k, r) < p.rows;
       s[r] = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float f[8];
-        T::unpack8(raw[r][i], f);
-        s[r] += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (l + i * G < vecs && live) raw = ld_shared_v4(ring + slot * kSlot + (r * V + i) * (T * 16));
+        H::unpack8(raw, d[r][i]);
+        s[r] += ((d[r][i][0] + d[r][i][1]) + (d[r][i][2] + d[r][i][3])) +
+                ((d[r][i][4] + d[r][i][5]) + (d[r][i][6] + d[r][i][7]));
       }
     }
+    slot = slot == D - 1 ? 0 : slot + 1;
     group_sum<G, R>(s, red, flip);
     float mean[R];
 #pragma unroll
@@ -135,13 +199,11 @@ __global__ void __launch_bounds__(kThreads, 2) layernorm_fwd_kernel(const LnFwdP
       s[r] = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float f[8];
-        T::unpack8(raw[r][i], f);
         float a = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float d = f[e] - mean[r];
-          a = fmaf(d, d, a);
+          d[r][i][e] -= mean[r];
+          a = fmaf(d[r][i][e], d[r][i][e], a);
         }
         if (l + i * G < vecs) s[r] += a;
       }
@@ -149,46 +211,47 @@ __global__ void __launch_bounds__(kThreads, 2) layernorm_fwd_kernel(const LnFwdP
     group_sum<G, R>(s, red, flip);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const long long row = walk.row(k, r);
+      const bool live = row < p.rows;
       const float rstd = rsqrtf(fmaf(s[r], inv_c, p.eps));
-      const bool live = row[r] < p.rows;
       if (l == 0 && live) {
-        if (p.mean) p.mean[row[r]] = mean[r];
-        if (p.rstd) p.rstd[row[r]] = rstd;
+        if (p.mean) p.mean[row] = mean[r];
+        if (p.rstd) p.rstd[row] = rstd;
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = l + i * G;
-        float f[8], gm[8], bt[8];
-        T::unpack8(raw[r][i], f);
+        float(&f)[8] = d[r][i];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e] - mean[r], rstd);
+        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], rstd);
         if constexpr (kCkpt) {
-          uint32_t mag = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mag = max(mag, c < vecs ? a8_mag(f[e]) : 0u);
+          uint32_t mag = a8_mag8(f);
+          if (c >= vecs) mag = 0u;
           mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
           mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
           const uint32_t b = a8_exponent(mag);
           const float inv = a8_inv_step(b);
           if (c < nb * 4 && live) {
-            uint2 k = make_uint2(0, 0);   // zero codes behind the last channel
+            uint2 q = make_uint2(0, 0);   // zero codes behind the last channel
             if (c < vecs)
-              k = make_uint2(a8_code4(f[0], f[1], f[2], f[3], inv), a8_code4(f[4], f[5], f[6], f[7], inv));
-            *reinterpret_cast<uint2*>(p.q + (row[r] * nb * 4 + c) * 8) = k;
-            if ((c & 3) == 0) p.scales[row[r] * nb + (c >> 2)] = static_cast<uint8_t>(b);
+              q = make_uint2(a8_code4(f[0], f[1], f[2], f[3], inv), a8_code4(f[4], f[5], f[6], f[7], inv));
+            *reinterpret_cast<uint2*>(p.q + (row * nb * 4 + c) * 8) = q;
+            if ((c & 3) == 0) p.scales[row * nb + (c >> 2)] = static_cast<uint8_t>(b);
           }
         }
         if (c < vecs && live) {
-          if (p.gamma) T::unpack8(ga[i], gm);
-          if (p.beta) T::unpack8(be[i], bt);
+          float gm[8], bt[8];
+          if (p.gamma) H::unpack8(V == 1 ? ga : ld_again(p.gamma + c * 8), gm);
+          if (p.beta) H::unpack8(V == 1 ? be : ld_again(p.beta + c * 8), bt);
           // (a fused multiply-add by name, so that every variant rounds alike)
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], p.gamma ? gm[e] : 1.0f, p.beta ? bt[e] : 0.0f);
-          *reinterpret_cast<uint4*>(p.y + row[r] * p.C + c * 8) = T::pack8(f);
+          *reinterpret_cast<uint4*>(p.y + row * p.C + c * 8) = H::pack8(f);
         }
       }
     }
   }
+  cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------------ layer norm, backward
@@ -208,30 +271,79 @@ struct LnBwdParams {
   int C;
 };
 
+// Shared bytes per thread of one ring step: dy, then x or the codes, then dres
+// (when there is one), then rstd, then the mean or the words that hold the
+// vectors' exponent bytes.
+__host__ __device__ constexpr int ln_bwd_src_bytes(bool ckpt) { return ckpt ? 8 : 16; }
+__host__ __device__ constexpr int ln_bwd_step_bytes(int V, int R, bool ckpt, bool dres) {
+  return R * (V * (16 + ln_bwd_src_bytes(ckpt) + (dres ? 16 : 0)) + 4 + (ckpt ? 4 * V : 4));
+}
+
 // dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dres, g = dy * gamma, and
 // each thread's share of dgamma = sum dy * xh and dbeta = sum dy for its own
 // channels, kept in fp32 registers over all of its rows; at the end the
 // block's groups are added in a fixed tree and the block writes one partial,
 // which layernorm_param_kernel adds up in block order: no atomics, so the
 // result does not depend on timing.
-template <bool kBF16, int G, int V, int R, bool kCkpt>
-__global__ void __launch_bounds__(kThreads, 1) layernorm_bwd_kernel(const LnBwdParams p) {
-  using T = Val16<kBF16>;
-  constexpr int kPerWarp = G < 32 ? 32 / G : 1;
-  constexpr int kWarps = kThreads / 32;
-  extern __shared__ float fold[];                       // [kWarps / 2][2][C] (groups within a warp)
-  __shared__ float red[G > 32 ? 2 * 8 * 2 * R : 1];
+template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
+__global__ void __launch_bounds__(T, kOcc) layernorm_bwd_kernel(const LnBwdParams p) {
+  using H = Val16<kBF16>;
+  constexpr int kWarps = T / 32;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
+  __shared__ float red[G > 32 ? 2 * (T / 32) * 2 * R : 1];
   int flip = 0;
   const int l = threadIdx.x % G;
   const int vecs = p.C / 8;
   const int nb = (p.C + 31) / 32;
   const float inv_c = 1.0f / static_cast<float>(p.C);
+  const bool has_res = p.dres != nullptr;
+  const Walk<G, R, T> walk(p.rows);
+  // the parts of a ring step
+  constexpr uint32_t kSrc = ln_bwd_src_bytes(kCkpt);
+  const uint32_t base = smem_addr(ring_mem);
+  const uint32_t step_bytes = has_res ? ln_bwd_step_bytes(V, R, kCkpt, true) * T : ln_bwd_step_bytes(V, R, kCkpt, false) * T;
+  constexpr uint32_t kDyEnd = R * V * T * 16;
+  constexpr uint32_t kSrcEnd = kDyEnd + R * V * T * kSrc;
+  const uint32_t res_end = kSrcEnd + (has_res ? kDyEnd : 0u);
   float dg[V][8], db[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.0f;
   griddep_wait();
+  const long long scale_bytes = p.rows * nb;
+  auto fetch = [&](long long k, int slot) {
+    if (k < walk.steps) {
+      const uint32_t s = base + slot * step_bytes;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const long long row = walk.row(k, r);
+        if (row >= p.rows) continue;
+        cp_async4(s + res_end + (r * T + threadIdx.x) * 4u, p.rstd + row);
+        if constexpr (!kCkpt) cp_async4(s + res_end + ((R + r) * T + threadIdx.x) * 4u, p.mean + row);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int c = l + i * G;
+          if (c >= vecs) continue;
+          const uint32_t at = (r * V + i) * T + threadIdx.x;
+          cp_async16(s + at * 16u, p.dy + row * p.C + c * 8);
+          if constexpr (kCkpt) {
+            cp_async8(s + kDyEnd + at * 8u, p.q + (row * nb * 4 + c) * 8);
+            // the aligned word that holds the exponent byte, short of the buffer's end
+            const long long off = (row * nb + (c >> 2)) & ~3LL;
+            cp_async4(s + res_end + (R * T + at) * 4u, p.scales + off,
+                      scale_bytes - off < 4 ? static_cast<uint32_t>(scale_bytes - off) : 4u);
+          } else {
+            cp_async16(s + kDyEnd + at * 16u, p.x + row * p.C + c * 8);
+          }
+          if (has_res) cp_async16(s + kSrcEnd + at * 16u, p.dres + row * p.C + c * 8);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < D - 1; ++k) fetch(k, k);
   uint4 ga[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -239,75 +351,50 @@ __global__ void __launch_bounds__(kThreads, 1) layernorm_bwd_kernel(const LnBwdP
     ga[i] = make_uint4(0, 0, 0, 0);
     if (p.gamma && c < vecs) ga[i] = __ldg(reinterpret_cast<const uint4*>(p.gamma) + c);
   }
-  constexpr int kStep = kPerWarp * R;
-  const long long walker = G > 32 ? blockIdx.x : blockIdx.x * static_cast<long long>(kWarps) + threadIdx.x / 32;
-  const long long walkers = static_cast<long long>(gridDim.x) * (G > 32 ? 1 : kWarps);
-  const int sub = G < 32 ? (threadIdx.x % 32) / G : 0;
-  for (long long row0 = walker * kStep; row0 < p.rows; row0 += walkers * kStep) {
-    uint4 rdy[R][V], rx[R][V], rres[R][V];
-    uint2 rq[R][V];
-    uint32_t rb[R][V];
-    float mean[R], rstd[R];
-    long long row[R];
+  int slot = 0;
+  for (long long k = 0; k < walk.steps; ++k) {
+    fetch(k + D - 1, slot == 0 ? D - 1 : slot - 1);
+    cp_async_wait<D - 1>();
+    const uint32_t s = base + slot * step_bytes;
+    float g[R][V][8], xh[R][V][8], rstd[R], c12[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      row[r] = row0 + r * kPerWarp + sub;
-      const bool live = row[r] < p.rows;
-      rstd[r] = live ? __ldg(p.rstd + row[r]) : 0.0f;
-      mean[r] = 0.0f;
-      if constexpr (!kCkpt) mean[r] = live ? __ldg(p.mean + row[r]) : 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = l + i * G;
-        const bool in = live && c < vecs;
-        rdy[r][i] = make_uint4(0, 0, 0, 0);
-        if (in) rdy[r][i] = *reinterpret_cast<const uint4*>(p.dy + row[r] * p.C + c * 8);
-        if constexpr (kCkpt) {
-          rq[r][i] = make_uint2(0, 0);
-          rb[r][i] = 7u;
-          if (in) {
-            rq[r][i] = __ldg(reinterpret_cast<const uint2*>(p.q + (row[r] * nb * 4 + c) * 8));
-            rb[r][i] = __ldg(p.scales + row[r] * nb + (c >> 2));
-          }
-        } else {
-          rx[r][i] = make_uint4(0, 0, 0, 0);
-          if (in) rx[r][i] = *reinterpret_cast<const uint4*>(p.x + row[r] * p.C + c * 8);
-        }
-        if (p.dres != nullptr) {
-          rres[r][i] = make_uint4(0, 0, 0, 0);
-          if (in) rres[r][i] = *reinterpret_cast<const uint4*>(p.dres + row[r] * p.C + c * 8);
-        }
-      }
-    }
-    // xh of a vector, from x or from its codes (zero behind the last channel or row)
-    auto normalised = [&](int r, int i, float (&xh)[8]) {
-      if constexpr (kCkpt) {
-        const float step = a8_step(rb[r][i]);
-        a8_decode4(rq[r][i].x, step, xh);
-        a8_decode4(rq[r][i].y, step, xh + 4);
-      } else {
-        T::unpack8(rx[r][i], xh);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xh[e] = l + i * G < vecs ? (xh[e] - mean[r]) * rstd[r] : 0.0f;
-      }
-    };
-    float c12[2 * R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
+      const long long row = walk.row(k, r);
+      const bool live = row < p.rows;
+      rstd[r] = live ? __uint_as_float(ld_shared_u32(s + res_end + (r * T + threadIdx.x) * 4u)) : 0.0f;
+      float mean = 0.0f;
+      if constexpr (!kCkpt)
+        mean = live ? __uint_as_float(ld_shared_u32(s + res_end + ((R + r) * T + threadIdx.x) * 4u)) : 0.0f;
       float a = 0.0f, b = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float dy[8], xh[8], gm[8];
-        T::unpack8(rdy[r][i], dy);
-        normalised(r, i, xh);
-        if (p.gamma) T::unpack8(ga[i], gm);
+        const int c = l + i * G;
+        const uint32_t at = (r * V + i) * T + threadIdx.x;
+        if (live && c < vecs) {
+          H::unpack8(ld_shared_v4(s + at * 16u), g[r][i]);
+          if constexpr (kCkpt) {
+            const uint32_t word = ld_shared_u32(s + res_end + (R * T + at) * 4u);
+            const uint32_t byte = static_cast<uint32_t>(row * nb + (c >> 2)) & 3u;
+            const float step = a8_step((word >> (8u * byte)) & 0xFFu);
+            const uint2 q = ld_shared_v2(s + kDyEnd + at * 8u);
+            a8_decode4(q.x, step, xh[r][i]);
+            a8_decode4(q.y, step, xh[r][i] + 4);
+          } else {
+            H::unpack8(ld_shared_v4(s + kDyEnd + at * 16u), xh[r][i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float g = p.gamma ? dy[e] * gm[e] : dy[e];
-          a += g;
-          b = fmaf(g, xh[e], b);
-          db[i][e] += dy[e];
-          dg[i][e] = fmaf(dy[e], xh[e], dg[i][e]);
+            for (int e = 0; e < 8; ++e) xh[r][i][e] = (xh[r][i][e] - mean) * rstd[r];
+          }
+          float gm[8];
+          if (p.gamma) H::unpack8(ga[i], gm);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float dy = g[r][i][e];
+            db[i][e] += dy;
+            dg[i][e] = fmaf(dy, xh[r][i][e], dg[i][e]);
+            g[r][i][e] = p.gamma ? dy * gm[e] : dy;
+            a += g[r][i][e];
+            b = fmaf(g[r][i][e], xh[r][i][e], b);
+          }
         }
       }
       c12[2 * r] = a;
@@ -316,30 +403,30 @@ __global__ void __launch_bounds__(kThreads, 1) layernorm_bwd_kernel(const LnBwdP
     group_sum<G, 2 * R>(c12, red, flip);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+      const long long row = walk.row(k, r);
       const float c1 = c12[2 * r] * inv_c, c2 = c12[2 * r + 1] * inv_c;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = l + i * G;
-        float dy[8], xh[8], gm[8], add[8];
-        T::unpack8(rdy[r][i], dy);
-        normalised(r, i, xh);
-        if (p.gamma) T::unpack8(ga[i], gm);
-        if (p.dres != nullptr) T::unpack8(rres[r][i], add);
+        if (row >= p.rows || c >= vecs) continue;
+        float o[8], add[8];
+        if (has_res) H::unpack8(ld_shared_v4(s + kSrcEnd + ((r * V + i) * T + threadIdx.x) * 16u), add);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float g = p.gamma ? dy[e] * gm[e] : dy[e];
-          dy[e] = rstd[r] * (g - fmaf(xh[e], c2, c1));
-          if (p.dres != nullptr) dy[e] += add[e];
-        }
-        if (row[r] < p.rows && c < vecs)
-          *reinterpret_cast<uint4*>(p.dx + row[r] * p.C + c * 8) = T::pack8(dy);
+        for (int e = 0; e < 8; ++e)
+          o[e] = fmaf(rstd[r], g[r][i][e] - fmaf(xh[r][i][e], c2, c1), has_res ? add[e] : 0.0f);
+        *reinterpret_cast<uint4*>(p.dx + row * p.C + c * 8) = H::pack8(o);
       }
     }
+    slot = slot == D - 1 ? 0 : slot + 1;
   }
+  cp_async_wait<0>();
   if (p.part == nullptr) return;
   float* out = p.part + static_cast<size_t>(blockIdx.x) * 2 * p.C;
   if constexpr (G <= 32) {
-    // lanes that hold the same channels, then the warps by halves
+    // lanes that hold the same channels, then the warps by halves through the
+    // ring's memory ([kWarps / 2][2][C] floats), which nobody fills any more
+    float* fold = reinterpret_cast<float*>(ring_mem);
+    __syncthreads();
 #pragma unroll
     for (int o = G; o < 32; o <<= 1)
 #pragma unroll
@@ -355,24 +442,26 @@ __global__ void __launch_bounds__(kThreads, 1) layernorm_bwd_kernel(const LnBwdP
       if (holds && warp >= half && warp < 2 * half)
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (l + i * G < vecs)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float* f = fold + (static_cast<size_t>(warp - half) * 2) * p.C + (l + i * G) * 8 + e;
-              f[0] = dg[i][e];
-              f[p.C] = db[i][e];
-            }
+          if (l + i * G < vecs) {
+            float4* f = reinterpret_cast<float4*>(fold + (static_cast<size_t>(warp - half) * 2) * p.C + (l + i * G) * 8);
+            f[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
+            f[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+            f += p.C / 4;
+            f[0] = make_float4(db[i][0], db[i][1], db[i][2], db[i][3]);
+            f[1] = make_float4(db[i][4], db[i][5], db[i][6], db[i][7]);
+          }
       __syncthreads();
       if (holds && warp < half)
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (l + i * G < vecs)
+          if (l + i * G < vecs) {
+            const float* f = fold + (static_cast<size_t>(warp) * 2) * p.C + (l + i * G) * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float* f = fold + (static_cast<size_t>(warp) * 2) * p.C + (l + i * G) * 8 + e;
-              dg[i][e] += f[0];
-              db[i][e] += f[p.C];
+              dg[i][e] += f[e];
+              db[i][e] += f[p.C + e];
             }
+          }
       __syncthreads();
     }
     if (warp != 0 || !holds) return;
@@ -422,9 +511,9 @@ __global__ void __launch_bounds__(1024) layernorm_param_kernel(const float* __re
 
 // ------------------------------------------------------------------ 8-bit checkpoints
 
-// The streaming kernels walk 16-channel units, two neighbouring threads a
-// 32-channel block: unit u of the flat index is row u / units, channels
-// 16 * (u % units) ..  A thread's first unit is found by division and the next
+// The streaming kernels walk units of 16 channels (two neighbouring threads a
+// 32-channel block) or 8: unit u of the flat index is row u / units, and unit
+// u % units of the row's padded channels.  A thread's first unit is found by division and the next
 // ones by adding the grid stride's quotient and remainder.
 struct UnitWalk {
   long long row, drow;
@@ -502,6 +591,8 @@ struct ReadParams {
 };
 
 // unpack: out = act(v * gamma + beta); gradient (kGrad): out = dy * act'(v).
+// Units of 8 channels here: the 16-bit side, two thirds and more of the bytes,
+// is then one contiguous 512-byte access a warp.
 template <bool kBF16, int kAct, bool kGrad>
 __global__ void __launch_bounds__(kThreads) act8_read_kernel(const ReadParams p) {
   using T = Val16<kBF16>;
@@ -510,53 +601,46 @@ __global__ void __launch_bounds__(kThreads) act8_read_kernel(const ReadParams p)
   UnitWalk w(u, stride, p.units);
   griddep_wait();
   for (; u < p.total; u += kUnroll * stride) {
-    uint4 k[kUnroll], d0[kUnroll], d1[kUnroll];
+    uint2 k[kUnroll];
+    uint4 d[kUnroll];
     uint32_t eb[kUnroll];
-    long long off[kUnroll];
-    int c0[kUnroll];
+    long long row[kUnroll];
+    int c[kUnroll];
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j, w.next()) {
       const long long uj = u + j * stride;
-      c0[j] = w.v * 16;
-      off[j] = w.row * p.C + c0[j];
-      if (uj < p.total) {
-        k[j] = __ldg(reinterpret_cast<const uint4*>(p.q) + uj);
-        eb[j] = __ldg(p.scales + (uj >> 1));
-        if constexpr (kGrad) {
-          if (c0[j] < p.C) d0[j] = *reinterpret_cast<const uint4*>(p.dy + off[j]);
-          if (c0[j] + 8 < p.C) d1[j] = *reinterpret_cast<const uint4*>(p.dy + off[j] + 8);
-        }
+      row[j] = w.row;
+      c[j] = uj < p.total ? w.v * 8 : p.C;                    // p.C: nothing to do
+      if (c[j] < p.C) {
+        k[j] = __ldg(reinterpret_cast<const uint2*>(p.q) + uj);
+        eb[j] = __ldg(p.scales + (uj >> 2));
+        if constexpr (kGrad) d[j] = *reinterpret_cast<const uint4*>(p.dy + row[j] * p.C + c[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
-      if (u + j * stride >= p.total) break;
+      if (c[j] >= p.C) continue;
       const float step = a8_step(eb[j]);
+      float v[8];
+      a8_decode4(k[j].x, step, v);
+      a8_decode4(k[j].y, step, v + 4);
+      if constexpr (kGrad) {
+        float g[8];
+        T::unpack8(d[j], g);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = c0[j] + 8 * h;
-        if (c >= p.C) break;
-        float v[8];
-        a8_decode4(h ? k[j].z : k[j].x, step, v);
-        a8_decode4(h ? k[j].w : k[j].y, step, v + 4);
-        if constexpr (kGrad) {
-          float d[8];
-          T::unpack8(h ? d1[j] : d0[j], d);
+        for (int e = 0; e < 8; ++e) v[e] = g[e] * act_slope_safe<kAct>(v[e]);
+      } else {
+        if (p.gamma || p.beta) {
+          float g[8], b[8];
+          if (p.gamma) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma + c[j])), g);
+          if (p.beta) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta + c[j])), b);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = d[e] * act_slope_safe<kAct>(v[e]);
-        } else {
-          if (p.gamma || p.beta) {
-            float g[8], b[8];
-            if (p.gamma) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma + c)), g);
-            if (p.beta) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta + c)), b);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], p.gamma ? g[e] : 1.0f, p.beta ? b[e] : 0.0f);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = act_value<kAct>(v[e]);
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], p.gamma ? g[e] : 1.0f, p.beta ? b[e] : 0.0f);
         }
-        *reinterpret_cast<uint4*>(p.out + off[j] + 8 * h) = T::pack8(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = act_value<kAct>(v[e]);
       }
+      *reinterpret_cast<uint4*>(p.out + row[j] * p.C + c[j]) = T::pack8(v);
     }
   }
 }
@@ -604,59 +688,84 @@ unsigned blocks_for(long long work, long long per_block, long long cap) {
   return static_cast<unsigned>(b < 1 ? 1 : b);
 }
 
-// Rows per step of a block (block-wide groups) or of its 8 warps.
-constexpr int rows_per_step(int G, int R) { return G > 32 ? R : (kThreads / 32) * (32 / G) * R; }
+// Rows per step of a block.
+constexpr int rows_per_step(int G, int R, int T) { return G > 32 ? R : (T / 32) * (32 / G) * R; }
 
-template <bool kBF16, int G, int V, int R>
-cudaError_t run_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
-  const unsigned blocks = blocks_for(p.rows, rows_per_step(G, R), static_cast<long long>(sms) * (V >= 4 ? 3 : 4));
-  if (p.q) return launch(layernorm_fwd_kernel<kBF16, G, V, R, true>, blocks, kThreads, 0, 1, stream, p);
-  return launch(layernorm_fwd_kernel<kBF16, G, V, R, false>, blocks, kThreads, 0, 1, stream, p);
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<unsigned long long>& done, size_t bytes) {
+  if (bytes <= 48 * 1024) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
 }
 
-// The narrowest group and vector count that hold a row, with about four
-// 16-byte loads in flight per thread.
-template <bool kBF16>
+template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
+cudaError_t run_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
+  static std::atomic<unsigned long long> ready{0};
+  auto kern = layernorm_fwd_kernel<kBF16, G, V, R, T, D, kOcc, kCkpt>;
+  const unsigned blocks = blocks_for(p.rows, rows_per_step(G, R, T), static_cast<long long>(sms) * kOcc);
+  const size_t smem = static_cast<size_t>(D) * R * V * T * 16;
+  const cudaError_t e = allow_smem(kern, ready, smem);
+  if (e != cudaSuccess) return e;
+  return launch(kern, blocks, T, smem, 1, stream, p);
+}
+
+// The narrowest group and vector count that hold a row.
+template <bool kBF16, bool kCkpt>
 cudaError_t dispatch_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
   const int vecs = p.C / 8;
-  if (vecs <= 8) return run_fwd<kBF16, 8, 1, 4>(p, sms, stream);
-  if (vecs <= 16) return run_fwd<kBF16, 16, 1, 4>(p, sms, stream);
-  if (vecs <= 32) return run_fwd<kBF16, 32, 1, 4>(p, sms, stream);
-  if (vecs <= 64) return run_fwd<kBF16, 32, 2, 2>(p, sms, stream);
-  if (vecs <= 128) return run_fwd<kBF16, 32, 4, 1>(p, sms, stream);
-  if (vecs <= 256) return run_fwd<kBF16, 256, 1, 2>(p, sms, stream);
-  if (vecs <= 512) return run_fwd<kBF16, 256, 2, 1>(p, sms, stream);
-  return run_fwd<kBF16, 256, 4, 1>(p, sms, stream);
+  if (vecs <= 8) return run_fwd<kBF16, 8, 1, 2, 256, 8, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 16) return run_fwd<kBF16, 16, 1, 2, 256, 8, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 32) return run_fwd<kBF16, 32, 1, 2, 256, 8, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 64) return run_fwd<kBF16, 32, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 128) return run_fwd<kBF16, 32, 4, 1, 256, 4, 2, kCkpt>(p, sms, stream);
+  if (vecs <= 256) return run_fwd<kBF16, 32, 8, 1, 128, 4, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 512) return run_fwd<kBF16, 256, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
+  return run_fwd<kBF16, 256, 4, 1, 256, 4, 2, kCkpt>(p, sms, stream);
 }
 
-template <bool kBF16, int G, int V, int R>
+template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
 cudaError_t run_bwd(const LnBwdParams& p, unsigned blocks, cudaStream_t stream) {
-  const size_t smem = G > 32 ? 0 : static_cast<size_t>(kThreads / 64) * 2 * p.C * sizeof(float);
-  if (p.q) return launch(layernorm_bwd_kernel<kBF16, G, V, R, true>, blocks, kThreads, smem, 1, stream, p);
-  return launch(layernorm_bwd_kernel<kBF16, G, V, R, false>, blocks, kThreads, smem, 1, stream, p);
+  static std::atomic<unsigned long long> ready{0};
+  auto kern = layernorm_bwd_kernel<kBF16, G, V, R, T, D, kOcc, kCkpt>;
+  size_t smem = static_cast<size_t>(D) * ln_bwd_step_bytes(V, R, kCkpt, p.dres != nullptr) * T;
+  if constexpr (G <= 32) {   // the block's fold of its groups
+    const size_t fold = static_cast<size_t>(T / 64) * 2 * p.C * sizeof(float);
+    if (smem < fold) smem = fold;
+  }
+  const cudaError_t e = allow_smem(kern, ready, smem);
+  if (e != cudaSuccess) return e;
+  return launch(kern, blocks, T, smem, 1, stream, p);
 }
 
 unsigned bwd_blocks(long long rows, int C) {
   const int vecs = C / 8;
-  const int per = vecs <= 8    ? rows_per_step(8, 2)
-                  : vecs <= 16 ? rows_per_step(16, 2)
-                  : vecs <= 32 ? rows_per_step(32, 2)
-                  : vecs <= 128 ? rows_per_step(32, 1)
-                                : rows_per_step(256, 1);
+  const int per = vecs <= 8    ? rows_per_step(8, 2, 256)
+                  : vecs <= 16 ? rows_per_step(16, 2, 256)
+                  : vecs <= 32 ? rows_per_step(32, 2, 256)
+                  : vecs <= 64 ? rows_per_step(32, 1, 256)
+                  : vecs <= 128 ? rows_per_step(32, 1, 128)
+                  : vecs <= 256 ? rows_per_step(256, 2, 256)
+                                : rows_per_step(256, 1, 256);
   return blocks_for(rows, per, kLnBwdBlocks);
 }
 
-template <bool kBF16>
+template <bool kBF16, bool kCkpt>
 cudaError_t dispatch_bwd(const LnBwdParams& p, unsigned blocks, cudaStream_t stream) {
   const int vecs = p.C / 8;
-  if (vecs <= 8) return run_bwd<kBF16, 8, 1, 2>(p, blocks, stream);
-  if (vecs <= 16) return run_bwd<kBF16, 16, 1, 2>(p, blocks, stream);
-  if (vecs <= 32) return run_bwd<kBF16, 32, 1, 2>(p, blocks, stream);
-  if (vecs <= 64) return run_bwd<kBF16, 32, 2, 1>(p, blocks, stream);
-  if (vecs <= 128) return run_bwd<kBF16, 32, 4, 1>(p, blocks, stream);
-  if (vecs <= 256) return run_bwd<kBF16, 256, 1, 1>(p, blocks, stream);
-  if (vecs <= 512) return run_bwd<kBF16, 256, 2, 1>(p, blocks, stream);
-  return run_bwd<kBF16, 256, 4, 1>(p, blocks, stream);
+  if (vecs <= 8) return run_bwd<kBF16, 8, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 16) return run_bwd<kBF16, 16, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 32) return run_bwd<kBF16, 32, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 64) return run_bwd<kBF16, 32, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 128) return run_bwd<kBF16, 32, 4, 1, 128, 3, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 256) return run_bwd<kBF16, 256, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 512) return run_bwd<kBF16, 256, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
+  return run_bwd<kBF16, 256, 4, 1, 256, 4, 1, kCkpt>(p, blocks, stream);
 }
 
 template <bool kBF16, bool kGrad>
@@ -668,11 +777,8 @@ cudaError_t dispatch_read(int act, unsigned blocks, cudaStream_t stream, const R
 
 constexpr int kMaxAct8Channels = 1 << 24;
 
-// Units of 16 channels per row and in all.
-void unit_count(long long rows, int C, int& units, long long& total) {
-  units = 2 * ((C + 31) / 32);
-  total = rows * units;
-}
+// Units of `channels` channels per row, whose last block is padded.
+int units_per_row(int C, int channels) { return (32 / channels) * ((C + 31) / 32); }
 
 }  // namespace conv3d_channel
 
@@ -707,8 +813,11 @@ conv3d_status_t conv3d_layernorm_fwd(const void* x, const void* gamma, const voi
   LnFwdParams p{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(gamma),
                 static_cast<const uint16_t*>(beta), static_cast<uint16_t*>(y), mean, rstd,
                 static_cast<uint8_t*>(codes), static_cast<uint8_t*>(exponents), rows, C, eps};
-  const cudaError_t e = dtype == CONV3D_BF16 ? dispatch_fwd<true>(p, dev.num_sms, stream)
-                                             : dispatch_fwd<false>(p, dev.num_sms, stream);
+  const bool bf16 = dtype == CONV3D_BF16;
+  const cudaError_t e = codes ? (bf16 ? dispatch_fwd<true, true>(p, dev.num_sms, stream)
+                                      : dispatch_fwd<false, true>(p, dev.num_sms, stream))
+                              : (bf16 ? dispatch_fwd<true, false>(p, dev.num_sms, stream)
+                                      : dispatch_fwd<false, false>(p, dev.num_sms, stream));
   return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "layer norm launch");
 }
 
@@ -769,7 +878,9 @@ conv3d_status_t conv3d_layernorm_bwd(const void* dy, const void* x, const float*
                 static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(exponents), mean, rstd,
                 static_cast<const uint16_t*>(gamma), static_cast<const uint16_t*>(dres),
                 static_cast<uint16_t*>(dx), params ? static_cast<float*>(workspace) : nullptr, rows, C};
-  cudaError_t e = dtype == CONV3D_BF16 ? dispatch_bwd<true>(p, blocks, stream) : dispatch_bwd<false>(p, blocks, stream);
+  const bool bf16 = dtype == CONV3D_BF16;
+  cudaError_t e = from_codes ? (bf16 ? dispatch_bwd<true, true>(p, blocks, stream) : dispatch_bwd<false, true>(p, blocks, stream))
+                             : (bf16 ? dispatch_bwd<true, false>(p, blocks, stream) : dispatch_bwd<false, false>(p, blocks, stream));
   if (e != cudaSuccess) return cuda_fail(e, "layer norm gradient launch");
   if (!params) return CONV3D_OK;
   const unsigned cols = static_cast<unsigned>((2 * C + 31) / 32);
@@ -794,9 +905,8 @@ conv3d_status_t conv3d_act8_pack(const void* x, void* codes, void* exponents, lo
     return overlapping("x, codes and exponents must not overlap");
   Device dev;
   if ((st = current_device(dev)) != CONV3D_OK) return st;
-  int units;
-  long long total;
-  unit_count(rows, C, units, total);
+  const int units = units_per_row(C, 16);
+  const long long total = rows * units;
   const unsigned blocks = blocks_for(total, kThreads * kUnroll, dev.num_sms * 6LL);
   const uint16_t* x16 = static_cast<const uint16_t*>(x);
   uint8_t* q = static_cast<uint8_t*>(codes);
@@ -812,7 +922,7 @@ static conv3d_status_t act8_read(const void* codes, const void* exponents, const
                                  conv3d_dtype_t dtype, cudaStream_t stream) {
   conv3d_status_t st = check_sizes(rows, C, dtype, kMaxAct8Channels);
   if (st != CONV3D_OK) return st;
-  if (!codes || !exponents || !out || (grad && !dy) || act < CONV3D_ACT_NONE || act > CONV3D_ACT_GELU) {
+  if (!codes || !exponents || !out || (grad && !dy) || static_cast<int>(act) > CONV3D_ACT_GELU || static_cast<int>(act) < 0) {
     set_error("a tensor pointer is null or the activation %d unknown", static_cast<int>(act));
     return CONV3D_ERR_INVALID_ARG;
   }
@@ -828,9 +938,9 @@ static conv3d_status_t act8_read(const void* codes, const void* exponents, const
   if ((st = current_device(dev)) != CONV3D_OK) return st;
   ReadParams p{static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(exponents),
                static_cast<const uint16_t*>(gamma), static_cast<const uint16_t*>(beta),
-               static_cast<const uint16_t*>(dy), static_cast<uint16_t*>(out), 0, 0, C};
-  unit_count(rows, C, p.units, p.total);
-  const unsigned blocks = blocks_for(p.total, kThreads * kUnroll, dev.num_sms * 6LL);
+               static_cast<const uint16_t*>(dy), static_cast<uint16_t*>(out), rows * units_per_row(C, 8),
+               units_per_row(C, 8), C};
+  const unsigned blocks = blocks_for(p.total, kThreads * kUnroll, dev.num_sms * 8LL);
   const bool bf16 = dtype == CONV3D_BF16;
   const cudaError_t e = grad ? (bf16 ? dispatch_read<true, true>(act, blocks, stream, p)
                                      : dispatch_read<false, true>(act, blocks, stream, p))
