@@ -53,7 +53,50 @@ struct Val16 {
   static __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
   }
+  // the same with the eight values as four pairs
+  static __device__ __forceinline__ float2 pair(uint32_t w) {
+    if constexpr (kBF16) return make_float2(lo(w), hi(w));
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+  static __device__ __forceinline__ void unpack8(const uint4& q, float2 (&f)[4]) {
+    f[0] = pair(q.x); f[1] = pair(q.y); f[2] = pair(q.z); f[3] = pair(q.w);
+  }
+  static __device__ __forceinline__ uint4 pack8(const float2 (&f)[4]) {
+    return make_uint4(pack(f[0].x, f[0].y), pack(f[1].x, f[1].y), pack(f[2].x, f[2].y), pack(f[3].x, f[3].y));
+  }
 };
+
+// ------------------------------------------------------------------ pairs
+
+// Two fp32 values per instruction (sm_100's packed fp32 operations, each lane
+// rounded as the scalar operation is): the channel-wise kernels are bound by
+// instruction issue, and their sums and products come in pairs.
+__device__ __forceinline__ unsigned long long f2_bits(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 f2_from(unsigned long long b) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(b));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+  return f2_from(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_from(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_from(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // ------------------------------------------------------------------ activations
 
@@ -103,14 +146,60 @@ __device__ __forceinline__ float act_slope(float v) {
   }
 }
 
-// An infinite v makes u infinite and 1 - t^2 zero, and their product NaN; the
-// limits are used instead where |v| is so large that t has saturated.
+// The same for a pair: all but the two tanh in packed operations.
+__device__ __forceinline__ float2 tanh_hw2(float2 x) { return make_float2(tanh_hw(x.x), tanh_hw(x.y)); }
+
+template <int kAct>
+__device__ __forceinline__ float2 act_value(float2 v) {
+  if constexpr (kAct == kActSilu) {
+    const float2 h = mul2(both(0.5f), v);
+    return fma2(h, tanh_hw2(h), h);
+  } else if constexpr (kAct == kActGelu) {
+    const float2 u = mul2(v, fma2(both(kGeluC), mul2(v, v), both(kGeluA)));
+    const float2 h = mul2(both(0.5f), v);
+    return fma2(h, tanh_hw2(u), h);
+  } else {
+    return v;
+  }
+}
+
+template <int kAct>
+__device__ __forceinline__ float2 act_slope(float2 v) {
+  if constexpr (kAct == kActSilu) {
+    const float2 t = tanh_hw2(mul2(both(0.5f), v));
+    const float2 c = mul2(both(0.25f), v);
+    const float2 n = mul2(t, both(-1.0f));
+    return fma2(c, fma2(n, t, both(1.0f)), fma2(both(0.5f), t, both(0.5f)));
+  } else if constexpr (kAct == kActGelu) {
+    const float2 v2 = mul2(v, v);
+    const float2 t = tanh_hw2(mul2(v, fma2(both(kGeluC), v2, both(kGeluA))));
+    const float2 c = mul2(mul2(both(0.5f), v), fma2(both(3.0f * kGeluC), v2, both(kGeluA)));
+    const float2 n = mul2(t, both(-1.0f));
+    return fma2(c, fma2(n, t, both(1.0f)), fma2(both(0.5f), t, both(0.5f)));
+  } else {
+    return both(1.0f);
+  }
+}
+
+// Beyond |v| = 64 both derivatives are 0 or 1, t has long been -1 or 1 exactly,
+// and v^3 may overflow, which would leave infinity times zero: such arguments
+// are brought back to +-64.  (NaN stays: fminf and fmaxf would drop it.)
 template <int kAct>
 __device__ __forceinline__ float act_slope_safe(float v) {
   if constexpr (kAct == kActNone) return 1.0f;
-  const float c = fminf(fmaxf(v, -64.0f), 64.0f);
-  const float s = act_slope<kAct>(c);
+  const float s = act_slope<kAct>(fminf(fmaxf(v, -64.0f), 64.0f));
   return v == v ? s : v;
+}
+// For the values of one checkpoint block: only a step over 1/2 can hold one, and
+// a block marked as not finite (NaN step) fails the comparison and stays NaN.
+template <int N>
+__device__ __forceinline__ void act_limit(float2 (&v)[N], float step) {
+  if (step > 0.5f)
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      v[e].x = fminf(fmaxf(v[e].x, -64.0f), 64.0f);
+      v[e].y = fminf(fmaxf(v[e].y, -64.0f), 64.0f);
+    }
 }
 
 // ------------------------------------------------------------------ checkpoint code
@@ -127,10 +216,10 @@ __device__ __forceinline__ float a8_max(float m, float v) {
 }
 
 // The largest magnitude of 8 values, as bits.
-__device__ __forceinline__ uint32_t a8_mag8(const float (&f)[8]) {
+__device__ __forceinline__ uint32_t a8_mag8(const float2 (&f)[4]) {
   float m = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = a8_max(m, f[e]);
+  for (int e = 0; e < 4; ++e) m = a8_max(a8_max(m, f[e].x), f[e].y);
   return __float_as_uint(m);
 }
 
@@ -153,23 +242,25 @@ __device__ __forceinline__ float a8_step(uint32_t b) {
 // Codes of four values, the first in the low byte.  v * inv + 1.5 * 2^23
 // rounds v * inv (exact: inv is a power of two) to the nearest integer, ties to
 // even, and leaves it in the low bits of the sum in two's complement.
-__device__ __forceinline__ uint32_t a8_code4(float a, float b, float c, float d, float inv) {
+__device__ __forceinline__ uint32_t a8_code4(float2 a, float2 b, float inv) {
   constexpr float kMagic = 12582912.0f;
   const float lo = kMagic - 127.0f, hi = kMagic + 127.0f;
-  const uint32_t ia = __float_as_uint(fminf(fmaxf(fmaf(a, inv, kMagic), lo), hi));
-  const uint32_t ib = __float_as_uint(fminf(fmaxf(fmaf(b, inv, kMagic), lo), hi));
-  const uint32_t ic = __float_as_uint(fminf(fmaxf(fmaf(c, inv, kMagic), lo), hi));
-  const uint32_t id = __float_as_uint(fminf(fmaxf(fmaf(d, inv, kMagic), lo), hi));
-  return __byte_perm(__byte_perm(ia, ib, 0x0040), __byte_perm(ic, id, 0x0040), 0x5410);
+  a = fma2(a, both(inv), both(kMagic));
+  b = fma2(b, both(inv), both(kMagic));
+  const uint32_t i0 = __float_as_uint(fminf(fmaxf(a.x, lo), hi)), i1 = __float_as_uint(fminf(fmaxf(a.y, lo), hi));
+  const uint32_t i2 = __float_as_uint(fminf(fmaxf(b.x, lo), hi)), i3 = __float_as_uint(fminf(fmaxf(b.y, lo), hi));
+  return __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
 }
 
 // Values of four codes: the byte k + 128 under the exponent of 2^23 is the
 // float 2^23 + 128 + k, from which the subtraction leaves k exactly.
-__device__ __forceinline__ void a8_decode4(uint32_t w, float step, float* v) {
+__device__ __forceinline__ void a8_decode4(uint32_t w, float step, float2* v) {
   w ^= 0x80808080u;
+  float f[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v[i] = (__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + i)) - 8388736.0f) * step;
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + i));
+  v[0] = mul2(add2(make_float2(f[0], f[1]), both(-8388736.0f)), both(step));
+  v[1] = mul2(add2(make_float2(f[2], f[3]), both(-8388736.0f)), both(step));
 }
 
 }  // namespace conv3d

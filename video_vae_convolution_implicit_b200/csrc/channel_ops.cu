@@ -92,32 +92,31 @@ __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
   return v;
 }
 
-// A cached 16-byte load that stays where it is written: rows of two and more
-// vectors a thread read gamma and beta again at each use (from L1) rather than
-// hold them unpacked in registers.
-__device__ __forceinline__ uint4 ld_again(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
+__device__ __forceinline__ void st_global_v4(void* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
 
-// The rows of one walker.
+// The rows of one walker.  Row r of step k is first + k * stride + r *
+// kPerWarp; it exists while k < live(r), so that a step needs a 32-bit
+// comparison and an addition to the running offsets.
 template <int G, int R, int T>
 struct Walk {
   static constexpr int kPerWarp = G < 32 ? 32 / G : 1;
   static constexpr int kStep = kPerWarp * R;
-  long long first, stride;   // first row of step 0 (this thread's, r = 0) and rows between steps
-  long long steps;
+  long long first, stride;
+  int steps;            // of the walker: the same in all of its threads
+  int live_steps[R];
   __device__ __forceinline__ explicit Walk(long long rows) {
     const long long walker = G > 32 ? blockIdx.x : blockIdx.x * static_cast<long long>(T / 32) + threadIdx.x / 32;
     const long long walkers = static_cast<long long>(gridDim.x) * (G > 32 ? 1 : T / 32);
     const int sub = G < 32 ? (threadIdx.x % 32) / G : 0;
     first = walker * kStep + sub;
     stride = walkers * kStep;
-    const long long left = rows - walker * kStep;
-    steps = left > 0 ? (left + stride - 1) / stride : 0;
+    steps = count(rows - walker * kStep);
+#pragma unroll
+    for (int r = 0; r < R; ++r) live_steps[r] = count(rows - first - r * kPerWarp);
   }
-  __device__ __forceinline__ long long row(long long step, int r) const { return first + step * stride + r * kPerWarp; }
+  __device__ __forceinline__ int count(long long left) const {
+    return left > 0 ? static_cast<int>((left + stride - 1) / stride) : 0;
+  }
 };
 
 // ------------------------------------------------------------------ layer norm, forward
@@ -143,6 +142,10 @@ struct LnFwdParams {
 template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
 __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParams p) {
   using H = Val16<kBF16>;
+  constexpr uint32_t kSlot = R * V * T * 16;
+  // gamma and beta as fp32: in registers, or in shared memory behind the ring
+  // ([2][C] floats) where a thread holds more than two vectors
+  constexpr bool kRegParams = V <= 2;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[G > 32 ? 2 * (T / 32) * R : 1];
   int flip = 0;
@@ -152,43 +155,67 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
   const float inv_c = 1.0f / static_cast<float>(p.C);
   const Walk<G, R, T> walk(p.rows);
   const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16u;
-  constexpr uint32_t kSlot = R * V * T * 16;
-  griddep_wait();
-  auto fetch = [&](long long k, int slot) {
-    if (k < walk.steps)
+  const uint32_t params = smem_addr(ring_mem) + D * kSlot;
+  bool in[V];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const long long row = walk.row(k, r);
+  for (int i = 0; i < V; ++i) in[i] = l + i * G < vecs;
+  griddep_wait();
+  // byte offsets of this thread's first vector in x and y, now and of the next fetch
+  const long long first = (walk.first * p.C + l * 8) * 2, advance = walk.stride * p.C * 2;
+  const int per_row = Walk<G, R, T>::kPerWarp * p.C * 2;
+  const char* next = reinterpret_cast<const char*>(p.x) + first;
+  auto fetch = [&](int k, int slot) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (k < walk.live_steps[r])
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (l + i * G < vecs && row < p.rows)
-            cp_async16(ring + slot * kSlot + (r * V + i) * (T * 16), p.x + row * p.C + (l + i * G) * 8);
-      }
+          if (in[i]) cp_async16(ring + slot * kSlot + (r * V + i) * (T * 16), next + r * per_row + i * (G * 16));
+    next += advance;
     cp_async_commit();   // one group per step, empty ones included, so the count stays fixed
   };
 #pragma unroll
   for (int k = 0; k < D - 1; ++k) fetch(k, k);
-  uint4 ga, be;   // V == 1
-  if (V == 1 && p.gamma && l < vecs) ga = __ldg(reinterpret_cast<const uint4*>(p.gamma) + l);
-  if (V == 1 && p.beta && l < vecs) be = __ldg(reinterpret_cast<const uint4*>(p.beta) + l);
+  float2 gm[kRegParams ? V : 1][4], bt[kRegParams ? V : 1][4];
+  if constexpr (kRegParams) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        gm[i][e] = both(1.0f);
+        bt[i][e] = both(0.0f);
+      }
+      if (p.gamma && in[i]) H::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma) + l + i * G), gm[i]);
+      if (p.beta && in[i]) H::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta) + l + i * G), bt[i]);
+    }
+  } else {
+    for (int c = threadIdx.x; c < p.C; c += T) {
+      const float g = p.gamma ? H::lo(p.gamma[c]) : 1.0f, b = p.beta ? H::lo(p.beta[c]) : 0.0f;
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(params + c * 4u), "f"(g) : "memory");
+      asm volatile("st.shared.f32 [%0], %1;" ::"r"(params + (p.C + c) * 4u), "f"(b) : "memory");
+    }
+    __syncthreads();
+  }
+  char* out = reinterpret_cast<char*>(p.y) + first;
+  long long row0 = walk.first;
   int slot = 0;
-  for (long long k = 0; k < walk.steps; ++k) {
+  for (int k = 0; k < walk.steps; ++k) {
     // the slot of the step before this one was read into registers then: refill it
     fetch(k + D - 1, slot == 0 ? D - 1 : slot - 1);
     cp_async_wait<D - 1>();
-    float d[R][V][8], s[R];
+    float2 d[R][V][4];
+    float s[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool live = walk.row(k, r) < p.rows;
-      s[r] = 0.0f;
+      float2 a = both(0.0f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         uint4 raw = make_uint4(0, 0, 0, 0);
-        if (l + i * G < vecs && live) raw = ld_shared_v4(ring + slot * kSlot + (r * V + i) * (T * 16));
+        if (in[i] && k < walk.live_steps[r]) raw = ld_shared_v4(ring + slot * kSlot + (r * V + i) * (T * 16));
         H::unpack8(raw, d[r][i]);
-        s[r] += ((d[r][i][0] + d[r][i][1]) + (d[r][i][2] + d[r][i][3])) +
-                ((d[r][i][4] + d[r][i][5]) + (d[r][i][6] + d[r][i][7]));
+        a = add2(a, add2(add2(d[r][i][0], d[r][i][1]), add2(d[r][i][2], d[r][i][3])));
       }
+      s[r] = a.x + a.y;
     }
     slot = slot == D - 1 ? 0 : slot + 1;
     group_sum<G, R>(s, red, flip);
@@ -196,23 +223,24 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       mean[r] = s[r] * inv_c;
-      s[r] = 0.0f;
+      float2 a = both(0.0f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float a = 0.0f;
+        float2 sq = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          d[r][i][e] -= mean[r];
-          a = fmaf(d[r][i][e], d[r][i][e], a);
+        for (int e = 0; e < 4; ++e) {
+          d[r][i][e] = add2(d[r][i][e], both(-mean[r]));
+          sq = fma2(d[r][i][e], d[r][i][e], sq);
         }
-        if (l + i * G < vecs) s[r] += a;
+        if (in[i]) a = add2(a, sq);
       }
+      s[r] = a.x + a.y;
     }
     group_sum<G, R>(s, red, flip);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const long long row = walk.row(k, r);
-      const bool live = row < p.rows;
+      const bool live = k < walk.live_steps[r];
+      const long long row = row0 + r * Walk<G, R, T>::kPerWarp;
       const float rstd = rsqrtf(fmaf(s[r], inv_c, p.eps));
       if (l == 0 && live) {
         if (p.mean) p.mean[row] = mean[r];
@@ -220,36 +248,45 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = l + i * G;
-        float(&f)[8] = d[r][i];
+        float2(&f)[4] = d[r][i];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(f[e], rstd);
+        for (int e = 0; e < 4; ++e) f[e] = mul2(f[e], both(rstd));
         if constexpr (kCkpt) {
+          const int c = l + i * G;
           uint32_t mag = a8_mag8(f);
-          if (c >= vecs) mag = 0u;
+          if (!in[i]) mag = 0u;
           mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
           mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 2));
           const uint32_t b = a8_exponent(mag);
           const float inv = a8_inv_step(b);
           if (c < nb * 4 && live) {
             uint2 q = make_uint2(0, 0);   // zero codes behind the last channel
-            if (c < vecs)
-              q = make_uint2(a8_code4(f[0], f[1], f[2], f[3], inv), a8_code4(f[4], f[5], f[6], f[7], inv));
+            if (in[i]) q = make_uint2(a8_code4(f[0], f[1], inv), a8_code4(f[2], f[3], inv));
             *reinterpret_cast<uint2*>(p.q + (row * nb * 4 + c) * 8) = q;
             if ((c & 3) == 0) p.scales[row * nb + (c >> 2)] = static_cast<uint8_t>(b);
           }
         }
-        if (c < vecs && live) {
-          float gm[8], bt[8];
-          if (p.gamma) H::unpack8(V == 1 ? ga : ld_again(p.gamma + c * 8), gm);
-          if (p.beta) H::unpack8(V == 1 ? be : ld_again(p.beta + c * 8), bt);
-          // (a fused multiply-add by name, so that every variant rounds alike)
+        if (in[i] && live) {
+          if constexpr (kRegParams) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = fmaf(f[e], p.gamma ? gm[e] : 1.0f, p.beta ? bt[e] : 0.0f);
-          *reinterpret_cast<uint4*>(p.y + row * p.C + c * 8) = H::pack8(f);
+            for (int e = 0; e < 4; ++e) f[e] = fma2(f[e], gm[i][e], bt[i][e]);
+          } else {
+            const uint32_t at = params + (l + i * G) * 32u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 g = ld_shared_v4(at + h * 16u), b = ld_shared_v4(at + p.C * 4u + h * 16u);
+              f[2 * h] = fma2(f[2 * h], make_float2(__uint_as_float(g.x), __uint_as_float(g.y)),
+                              make_float2(__uint_as_float(b.x), __uint_as_float(b.y)));
+              f[2 * h + 1] = fma2(f[2 * h + 1], make_float2(__uint_as_float(g.z), __uint_as_float(g.w)),
+                                  make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
+            }
+          }
+          st_global_v4(out + r * per_row + i * (G * 16), H::pack8(f));
         }
       }
     }
+    out += advance;
+    row0 += walk.stride;
   }
   cp_async_wait<0>();
 }
@@ -289,6 +326,7 @@ template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
 __global__ void __launch_bounds__(T, kOcc) layernorm_bwd_kernel(const LnBwdParams p) {
   using H = Val16<kBF16>;
   constexpr int kWarps = T / 32;
+  constexpr int kPerWarp = Walk<G, R, T>::kPerWarp;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[G > 32 ? 2 * (T / 32) * 2 * R : 1];
   int flip = 0;
@@ -305,118 +343,136 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_bwd_kernel(const LnBwdParam
   constexpr uint32_t kDyEnd = R * V * T * 16;
   constexpr uint32_t kSrcEnd = kDyEnd + R * V * T * kSrc;
   const uint32_t res_end = kSrcEnd + (has_res ? kDyEnd : 0u);
-  float dg[V][8], db[V][8];
+  bool in[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) in[i] = l + i * G < vecs;
+  float2 dg[V][4], db[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.0f;
+    for (int e = 0; e < 4; ++e) dg[i][e] = db[i][e] = both(0.0f);
   griddep_wait();
   const long long scale_bytes = p.rows * nb;
-  auto fetch = [&](long long k, int slot) {
-    if (k < walk.steps) {
-      const uint32_t s = base + slot * step_bytes;
+  // running byte offsets: the 16-bit tensors share one, the codes' is its own
+  const long long first = (walk.first * p.C + l * 8) * 2, advance = walk.stride * p.C * 2;
+  const int per_row = kPerWarp * p.C * 2;
+  long long ahead = first;
+  const uint8_t* codes = kCkpt ? p.q + walk.first * nb * 32 + l * 8 : nullptr;
+  long long row_ahead = walk.first;
+  auto fetch = [&](int k, int slot) {
+    const uint32_t s = base + slot * step_bytes;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const long long row = walk.row(k, r);
-        if (row >= p.rows) continue;
+    for (int r = 0; r < R; ++r) {
+      if (k < walk.live_steps[r]) {
+        const long long row = row_ahead + r * kPerWarp;
         cp_async4(s + res_end + (r * T + threadIdx.x) * 4u, p.rstd + row);
         if constexpr (!kCkpt) cp_async4(s + res_end + ((R + r) * T + threadIdx.x) * 4u, p.mean + row);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const int c = l + i * G;
-          if (c >= vecs) continue;
-          const uint32_t at = (r * V + i) * T + threadIdx.x;
-          cp_async16(s + at * 16u, p.dy + row * p.C + c * 8);
-          if constexpr (kCkpt) {
-            cp_async8(s + kDyEnd + at * 8u, p.q + (row * nb * 4 + c) * 8);
-            // the aligned word that holds the exponent byte, short of the buffer's end
-            const long long off = (row * nb + (c >> 2)) & ~3LL;
-            cp_async4(s + res_end + (R * T + at) * 4u, p.scales + off,
-                      scale_bytes - off < 4 ? static_cast<uint32_t>(scale_bytes - off) : 4u);
-          } else {
-            cp_async16(s + kDyEnd + at * 16u, p.x + row * p.C + c * 8);
+          if (in[i]) {
+            const uint32_t at = (r * V + i) * T + threadIdx.x;
+            const long long off = ahead + r * per_row + i * (G * 16);
+            cp_async16(s + at * 16u, reinterpret_cast<const char*>(p.dy) + off);
+            if (has_res) cp_async16(s + kSrcEnd + at * 16u, reinterpret_cast<const char*>(p.dres) + off);
+            if constexpr (kCkpt) {
+              cp_async8(s + kDyEnd + at * 8u, codes + r * (kPerWarp * nb * 32) + i * (G * 8));
+              // the aligned word that holds the exponent byte, short of the buffer's end
+              const long long e = (row * nb + ((l + i * G) >> 2)) & ~3LL;
+              const long long left = scale_bytes - e;
+              cp_async4(s + res_end + (R * T + at) * 4u, p.scales + e, left < 4 ? static_cast<uint32_t>(left) : 4u);
+            } else {
+              cp_async16(s + kDyEnd + at * 16u, reinterpret_cast<const char*>(p.x) + off);
+            }
           }
-          if (has_res) cp_async16(s + kSrcEnd + at * 16u, p.dres + row * p.C + c * 8);
         }
       }
     }
+    ahead += advance;
+    if constexpr (kCkpt) codes += walk.stride * nb * 32;
+    row_ahead += walk.stride;
     cp_async_commit();
   };
 #pragma unroll
   for (int k = 0; k < D - 1; ++k) fetch(k, k);
-  uint4 ga[V];
+  float2 gm[V][4];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = l + i * G;
-    ga[i] = make_uint4(0, 0, 0, 0);
-    if (p.gamma && c < vecs) ga[i] = __ldg(reinterpret_cast<const uint4*>(p.gamma) + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gm[i][e] = both(1.0f);
+    if (p.gamma && in[i]) H::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma) + l + i * G), gm[i]);
   }
+  char* out_dx = reinterpret_cast<char*>(p.dx) + first;
+  uint32_t row_nb = static_cast<uint32_t>(walk.first * nb);   // low bits of row * nb: the exponent byte's place
   int slot = 0;
-  for (long long k = 0; k < walk.steps; ++k) {
+  for (int k = 0; k < walk.steps; ++k) {
     fetch(k + D - 1, slot == 0 ? D - 1 : slot - 1);
     cp_async_wait<D - 1>();
     const uint32_t s = base + slot * step_bytes;
-    float g[R][V][8], xh[R][V][8], rstd[R], c12[2 * R];
+    float2 g[R][V][4], xh[R][V][4];
+    float rstd[R], c12[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const long long row = walk.row(k, r);
-      const bool live = row < p.rows;
+      const bool live = k < walk.live_steps[r];
       rstd[r] = live ? __uint_as_float(ld_shared_u32(s + res_end + (r * T + threadIdx.x) * 4u)) : 0.0f;
       float mean = 0.0f;
       if constexpr (!kCkpt)
         mean = live ? __uint_as_float(ld_shared_u32(s + res_end + ((R + r) * T + threadIdx.x) * 4u)) : 0.0f;
-      float a = 0.0f, b = 0.0f;
+      float2 a = both(0.0f), b = both(0.0f);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = l + i * G;
         const uint32_t at = (r * V + i) * T + threadIdx.x;
-        if (live && c < vecs) {
+        if (live && in[i]) {
           H::unpack8(ld_shared_v4(s + at * 16u), g[r][i]);
           if constexpr (kCkpt) {
             const uint32_t word = ld_shared_u32(s + res_end + (R * T + at) * 4u);
-            const uint32_t byte = static_cast<uint32_t>(row * nb + (c >> 2)) & 3u;
+            const uint32_t byte = (row_nb + static_cast<uint32_t>(r * kPerWarp * nb + ((l + i * G) >> 2))) & 3u;
             const float step = a8_step((word >> (8u * byte)) & 0xFFu);
             const uint2 q = ld_shared_v2(s + kDyEnd + at * 8u);
             a8_decode4(q.x, step, xh[r][i]);
-            a8_decode4(q.y, step, xh[r][i] + 4);
+            a8_decode4(q.y, step, xh[r][i] + 2);
           } else {
             H::unpack8(ld_shared_v4(s + kDyEnd + at * 16u), xh[r][i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xh[r][i][e] = (xh[r][i][e] - mean) * rstd[r];
+            for (int e = 0; e < 4; ++e) xh[r][i][e] = mul2(add2(xh[r][i][e], both(-mean)), both(rstd[r]));
           }
-          float gm[8];
-          if (p.gamma) H::unpack8(ga[i], gm);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float dy = g[r][i][e];
-            db[i][e] += dy;
-            dg[i][e] = fmaf(dy, xh[r][i][e], dg[i][e]);
-            g[r][i][e] = p.gamma ? dy * gm[e] : dy;
-            a += g[r][i][e];
-            b = fmaf(g[r][i][e], xh[r][i][e], b);
+          for (int e = 0; e < 4; ++e) {
+            const float2 dy = g[r][i][e];
+            db[i][e] = add2(db[i][e], dy);
+            dg[i][e] = fma2(dy, xh[r][i][e], dg[i][e]);
+            g[r][i][e] = mul2(dy, gm[i][e]);
+            a = add2(a, g[r][i][e]);
+            b = fma2(g[r][i][e], xh[r][i][e], b);
           }
         }
       }
-      c12[2 * r] = a;
-      c12[2 * r + 1] = b;
+      c12[2 * r] = a.x + a.y;
+      c12[2 * r + 1] = b.x + b.y;
     }
     group_sum<G, 2 * R>(c12, red, flip);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const long long row = walk.row(k, r);
-      const float c1 = c12[2 * r] * inv_c, c2 = c12[2 * r + 1] * inv_c;
+      // dx = rstd * g - rstd * c1 - xh * (rstd * c2)
+      const float2 k1 = both(-rstd[r] * (c12[2 * r] * inv_c)), k2 = both(-rstd[r] * (c12[2 * r + 1] * inv_c));
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = l + i * G;
-        if (row >= p.rows || c >= vecs) continue;
-        float o[8], add[8];
-        if (has_res) H::unpack8(ld_shared_v4(s + kSrcEnd + ((r * V + i) * T + threadIdx.x) * 16u), add);
+        if (k < walk.live_steps[r] && in[i]) {
+          float2 o[4];
+          if (has_res) {
+            H::unpack8(ld_shared_v4(s + kSrcEnd + ((r * V + i) * T + threadIdx.x) * 16u), o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          o[e] = fmaf(rstd[r], g[r][i][e] - fmaf(xh[r][i][e], c2, c1), has_res ? add[e] : 0.0f);
-        *reinterpret_cast<uint4*>(p.dx + row * p.C + c * 8) = H::pack8(o);
+            for (int e = 0; e < 4; ++e)
+              o[e] = add2(o[e], fma2(g[r][i][e], both(rstd[r]), fma2(xh[r][i][e], k2, k1)));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = fma2(g[r][i][e], both(rstd[r]), fma2(xh[r][i][e], k2, k1));
+          }
+          st_global_v4(out_dx + r * per_row + i * (G * 16), H::pack8(o));
+        }
       }
     }
+    out_dx += advance;
+    row_nb += static_cast<uint32_t>(walk.stride * nb);
     slot = slot == D - 1 ? 0 : slot + 1;
   }
   cp_async_wait<0>();
@@ -432,9 +488,11 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_bwd_kernel(const LnBwdParam
 #pragma unroll
       for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dg[i][e] += __shfl_xor_sync(0xFFFFFFFFu, dg[i][e], o);
-          db[i][e] += __shfl_xor_sync(0xFFFFFFFFu, db[i][e], o);
+        for (int e = 0; e < 4; ++e) {
+          dg[i][e].x += __shfl_xor_sync(0xFFFFFFFFu, dg[i][e].x, o);
+          dg[i][e].y += __shfl_xor_sync(0xFFFFFFFFu, dg[i][e].y, o);
+          db[i][e].x += __shfl_xor_sync(0xFFFFFFFFu, db[i][e].x, o);
+          db[i][e].y += __shfl_xor_sync(0xFFFFFFFFu, db[i][e].y, o);
         }
     const int warp = threadIdx.x / 32;
     const bool holds = threadIdx.x % 32 < G;
@@ -444,22 +502,22 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_bwd_kernel(const LnBwdParam
         for (int i = 0; i < V; ++i)
           if (l + i * G < vecs) {
             float4* f = reinterpret_cast<float4*>(fold + (static_cast<size_t>(warp - half) * 2) * p.C + (l + i * G) * 8);
-            f[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-            f[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+            f[0] = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
+            f[1] = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
             f += p.C / 4;
-            f[0] = make_float4(db[i][0], db[i][1], db[i][2], db[i][3]);
-            f[1] = make_float4(db[i][4], db[i][5], db[i][6], db[i][7]);
+            f[0] = make_float4(db[i][0].x, db[i][0].y, db[i][1].x, db[i][1].y);
+            f[1] = make_float4(db[i][2].x, db[i][2].y, db[i][3].x, db[i][3].y);
           }
       __syncthreads();
       if (holds && warp < half)
 #pragma unroll
         for (int i = 0; i < V; ++i)
           if (l + i * G < vecs) {
-            const float* f = fold + (static_cast<size_t>(warp) * 2) * p.C + (l + i * G) * 8;
+            const float2* f = reinterpret_cast<const float2*>(fold + (static_cast<size_t>(warp) * 2) * p.C + (l + i * G) * 8);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              dg[i][e] += f[e];
-              db[i][e] += f[p.C + e];
+            for (int e = 0; e < 4; ++e) {
+              dg[i][e] = add2(dg[i][e], f[e]);
+              db[i][e] = add2(db[i][e], f[p.C / 2 + e]);
             }
           }
       __syncthreads();
@@ -471,11 +529,11 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_bwd_kernel(const LnBwdParam
     const int c = l + i * G;
     if (c < vecs) {
       float4* o = reinterpret_cast<float4*>(out + c * 8);
-      o[0] = make_float4(dg[i][0], dg[i][1], dg[i][2], dg[i][3]);
-      o[1] = make_float4(dg[i][4], dg[i][5], dg[i][6], dg[i][7]);
+      o[0] = make_float4(dg[i][0].x, dg[i][0].y, dg[i][1].x, dg[i][1].y);
+      o[1] = make_float4(dg[i][2].x, dg[i][2].y, dg[i][3].x, dg[i][3].y);
       o = reinterpret_cast<float4*>(out + p.C + c * 8);
-      o[0] = make_float4(db[i][0], db[i][1], db[i][2], db[i][3]);
-      o[1] = make_float4(db[i][4], db[i][5], db[i][6], db[i][7]);
+      o[0] = make_float4(db[i][0].x, db[i][0].y, db[i][1].x, db[i][1].y);
+      o[1] = make_float4(db[i][2].x, db[i][2].y, db[i][3].x, db[i][3].y);
     }
   }
 }
@@ -560,19 +618,17 @@ __global__ void __launch_bounds__(kThreads) act8_pack_kernel(const uint16_t* __r
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       const long long uk = u0 + (threadIdx.x & 31) + k * stride;
-      float f[8], g[8];
+      float2 f[4], g[4];
       T::unpack8(a[k], f);
       T::unpack8(b[k], g);
-      uint32_t mag = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) mag = max(mag, max(a8_mag(f[e]), a8_mag(g[e])));
+      uint32_t mag = max(a8_mag8(f), a8_mag8(g));
       mag = max(mag, __shfl_xor_sync(0xFFFFFFFFu, mag, 1));
       const uint32_t eb = a8_exponent(mag);
       const float inv = a8_inv_step(eb);
       if (uk < total) {
         *reinterpret_cast<uint4*>(q + uk * 16) =
-            make_uint4(a8_code4(f[0], f[1], f[2], f[3], inv), a8_code4(f[4], f[5], f[6], f[7], inv),
-                       a8_code4(g[0], g[1], g[2], g[3], inv), a8_code4(g[4], g[5], g[6], g[7], inv));
+            make_uint4(a8_code4(f[0], f[1], inv), a8_code4(f[2], f[3], inv), a8_code4(g[0], g[1], inv),
+                       a8_code4(g[2], g[3], inv));
         if ((uk & 1) == 0) scales[uk >> 1] = static_cast<uint8_t>(eb);
       }
     }
@@ -621,24 +677,35 @@ __global__ void __launch_bounds__(kThreads) act8_read_kernel(const ReadParams p)
     for (int j = 0; j < kUnroll; ++j) {
       if (c[j] >= p.C) continue;
       const float step = a8_step(eb[j]);
-      float v[8];
+      float2 v[4];
       a8_decode4(k[j].x, step, v);
-      a8_decode4(k[j].y, step, v + 4);
+      a8_decode4(k[j].y, step, v + 2);
       if constexpr (kGrad) {
-        float g[8];
+        float2 g[4];
         T::unpack8(d[j], g);
+        if constexpr (kAct != kActNone) {
+          act_limit(v, step);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = g[e] * act_slope_safe<kAct>(v[e]);
+          for (int e = 0; e < 4; ++e) v[e] = mul2(g[e], act_slope<kAct>(v[e]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = g[e];
+        }
       } else {
         if (p.gamma || p.beta) {
-          float g[8], b[8];
+          float2 g[4], b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            g[e] = both(1.0f);
+            b[e] = both(0.0f);
+          }
           if (p.gamma) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma + c[j])), g);
           if (p.beta) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta + c[j])), b);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], p.gamma ? g[e] : 1.0f, p.beta ? b[e] : 0.0f);
+          for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], g[e], b[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = act_value<kAct>(v[e]);
+        for (int e = 0; e < 4; ++e) v[e] = act_value<kAct>(v[e]);
       }
       *reinterpret_cast<uint4*>(p.out + row[j] * p.C + c[j]) = T::pack8(v);
     }
@@ -709,7 +776,7 @@ cudaError_t run_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
   static std::atomic<unsigned long long> ready{0};
   auto kern = layernorm_fwd_kernel<kBF16, G, V, R, T, D, kOcc, kCkpt>;
   const unsigned blocks = blocks_for(p.rows, rows_per_step(G, R, T), static_cast<long long>(sms) * kOcc);
-  const size_t smem = static_cast<size_t>(D) * R * V * T * 16;
+  const size_t smem = static_cast<size_t>(D) * R * V * T * 16 + (V <= 2 ? 0 : 2 * p.C * sizeof(float));
   const cudaError_t e = allow_smem(kern, ready, smem);
   if (e != cudaSuccess) return e;
   return launch(kern, blocks, T, smem, 1, stream, p);
@@ -720,10 +787,10 @@ template <bool kBF16, bool kCkpt>
 cudaError_t dispatch_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
   const int vecs = p.C / 8;
   if (vecs <= 8) return run_fwd<kBF16, 8, 1, 2, 256, 8, 3, kCkpt>(p, sms, stream);
-  if (vecs <= 16) return run_fwd<kBF16, 16, 1, 2, 256, 8, 3, kCkpt>(p, sms, stream);
-  if (vecs <= 32) return run_fwd<kBF16, 32, 1, 2, 256, 8, 3, kCkpt>(p, sms, stream);
-  if (vecs <= 64) return run_fwd<kBF16, 32, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
-  if (vecs <= 128) return run_fwd<kBF16, 32, 4, 1, 256, 4, 2, kCkpt>(p, sms, stream);
+  if (vecs <= 16) return run_fwd<kBF16, 8, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 32) return run_fwd<kBF16, 16, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 64) return run_fwd<kBF16, 16, 4, 1, 256, 4, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 128) return run_fwd<kBF16, 32, 4, 1, 256, 4, 3, kCkpt>(p, sms, stream);
   if (vecs <= 256) return run_fwd<kBF16, 32, 8, 1, 128, 4, 3, kCkpt>(p, sms, stream);
   if (vecs <= 512) return run_fwd<kBF16, 256, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
   return run_fwd<kBF16, 256, 4, 1, 256, 4, 2, kCkpt>(p, sms, stream);
@@ -746,8 +813,8 @@ cudaError_t run_bwd(const LnBwdParams& p, unsigned blocks, cudaStream_t stream) 
 unsigned bwd_blocks(long long rows, int C) {
   const int vecs = C / 8;
   const int per = vecs <= 8    ? rows_per_step(8, 2, 256)
-                  : vecs <= 16 ? rows_per_step(16, 2, 256)
-                  : vecs <= 32 ? rows_per_step(32, 2, 256)
+                  : vecs <= 16 ? rows_per_step(8, 1, 256)
+                  : vecs <= 32 ? rows_per_step(16, 1, 256)
                   : vecs <= 64 ? rows_per_step(32, 1, 256)
                   : vecs <= 128 ? rows_per_step(32, 1, 128)
                   : vecs <= 256 ? rows_per_step(256, 2, 256)
@@ -759,8 +826,8 @@ template <bool kBF16, bool kCkpt>
 cudaError_t dispatch_bwd(const LnBwdParams& p, unsigned blocks, cudaStream_t stream) {
   const int vecs = p.C / 8;
   if (vecs <= 8) return run_bwd<kBF16, 8, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
-  if (vecs <= 16) return run_bwd<kBF16, 16, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
-  if (vecs <= 32) return run_bwd<kBF16, 32, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 16) return run_bwd<kBF16, 8, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 32) return run_bwd<kBF16, 16, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
   if (vecs <= 64) return run_bwd<kBF16, 32, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
   if (vecs <= 128) return run_bwd<kBF16, 32, 4, 1, 128, 3, 2, kCkpt>(p, blocks, stream);
   if (vecs <= 256) return run_bwd<kBF16, 256, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);

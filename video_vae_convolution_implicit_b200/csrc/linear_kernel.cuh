@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           const int col = col0 + 32 * j;
           uint32_t raw[32];
           tmem_ld_32x32b_x32(t_row + j * 32, raw);
-          float v[32];
+          float2 v[16];
           if constexpr (kLoadCodes) {
             const uint32_t b = load_no & 1;
             if (!wait_bounded(lbar + 8 * b, (load_no >> 1) & 1, ctl, true)) {
@@ -334,28 +334,30 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             const float step = a8_step((eb4 >> (8 * j)) & 0xFFu);
             const uint4 k0 = ld_shared_v4(cbuf + b * kLinCodeBytes + swz32(lane, 0));
             const uint4 k1 = ld_shared_v4(cbuf + b * kLinCodeBytes + swz32(lane, 1));
-            a8_decode4(k0.x, step, v); a8_decode4(k0.y, step, v + 4);
-            a8_decode4(k0.z, step, v + 8); a8_decode4(k0.w, step, v + 12);
-            a8_decode4(k1.x, step, v + 16); a8_decode4(k1.y, step, v + 20);
-            a8_decode4(k1.z, step, v + 24); a8_decode4(k1.w, step, v + 28);
+            a8_decode4(k0.x, step, v); a8_decode4(k0.y, step, v + 2);
+            a8_decode4(k0.z, step, v + 4); a8_decode4(k0.w, step, v + 6);
+            a8_decode4(k1.x, step, v + 8); a8_decode4(k1.y, step, v + 10);
+            a8_decode4(k1.z, step, v + 12); a8_decode4(k1.w, step, v + 14);
+            act_limit(v, step);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = act_slope_safe<kAct>(v[e]);
+            for (int e = 0; e < 16; ++e) v[e] = act_slope<kAct>(v[e]);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] *= __uint_as_float(raw[e]);
+            for (int e = 0; e < 16; ++e)
+              v[e] = mul2(v[e], make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])));
           } else {
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
+            for (int e = 0; e < 16; ++e) v[e] = make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1]));
           }
           if (!kBwd && bias4 != nullptr) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               if (col + 8 * g < p.N) {
-                float f[8];
+                float2 f[4];
                 T::unpack8(__ldg(bias4 + col / 8 + g), f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[8 * g + e] += f[e];
+                for (int e = 0; e < 4; ++e) v[4 * g + e] = add2(v[4 * g + e], f[e]);
               }
           }
           const uint32_t ob = obuf + (out_no & 1) * kLinOutBytes;
@@ -364,22 +366,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if (lane == 0) bulk_wait_group_read<1>();
           __syncwarp();
           if constexpr (!kBwd && kQ) {
-            uint32_t mag = 0;
+            float m = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mag = max(mag, a8_mag(v[e]));
-            const uint32_t eb = a8_exponent(mag);
+            for (int e = 0; e < 16; ++e) m = a8_max(a8_max(m, v[e].x), v[e].y);
+            const uint32_t eb = a8_exponent(__float_as_uint(m));
             const float inv = a8_inv_step(eb);
             eb4 |= eb << (8 * j);
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              st_shared_v4(cb + swz32(lane, h), a8_code4(v[16 * h], v[16 * h + 1], v[16 * h + 2], v[16 * h + 3], inv),
-                           a8_code4(v[16 * h + 4], v[16 * h + 5], v[16 * h + 6], v[16 * h + 7], inv),
-                           a8_code4(v[16 * h + 8], v[16 * h + 9], v[16 * h + 10], v[16 * h + 11], inv),
-                           a8_code4(v[16 * h + 12], v[16 * h + 13], v[16 * h + 14], v[16 * h + 15], inv));
+              st_shared_v4(cb + swz32(lane, h), a8_code4(v[8 * h], v[8 * h + 1], inv),
+                           a8_code4(v[8 * h + 2], v[8 * h + 3], inv), a8_code4(v[8 * h + 4], v[8 * h + 5], inv),
+                           a8_code4(v[8 * h + 6], v[8 * h + 7], inv));
           }
           if constexpr (!kBwd && kAct != kActNone) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = act_value<kAct>(v[e]);
+            for (int e = 0; e < 16; ++e) v[e] = act_value<kAct>(v[e]);
           }
           if (has_res) {
             const uint32_t b = load_no & 1;
@@ -390,16 +391,16 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             ++load_no;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              float f[8];
+              float2 f[4];
               T::unpack8(ld_shared_v4(abuf + b * kLinOutBytes + swz64(lane, g)), f);
 #pragma unroll
-              for (int e = 0; e < 8; ++e) v[8 * g + e] += f[e];
+              for (int e = 0; e < 4; ++e) v[4 * g + e] = add2(v[4 * g + e], f[e]);
             }
           }
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            st_shared_v4(ob + swz64(lane, g), T::pack(v[8 * g], v[8 * g + 1]), T::pack(v[8 * g + 2], v[8 * g + 3]),
-                         T::pack(v[8 * g + 4], v[8 * g + 5]), T::pack(v[8 * g + 6], v[8 * g + 7]));
+            st_shared_v4(ob + swz64(lane, g), T::pack(v[4 * g].x, v[4 * g].y), T::pack(v[4 * g + 1].x, v[4 * g + 1].y),
+                         T::pack(v[4 * g + 2].x, v[4 * g + 2].y), T::pack(v[4 * g + 3].x, v[4 * g + 3].y));
           fence_proxy_async_shared();
           __syncwarp();   // the chunk is staged, and every lane has read its load buffer
           if (lane == 0) {
@@ -620,7 +621,7 @@ __global__ void __launch_bounds__(kLinRowsThreads)
         v += bv;
         if constexpr (kQ) {
           const uint32_t b = a8_exponent(__reduce_max_sync(0xFFFFFFFFu, a8_mag(v)));
-          p.codes[row * p.blocks * 32 + ch] = static_cast<uint8_t>(a8_code4(v, 0.0f, 0.0f, 0.0f, a8_inv_step(b)) & 0xFFu);
+          p.codes[row * p.blocks * 32 + ch] = static_cast<uint8_t>(a8_code4(make_float2(v, 0.0f), both(0.0f), a8_inv_step(b)) & 0xFFu);
           if (lane == 0) p.exponents[row * p.blocks + block] = static_cast<uint8_t>(b);
         }
         v = act_value<kAct>(v);
