@@ -239,17 +239,27 @@ __device__ __forceinline__ float a8_step(uint32_t b) {
   return __uint_as_float(b == 255u ? 0x7FFFFFFFu : (b - 6u) << 23);
 }
 
-// Codes of four values, the first in the low byte.  v * inv + 1.5 * 2^23
-// rounds v * inv (exact: inv is a power of two) to the nearest integer, ties to
-// even, and leaves it in the low bits of the sum in two's complement.
+// v * inv + 1.5 * 2^23 rounds v * inv (exact: inv is a power of two) to the
+// nearest integer, ties to even, and leaves it in the low bits of the sum in
+// two's complement.
+constexpr float kA8Magic = 12582912.0f;
+__device__ __forceinline__ float2 a8_round(float2 v, float inv) { return fma2(v, both(inv), both(kA8Magic)); }
+
+// Only a block whose largest magnitude is 127.5 steps and more (its fraction
+// bits are 0x7F0000 and up) rounds to 128 and has to be clamped.
+__device__ __forceinline__ bool a8_clamps(uint32_t mag) { return (mag & 0x7FFFFFu) >= 0x7F0000u; }
+__device__ __forceinline__ float2 a8_clamp(float2 r) {
+  return make_float2(fminf(fmaxf(r.x, kA8Magic - 127.0f), kA8Magic + 127.0f),
+                     fminf(fmaxf(r.y, kA8Magic - 127.0f), kA8Magic + 127.0f));
+}
+
+// The low bytes of four rounded values, the first lowest.
+__device__ __forceinline__ uint32_t a8_bytes(float2 a, float2 b) {
+  return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                     __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
+}
 __device__ __forceinline__ uint32_t a8_code4(float2 a, float2 b, float inv) {
-  constexpr float kMagic = 12582912.0f;
-  const float lo = kMagic - 127.0f, hi = kMagic + 127.0f;
-  a = fma2(a, both(inv), both(kMagic));
-  b = fma2(b, both(inv), both(kMagic));
-  const uint32_t i0 = __float_as_uint(fminf(fmaxf(a.x, lo), hi)), i1 = __float_as_uint(fminf(fmaxf(a.y, lo), hi));
-  const uint32_t i2 = __float_as_uint(fminf(fmaxf(b.x, lo), hi)), i3 = __float_as_uint(fminf(fmaxf(b.y, lo), hi));
-  return __byte_perm(__byte_perm(i0, i1, 0x0040), __byte_perm(i2, i3, 0x0040), 0x5410);
+  return a8_bytes(a8_clamp(a8_round(a, inv)), a8_clamp(a8_round(b, inv)));
 }
 
 // Values of four codes: the byte k + 128 under the exponent of 2^23 is the

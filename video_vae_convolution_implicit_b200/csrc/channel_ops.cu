@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
   using H = Val16<kBF16>;
   constexpr uint32_t kSlot = R * V * T * 16;
   // gamma and beta as fp32: in registers, or in shared memory behind the ring
-  // ([2][C] floats) where a thread holds more than two vectors
-  constexpr bool kRegParams = V <= 2;
+  // ([2][C] floats) where a thread holds more than three vectors
+  constexpr bool kRegParams = V <= 3;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[G > 32 ? 2 * (T / 32) * R : 1];
   int flip = 0;
@@ -548,10 +548,16 @@ __global__ void __launch_bounds__(1024) layernorm_param_kernel(const float* __re
   const int w = threadIdx.x >> 5;
   griddep_wait();
   float a = 0.0f;
-  if (col < 2 * C) {
-#pragma unroll 4
-    for (int b = w; b < blocks; b += 32) a += __ldcg(part + static_cast<size_t>(b) * 2 * C + col);
-  }
+  constexpr int kBatch = 10;   // loads in flight: all of a warp's 296 / 32
+  if (col < 2 * C)
+    for (int b = w; b < blocks; b += 32 * kBatch) {
+      float v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        v[k] = b + 32 * k < blocks ? __ldcg(part + static_cast<size_t>(b + 32 * k) * 2 * C + col) : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) a += v[k];
+    }
   s[w][threadIdx.x & 31] = a;
   __syncthreads();
   if (w == 0 && col < 2 * C) {
@@ -646,16 +652,23 @@ struct ReadParams {
   int units, C;
 };
 
-// unpack: out = act(v * gamma + beta); gradient (kGrad): out = dy * act'(v).
+// kPlain: out = act(v); kAffine: out = act(v * gamma + beta); kGrad: out = dy * act'(v).
 // Units of 8 channels here: the 16-bit side, two thirds and more of the bytes,
 // is then one contiguous 512-byte access a warp.
-template <bool kBF16, int kAct, bool kGrad>
-__global__ void __launch_bounds__(kThreads) act8_read_kernel(const ReadParams p) {
+enum class Read { kPlain, kAffine, kGrad };
+
+template <bool kBF16, int kAct, Read kMode>
+__global__ void __launch_bounds__(kThreads, kMode == Read::kGrad ? 3 : 4) act8_read_kernel(const ReadParams p) {
   using T = Val16<kBF16>;
+  constexpr bool kGrad = kMode == Read::kGrad;
   const long long stride = static_cast<long long>(gridDim.x) * kThreads;
   long long u = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
   UnitWalk w(u, stride, p.units);
   griddep_wait();
+  // gamma and beta of this thread's channels; the host makes the stride a
+  // multiple of a row where it can, and then they stay the same
+  float2 g[4], b[4];
+  int of = -1;
   for (; u < p.total; u += kUnroll * stride) {
     uint2 k[kUnroll];
     uint4 d[kUnroll];
@@ -681,26 +694,28 @@ __global__ void __launch_bounds__(kThreads) act8_read_kernel(const ReadParams p)
       a8_decode4(k[j].x, step, v);
       a8_decode4(k[j].y, step, v + 2);
       if constexpr (kGrad) {
-        float2 g[4];
-        T::unpack8(d[j], g);
+        float2 dy[4];
+        T::unpack8(d[j], dy);
         if constexpr (kAct != kActNone) {
           act_limit(v, step);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = mul2(g[e], act_slope<kAct>(v[e]));
+          for (int e = 0; e < 4; ++e) v[e] = mul2(dy[e], act_slope<kAct>(v[e]));
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = g[e];
+          for (int e = 0; e < 4; ++e) v[e] = dy[e];
         }
       } else {
-        if (p.gamma || p.beta) {
-          float2 g[4], b[4];
+        if constexpr (kMode == Read::kAffine) {
+          if (c[j] != of) {
+            of = c[j];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            g[e] = both(1.0f);
-            b[e] = both(0.0f);
+            for (int e = 0; e < 4; ++e) {
+              g[e] = both(1.0f);
+              b[e] = both(0.0f);
+            }
+            if (p.gamma) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma + of)), g);
+            if (p.beta) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta + of)), b);
           }
-          if (p.gamma) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma + c[j])), g);
-          if (p.beta) T::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta + c[j])), b);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = fma2(v[e], g[e], b[e]);
         }
@@ -776,7 +791,7 @@ cudaError_t run_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
   static std::atomic<unsigned long long> ready{0};
   auto kern = layernorm_fwd_kernel<kBF16, G, V, R, T, D, kOcc, kCkpt>;
   const unsigned blocks = blocks_for(p.rows, rows_per_step(G, R, T), static_cast<long long>(sms) * kOcc);
-  const size_t smem = static_cast<size_t>(D) * R * V * T * 16 + (V <= 2 ? 0 : 2 * p.C * sizeof(float));
+  const size_t smem = static_cast<size_t>(D) * R * V * T * 16 + (V <= 3 ? 0 : 2 * p.C * sizeof(float));
   const cudaError_t e = allow_smem(kern, ready, smem);
   if (e != cudaSuccess) return e;
   return launch(kern, blocks, T, smem, 1, stream, p);
@@ -789,11 +804,12 @@ cudaError_t dispatch_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
   if (vecs <= 8) return run_fwd<kBF16, 8, 1, 2, 256, 8, 3, kCkpt>(p, sms, stream);
   if (vecs <= 16) return run_fwd<kBF16, 8, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
   if (vecs <= 32) return run_fwd<kBF16, 16, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
-  if (vecs <= 64) return run_fwd<kBF16, 16, 4, 1, 256, 4, 3, kCkpt>(p, sms, stream);
-  if (vecs <= 128) return run_fwd<kBF16, 32, 4, 1, 256, 4, 3, kCkpt>(p, sms, stream);
-  if (vecs <= 256) return run_fwd<kBF16, 32, 8, 1, 128, 4, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 64) return run_fwd<kBF16, 32, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
+  if (vecs <= 96) return run_fwd<kBF16, 32, 3, 1, 256, 5, 2, kCkpt>(p, sms, stream);
+  if (vecs <= 128) return run_fwd<kBF16, 128, 1, 4, 128, 4, 5, kCkpt>(p, sms, stream);
+  if (vecs <= 256) return run_fwd<kBF16, 256, 1, 4, 256, 4, 2, kCkpt>(p, sms, stream);
   if (vecs <= 512) return run_fwd<kBF16, 256, 2, 1, 256, 8, 3, kCkpt>(p, sms, stream);
-  return run_fwd<kBF16, 256, 4, 1, 256, 4, 2, kCkpt>(p, sms, stream);
+  return run_fwd<kBF16, 512, 2, 1, 512, 8, 1, kCkpt>(p, sms, stream);
 }
 
 template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
@@ -817,9 +833,8 @@ unsigned bwd_blocks(long long rows, int C) {
                   : vecs <= 32 ? rows_per_step(16, 1, 256)
                   : vecs <= 64 ? rows_per_step(32, 1, 256)
                   : vecs <= 128 ? rows_per_step(32, 1, 128)
-                  : vecs <= 256 ? rows_per_step(256, 2, 256)
                                 : rows_per_step(256, 1, 256);
-  return blocks_for(rows, per, kLnBwdBlocks);
+  return blocks_for(rows, per, vecs > 128 && vecs <= 256 ? 2 * kLnBwdBlocks : kLnBwdBlocks);
 }
 
 template <bool kBF16, bool kCkpt>
@@ -829,17 +844,25 @@ cudaError_t dispatch_bwd(const LnBwdParams& p, unsigned blocks, cudaStream_t str
   if (vecs <= 16) return run_bwd<kBF16, 8, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
   if (vecs <= 32) return run_bwd<kBF16, 16, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
   if (vecs <= 64) return run_bwd<kBF16, 32, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 96) return run_bwd<kBF16, 32, 3, 1, 128, 4, 2, kCkpt>(p, blocks, stream);
   if (vecs <= 128) return run_bwd<kBF16, 32, 4, 1, 128, 3, 2, kCkpt>(p, blocks, stream);
-  if (vecs <= 256) return run_bwd<kBF16, 256, 1, 2, 256, 3, 2, kCkpt>(p, blocks, stream);
+  if (vecs <= 256) return run_bwd<kBF16, 128, 2, 1, 128, 4, 4, kCkpt>(p, blocks, stream);
   if (vecs <= 512) return run_bwd<kBF16, 256, 2, 1, 256, 4, 2, kCkpt>(p, blocks, stream);
   return run_bwd<kBF16, 256, 4, 1, 256, 4, 1, kCkpt>(p, blocks, stream);
 }
 
-template <bool kBF16, bool kGrad>
+template <bool kBF16, Read kMode>
 cudaError_t dispatch_read(int act, unsigned blocks, cudaStream_t stream, const ReadParams& p) {
-  if (act == kActSilu) return launch(act8_read_kernel<kBF16, kActSilu, kGrad>, blocks, kThreads, 0, 1, stream, p);
-  if (act == kActGelu) return launch(act8_read_kernel<kBF16, kActGelu, kGrad>, blocks, kThreads, 0, 1, stream, p);
-  return launch(act8_read_kernel<kBF16, kActNone, kGrad>, blocks, kThreads, 0, 1, stream, p);
+  if (act == kActSilu) return launch(act8_read_kernel<kBF16, kActSilu, kMode>, blocks, kThreads, 0, 1, stream, p);
+  if (act == kActGelu) return launch(act8_read_kernel<kBF16, kActGelu, kMode>, blocks, kThreads, 0, 1, stream, p);
+  return launch(act8_read_kernel<kBF16, kActNone, kMode>, blocks, kThreads, 0, 1, stream, p);
+}
+
+template <bool kBF16>
+cudaError_t dispatch_read(Read mode, int act, unsigned blocks, cudaStream_t stream, const ReadParams& p) {
+  if (mode == Read::kGrad) return dispatch_read<kBF16, Read::kGrad>(act, blocks, stream, p);
+  if (mode == Read::kAffine) return dispatch_read<kBF16, Read::kAffine>(act, blocks, stream, p);
+  return dispatch_read<kBF16, Read::kPlain>(act, blocks, stream, p);
 }
 
 constexpr int kMaxAct8Channels = 1 << 24;
@@ -1007,12 +1030,20 @@ static conv3d_status_t act8_read(const void* codes, const void* exponents, const
                static_cast<const uint16_t*>(gamma), static_cast<const uint16_t*>(beta),
                static_cast<const uint16_t*>(dy), static_cast<uint16_t*>(out), rows * units_per_row(C, 8),
                units_per_row(C, 8), C};
-  const unsigned blocks = blocks_for(p.total, kThreads * kUnroll, dev.num_sms * 8LL);
+  unsigned blocks = blocks_for(p.total, kThreads * kUnroll, dev.num_sms * 8LL);
+  if (gamma || beta) {   // whole rows per grid stride, so that a thread keeps its channels
+    unsigned a = kThreads, b = static_cast<unsigned>(p.units);
+    while (b != 0) {
+      const unsigned r = a % b;
+      a = b;
+      b = r;
+    }
+    const unsigned m = static_cast<unsigned>(p.units) / a;   // blocks that hold a whole number of rows
+    if (blocks > m) blocks -= blocks % m;
+  }
   const bool bf16 = dtype == CONV3D_BF16;
-  const cudaError_t e = grad ? (bf16 ? dispatch_read<true, true>(act, blocks, stream, p)
-                                     : dispatch_read<false, true>(act, blocks, stream, p))
-                             : (bf16 ? dispatch_read<true, false>(act, blocks, stream, p)
-                                     : dispatch_read<false, false>(act, blocks, stream, p));
+  const Read mode = grad ? Read::kGrad : gamma || beta ? Read::kAffine : Read::kPlain;
+  const cudaError_t e = bf16 ? dispatch_read<true>(mode, act, blocks, stream, p) : dispatch_read<false>(mode, act, blocks, stream, p);
   return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "checkpoint read launch");
 }
 

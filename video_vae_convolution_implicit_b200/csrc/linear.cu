@@ -17,7 +17,7 @@ namespace conv3d_linear {
 using namespace conv3d;
 using namespace conv3d_internal;
 
-constexpr int kReserve = 1024 + 8 * (2 * MAX_STAGES + 2 + 2 + 1 + 2 * kLinEpiWarps);   // alignment, barriers
+constexpr int kReserve = 1024 + 8 * (2 * MAX_STAGES + 2 + 2 + 1 + 1);   // alignment, barriers
 
 // One product: C [M, N] = A [M, K] B^T, B = w [N, K] (forward) or w^T with w [K, N] (gradient).
 struct Product {
@@ -37,6 +37,8 @@ struct Product {
 struct Plan {
   bool pair;
   int BN, split, stages;
+  bool resident;      // pair kernel: B's column tile stays in shared memory
+  int units;          // pair kernel: CTA pairs
   size_t smem;
 };
 
@@ -70,13 +72,31 @@ Plan choose(const Product& P, const Device& dev) {
   }
   if (L.pair) {
     L.split = 1;
-    const size_t stage = kLinABytes + static_cast<size_t>(L.BN / 2) * BK * 2;
     const bool q = P.codes != nullptr;
-    const size_t epi = kLinEpiWarps * 2 *
-                       (kLinOutBytes + (P.residual ? kLinOutBytes : 0) + (q ? kLinCodeBytes : 0));
+    const size_t epi = kLinEpiWarps * (kLinOutBytes + (q && (P.bwd || P.residual) ? kLinCodeBytes : 0) +
+                                       (P.bwd ? 0 : kLinBiasBytes));
     const size_t room = dev.max_smem_optin - 64 - kReserve - epi;
-    L.stages = static_cast<int>(room / stage < MAX_STAGES ? room / stage : MAX_STAGES);
-    L.smem = kReserve + epi + L.stages * stage;
+    const size_t b_bytes = static_cast<size_t>(L.BN / 2) * BK * 2;
+    const int tiles_n = (P.N + L.BN - 1) / L.BN;
+    const long long tiles = mt * tiles_n;
+    // B resident where it leaves at least two stages for A and the pairs, a
+    // multiple of the column tiles then, need at most a tenth more rounds
+    const long long units = pairs / tiles_n * tiles_n;
+    L.resident = false;
+    L.units = static_cast<int>(tiles < pairs ? tiles : pairs);
+    const char* env = getenv("CONV3D_LINEAR_RESIDENT");   // tuning and tests: 0 never, 1 wherever it fits
+    if (units > 0 && kblocks * b_bytes + 2 * kLinABytes <= room && (env == nullptr || env[0] != '0')) {
+      const long long rounds = (tiles + pairs - 1) / pairs, rounds_r = (tiles + units - 1) / units;
+      if (rounds_r * 10 <= rounds * 11 || (env != nullptr && env[0] == '1')) {
+        L.resident = true;
+        L.units = static_cast<int>(tiles < units ? tiles : units);
+      }
+    }
+    const size_t stage = kLinABytes + (L.resident ? 0 : b_bytes);
+    const size_t fixed = L.resident ? kblocks * b_bytes : 0;
+    const size_t fit = (room - fixed) / stage;
+    L.stages = static_cast<int>(fit < MAX_STAGES ? fit : MAX_STAGES);
+    L.smem = kReserve + epi + fixed + L.stages * stage;
     return L;
   }
   L.BN = 16;
@@ -125,6 +145,7 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
   p.kblocks = (P.K + BK - 1) / BK;
   p.BN = L.BN;
   p.split = L.split;
+  p.resident = L.resident ? 1 : 0;
   p.stages = L.stages;
   p.bias = static_cast<const uint16_t*>(P.bias);
   p.residual = static_cast<const uint16_t*>(P.residual);
@@ -132,31 +153,19 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
   p.codes = static_cast<uint8_t*>(P.codes);
   p.exponents = static_cast<uint8_t*>(P.exponents);
   p.blocks = (P.N + 31) / 32;
-  p.has_aux = P.residual != nullptr;
   p.status = dev.status;
   p.timeout_ns = wait_limit_ns();
   p.test_stall = take_stall(p.timeout_ns) ? 1 : 0;
   CUtensorMap map_a, map_w;
   if (plan_log())
     fprintf(stderr, "libconv3d: channel product %s %s, %d x %d x %d, tiles of %d, %d pieces, %d stages, %zu B shared\n",
-            kBwd ? "gradient" : "forward", L.pair ? "CTA pair" : "few rows", P.M, P.N, P.K, L.BN, L.split, L.stages,
+            kBwd ? "gradient" : "forward", L.resident ? "CTA pair, resident weight" : L.pair ? "CTA pair" : "few rows", P.M, P.N, P.K, L.BN, L.split, L.stages,
             L.smem);
   if (L.pair) {
     if ((st = encode_matrix(map_a, dt, P.a, K, M, K * 2, BK, BM, sw, "rows")) != CONV3D_OK) return st;
     st = kBwd ? encode_matrix(map_w, dt, P.w, N, K, N * 2, 64, BK, sw, "weight")
               : encode_matrix(map_w, dt, P.w, K, N, K * 2, BK, L.BN / 2, sw, "weight");
     if (st != CONV3D_OK) return st;
-    CUtensorMap map_out, map_aux, map_codes;
-    if ((st = encode_matrix(map_out, dt, P.out, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B, "output")) != CONV3D_OK)
-      return st;
-    map_aux = map_codes = map_out;   // not read unless replaced below
-    if (P.residual && (st = encode_matrix(map_aux, dt, P.residual, N, M, N * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B,
-                                          "residual")) != CONV3D_OK)
-      return st;
-    const unsigned long long cols = static_cast<unsigned long long>(p.blocks) * 32;
-    if (kQ && (st = encode_matrix(map_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, P.codes, cols, M, cols, 32, 32,
-                                  CU_TENSOR_MAP_SWIZZLE_32B, "codes")) != CONV3D_OK)
-      return st;
     p.tiles_n = (P.N + L.BN - 1) / L.BN;
     const long long tiles = static_cast<long long>(p.tiles_n) * ((P.M + 2 * BM - 1) / (2 * BM));
     if (tiles > INT_MAX / 2) {
@@ -169,9 +178,8 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
     static std::atomic<unsigned long long> ready{0};
     auto kern = linear_pair_kernel<kBF16, kBwd, kAct, kQ>;
     if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
-    const int pairs = dev.num_sms / 2;
-    const unsigned grid = 2u * static_cast<unsigned>(p.num_tiles < pairs ? p.num_tiles : pairs);
-    const cudaError_t e = launch(kern, grid, kLinThreads, L.smem, 2, stream, map_a, map_w, map_out, map_aux, map_codes, p);
+    const unsigned grid = 2u * static_cast<unsigned>(L.units);
+    const cudaError_t e = launch(kern, grid, kLinThreads, L.smem, 2, stream, map_a, map_w, p);
     return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "channel product launch");
   }
   st = kBwd ? encode_matrix(map_w, dt, P.w, N, K, N * 2, 64, BK, sw, "weight")

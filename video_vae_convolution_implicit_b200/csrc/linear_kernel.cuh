@@ -13,9 +13,16 @@
 //
 // linear_pair_kernel (many rows): persistent CTA pairs over tiles of 256 rows x
 // BN columns, warp-specialised as the convolution is -- TMA producer, one
-// tcgen05.mma issuer (cta_group::2), and 8 epilogue warps over two TMEM
-// accumulators -- since at 8 k-blocks a tile the epilogue has about as many
-// issue slots to spend as the tensor cores take for the tile.  Columns are the
+// tcgen05.mma issuer (cta_group::2), and epilogue warps over two TMEM
+// accumulators.  At 8 k-blocks a tile the epilogue has about as many issue slots
+// to spend as the tensor cores take for the tile (some 14 instructions a value
+// with GELU and the checkpoint), and a chunk is a long chain of dependent steps
+// (TMEM load, arithmetic, staging, fence, store): 16 warps, four to a scheduler,
+// hide it where 8 left two thirds of the slots empty.  The chunks go out by plain
+// stores through a swizzled buffer of the warp's own, and the residual and the
+// codes come in by cp.async, 16 bytes a thread: as TMA boxes of 32 x 32 values
+// they took 220 cycles each whatever their bytes, 7000 cycles a tile (measured
+// on B200, 512 -> 2048 on 36864 rows: the epilogue alone 63 us, the products 58).  Columns are the
 // fast tile index, so the tiles in flight share rows of A and A is read from
 // HBM about once; w stays in L2.
 //
@@ -33,12 +40,13 @@
 
 namespace conv3d {
 
-constexpr int kLinEpiWarps = 8;
+constexpr int kLinEpiWarps = 16;
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;   // producer, issuer, epilogue
 constexpr int kLinRowsThreads = 64 + 32 * 4;
 constexpr uint32_t kLinABytes = BM * BK * 2;           // one CTA's A rows of a k-block
 constexpr uint32_t kLinOutBytes = 32 * 32 * 2;         // a 32 x 32 chunk of 16-bit values
 constexpr uint32_t kLinCodeBytes = 32 * 32;            // the same chunk's codes
+constexpr uint32_t kLinBiasBytes = 64 * 4;             // the biases of a warp's (at most two) chunks
 
 struct LinearParams {
   int M, N;                 // rows and columns of the result
@@ -46,16 +54,16 @@ struct LinearParams {
   int BN;                   // columns per tile (pair) / rows per tile (rows kernel)
   int tiles_n, num_tiles;
   int split;                // CTAs per cluster along the contraction (rows kernel)
+  int resident;             // pair kernel: the CTA keeps its half of B's column tile in shared memory
   int stages;
   uint32_t tmem_cols;
   uint32_t idesc;
   const uint16_t* bias;     // [N] or null
-  const uint16_t* residual; // rows kernel; the pair kernel reads it through map_aux
-  uint16_t* out;            // rows kernel
-  uint8_t* codes;           // rows kernel: written (forward) or read (gradient)
-  uint8_t* exponents;       // written or read, [M][blocks]
+  const uint16_t* residual; // [M][N] or null
+  uint16_t* out;            // [M][N]
+  uint8_t* codes;           // written (forward) or read (gradient), [M][32 * blocks], or null
+  uint8_t* exponents;       // the same, [M][blocks]
   int blocks;               // ceil(N / 32)
-  int has_aux;              // forward: a residual is added
   int* status;
   unsigned long long timeout_ns;
   int test_stall;           // failure-detection test: the first stage's copies are skipped
@@ -76,11 +84,19 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "r"(r)
       : "memory");
 }
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c, int r) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(src), "r"(c), "r"(r)
-               : "memory");
+// Asynchronous 16-byte copy global -> shared and its group bookkeeping.
+__device__ __forceinline__ void lin_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void lin_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void lin_copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Arrive on an mbarrier of either CTA of the pair without ordering this
+// thread's memory operations: a release at cluster scope waits until its global
+// stores have been performed, a microsecond and more at every tile.  What it
+// signals, that tensor memory has been read, is complete by tcgen05.wait::ld.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 // MN-major operand in 64-element x 8-row atoms with the 128-byte swizzle:
@@ -105,14 +121,19 @@ __device__ __forceinline__ uint32_t swz32(uint32_t r, uint32_t h) { return r * 3
 
 // kBwd: the gradient (B MN-major, no bias; the chunk is multiplied by
 // act'(checkpoint) when kQ).  Forward: kQ writes the checkpoint.  Shared
-// memory: A ring, B ring, then per epilogue warp two output buffers, two
-// residual buffers (forward with a residual) and two code buffers (kQ), then
-// the barriers.
+// memory: A ring, B ring (or the whole column tile of B), then per epilogue warp
+// an output buffer, a code buffer (kQ, where it cannot share) and 64 fp32
+// biases, then the barriers.
+//
+// Resident B: with a short contraction (K <= 512 at BN = 256) a CTA's half of the
+// column tile fits beside the A ring.  A pair then stays with its columns and
+// loads only A, which halves what each tile draws from L2: with both operands
+// streamed that traffic and the stores of a short-K tile together outlast the
+// products.
 template <bool kBF16, bool kBwd, int kAct, bool kQ>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                       const __grid_constant__ CUtensorMap map_out, const __grid_constant__ CUtensorMap map_aux,
-                       const __grid_constant__ CUtensorMap map_codes, const LinearParams p) {
+                       const LinearParams p) {
   using T = Val16<kBF16>;
   extern __shared__ uint8_t lin_smem[];
   __shared__ uint32_t s_tmem_base;
@@ -130,18 +151,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t b_rows = static_cast<uint32_t>(p.BN) / 2;      // this CTA's half of B
   const uint32_t b_bytes = b_rows * BK * 2;
   const uint32_t a_ring = base;
-  const uint32_t b_ring = a_ring + p.stages * kLinABytes;
-  const uint32_t out_buf = b_ring + p.stages * b_bytes;
-  const uint32_t aux_buf = out_buf + kLinEpiWarps * 2 * kLinOutBytes;
-  const bool has_res = !kBwd && p.has_aux != 0;
-  const uint32_t code_buf = aux_buf + (has_res ? kLinEpiWarps * 2 * kLinOutBytes : 0);
-  const uint32_t bars = code_buf + (kQ ? kLinEpiWarps * 2 * kLinCodeBytes : 0);
+  const uint32_t b_ring = a_ring + p.stages * kLinABytes;      // or the whole half tile, by k-block
+  const uint32_t out_buf = b_ring + (p.resident ? p.kblocks : p.stages) * b_bytes;
+  const bool has_res = !kBwd && p.residual != nullptr;
+  // codes: a buffer of their own where the other is taken when they are staged
+  const bool own_codes = kQ && (kBwd || has_res);
+  const uint32_t code_buf = own_codes ? out_buf + kLinEpiWarps * kLinOutBytes : out_buf;
+  const uint32_t code_step = own_codes ? kLinCodeBytes : kLinOutBytes;
+  const uint32_t bias_buf = out_buf + kLinEpiWarps * (kLinOutBytes + (own_codes ? kLinCodeBytes : 0));
+  const uint32_t bars = bias_buf + (kBwd ? 0 : kLinEpiWarps * kLinBiasBytes);
   const uint32_t full_bar = bars;
   const uint32_t empty_bar = full_bar + 8 * p.stages;
   const uint32_t tfull_bar = empty_bar + 8 * p.stages;
   const uint32_t tempty_bar = tfull_bar + 16;
   const uint32_t drain_bar = tempty_bar + 16;
-  const uint32_t lfull_bar = drain_bar + 8;                     // [epilogue warp][2]: loads of the epilogue
+  const uint32_t bfull_bar = drain_bar + 8;                     // the resident tile of B has landed
 
   SharedCtl ctl{&s_abort, p.status, p.timeout_ns, mapa_shared(smem_addr(const_cast<int*>(&s_abort)), rank ^ 1u)};
   const uint32_t peer_bar = smem_addr(&s_peer_bar);
@@ -158,14 +182,11 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       mbar_init(tempty_bar + 8 * a, kLinEpiWarps * 2);
     }
     mbar_init(drain_bar, 1);
+    mbar_init(bfull_bar, 1);
     mbar_init(peer_bar, 1);
-    for (int e = 0; e < 2 * kLinEpiWarps; ++e) mbar_init(lfull_bar + 8 * e, 1);
     fence_mbar_init();
     prefetch_tensormap(&map_a);
     prefetch_tensormap(&map_b);
-    prefetch_tensormap(&map_out);
-    if (has_res) prefetch_tensormap(&map_aux);
-    if (kQ) prefetch_tensormap(&map_codes);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_addr(&s_tmem_base), p.tmem_cols);
@@ -181,11 +202,26 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const uint32_t tx_bytes = 2 * (kLinABytes + b_bytes);
+      const uint32_t half_bytes = kLinABytes + (p.resident ? 0u : b_bytes);   // this CTA's share of a stage
       const bool stall = p.test_stall != 0;
       uint32_t stage = 0, phase = 0;
       long long issued = 0;
       bool ok = true;
+      auto load_b = [&](uint32_t dst, uint32_t bar, int kb, int col0) {
+        if constexpr (kBwd) {
+          for (uint32_t i = 0; i < b_rows / 64; ++i)
+            tma_load_2d_pair(dst + i * kMnBlockBytes, &map_b, bar, col0 + static_cast<int>(i) * 64, kb * BK);
+        } else {
+          tma_load_2d_pair(dst, &map_b, bar, kb * BK, col0);
+        }
+      };
+      if (p.resident) {
+        // every tile of this pair has the same columns (the number of pairs is
+        // a multiple of the column tiles): their B is loaded once
+        const int col0 = (unit % p.tiles_n) * p.BN + static_cast<int>(rank * b_rows);
+        if (leader) mbar_arrive_expect_tx(bfull_bar, 2 * p.kblocks * b_bytes);
+        for (int kb = 0; kb < p.kblocks; ++kb) load_b(b_ring + kb * b_bytes, mapa_shared(bfull_bar, 0), kb, col0);
+      }
       for (int t = unit; ok && t < p.num_tiles; t += num_units) {
         const int mt = t / p.tiles_n;
         const int row0 = mt * 2 * BM + static_cast<int>(rank) * BM;
@@ -198,16 +234,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           const uint32_t fb = full_bar + 8 * stage;
           if (!(stall && issued == 0)) {
             // rows past M, columns past N and the contraction's end read as zero
-            if (leader) mbar_arrive_expect_tx(fb, tx_bytes);
+            if (leader) mbar_arrive_expect_tx(fb, 2 * half_bytes);
             const uint32_t fb_leader = mapa_shared(fb, 0);
             tma_load_2d_pair(a_ring + stage * kLinABytes, &map_a, fb_leader, kb * BK, row0);
-            if constexpr (kBwd) {
-              for (uint32_t i = 0; i < b_rows / 64; ++i)
-                tma_load_2d_pair(b_ring + stage * b_bytes + i * kMnBlockBytes, &map_b, fb_leader,
-                                 col0 + static_cast<int>(i) * 64, kb * BK);
-            } else {
-              tma_load_2d_pair(b_ring + stage * b_bytes, &map_b, fb_leader, kb * BK, col0);
-            }
+            if (!p.resident) load_b(b_ring + stage * b_bytes, fb_leader, kb, col0);
           }
           ++issued;
           if (++stage == static_cast<uint32_t>(p.stages)) {
@@ -216,14 +246,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
       }
-      producer_finish<true>(!ok, issued, stall, p.stages, full_bar, kLinABytes + b_bytes, peer_count, peer_bar, ctl,
-                            leader);
+      producer_finish<true>(!ok, issued, stall, p.stages, full_bar, half_bytes, peer_count, peer_bar, ctl, leader);
+      // after an abort: B's copies, both CTAs', complete on the leader's barrier
+      if (!ok && p.resident && leader) wait_bounded(bfull_bar, 0, ctl, false);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
       uint32_t stage = 0, phase = 0;
-      bool ok = true;
+      bool ok = !p.resident || wait_bounded(bfull_bar, 0, ctl, true);
       int local = 0;
       for (int t = unit; ok && t < p.num_tiles; t += num_units, ++local) {
         const uint32_t acc = local & 1;
@@ -237,8 +268,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
           tc_fence_after();
           const uint64_t da = smem_desc_k_sw128(a_ring + stage * kLinABytes);
-          const uint64_t db = kBwd ? lin_desc_mn(b_ring + stage * b_bytes, kMnBlockBytes)
-                                   : smem_desc_k_sw128(b_ring + stage * b_bytes);
+          const uint32_t b_at = b_ring + (p.resident ? static_cast<uint32_t>(kb) : stage) * b_bytes;
+          const uint64_t db = kBwd ? lin_desc_mn(b_at, kMnBlockBytes) : smem_desc_k_sw128(b_at);
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k)   // 16 values along the contraction: 32 bytes of a K-major row, 16 rows of an MN-major block
             mma_f16_ss_pair(d_tmem, da + 2 * k, db + (kBwd ? (2048 >> 4) : 2) * k, p.idesc, (kb | k) != 0);
@@ -258,181 +289,200 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ epilogue
-    // Two warps share each quarter of the TMEM lanes (32 rows of the tile) and
-    // take half of its columns each, 32 at a time: one row and one checkpoint
-    // block per thread, so the block's exponent needs no exchange.
+    // Four warps share each quarter of the TMEM lanes (32 rows of the tile) and
+    // take a quarter of its columns each, 32 at a time: one row and one
+    // checkpoint block per thread, so the block's exponent needs no exchange.
     const uint32_t quarter = warp & 3;
     const uint32_t ew = warp - 2;
-    const int half = static_cast<int>(ew) / 4;
-    const int nj = p.BN / 64;                                  // chunks per warp and tile
-    const uint32_t obuf = out_buf + ew * 2 * kLinOutBytes;
-    const uint32_t abuf = aux_buf + ew * 2 * kLinOutBytes;
-    const uint32_t cbuf = code_buf + ew * 2 * kLinCodeBytes;
-    const uint32_t lbar = lfull_bar + ew * 16;
+    const int share = static_cast<int>(ew) / 4;
+    const int nj = p.BN / 128;                                 // chunks per warp and tile
+    const uint32_t ob = out_buf + ew * kLinOutBytes;
+    const uint32_t cb = code_buf + ew * code_step;
+    const uint32_t bb = bias_buf + ew * kLinBiasBytes;
+    // this lane's 16 bytes of a chunk's rows in the row-contiguous order of
+    // global memory: four lanes a 64-byte row of values, two a 32-byte row of codes
+    const int vrow = static_cast<int>(lane >> 2), vpart = static_cast<int>(lane & 3);
+    const int crow = static_cast<int>(lane >> 1), cpart = static_cast<int>(lane & 1);
     constexpr bool kLoadCodes = kBwd && kQ;
     const bool loads = has_res || kLoadCodes;
-    const uint4* bias4 = reinterpret_cast<const uint4*>(p.bias);
-    uint32_t out_no = 0;          // chunks stored so far: buffer out_no & 1
-    uint32_t load_no = 0;         // chunks whose load was waited for: buffer load_no & 1
-    uint32_t asked_no = 0;        // chunks whose load was issued
-    bool ok = true;
-    int local = 0;
-    for (int t = unit; ok && t < p.num_tiles; t += num_units, ++local) {
-      const uint32_t acc = local & 1;
+    // where this warp's rows and columns of a tile begin, and how many of its
+    // chunks hold part of the result
+    auto place = [&](int t, int& row0, int& col0) {
       const int mt = t / p.tiles_n;
-      const int row0 = mt * 2 * BM + static_cast<int>(rank) * BM + static_cast<int>(quarter) * 32;
-      const int col0 = (t - mt * p.tiles_n) * p.BN + half * nj * 32;
-      const int row = row0 + static_cast<int>(lane);
-      int live = (p.N - col0 + 31) / 32;                        // chunks with a column of the result
-      live = live < 0 ? 0 : live > nj ? nj : live;
-      if (row0 >= p.M) live = 0;
-      auto ask = [&](int j) {                                   // lane 0: load chunk j's residual or codes
-        const uint32_t b = asked_no & 1;
-        if constexpr (kLoadCodes) {
-          mbar_arrive_expect_tx(lbar + 8 * b, kLinCodeBytes);
-          tma_load_2d(cbuf + b * kLinCodeBytes, &map_codes, lbar + 8 * b, col0 + 32 * j, row0);
-        } else {
-          mbar_arrive_expect_tx(lbar + 8 * b, kLinOutBytes);
-          tma_load_2d(abuf + b * kLinOutBytes, &map_aux, lbar + 8 * b, col0 + 32 * j, row0);
+      row0 = mt * 2 * BM + static_cast<int>(rank) * BM + static_cast<int>(quarter) * 32;
+      col0 = (t - mt * p.tiles_n) * p.BN + share * nj * 32;
+      const int live = (p.N - col0 + 31) / 32;
+      return row0 >= p.M || live < 0 ? 0 : live > nj ? nj : live;
+    };
+    // The residual or the codes of the warp's next chunk are always under way:
+    // the load is issued when the buffer is free (the residual's is the output
+    // buffer, in which the sum replaces it), for the next live chunk, of this tile
+    // or a later one (next_t, next_j), and a chunk's exponent byte is fetched
+    // with it.
+    int next_t = unit, next_j = 0;
+    uint32_t next_eb = 0;
+    auto ask = [&]() {
+      int row0, col0;
+      while (next_t < p.num_tiles && next_j >= place(next_t, row0, col0)) {
+        next_t += num_units;
+        next_j = 0;
+      }
+      if (next_t >= p.num_tiles) return;
+      const int col = col0 + 32 * next_j;
+      if constexpr (kLoadCodes) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = crow + 16 * i;
+          if (row0 + r < p.M)
+            lin_copy16(cb + swz32(r, cpart),
+                       p.codes + (static_cast<size_t>(row0 + r) * p.blocks + col / 32) * 32 + cpart * 16);
         }
-      };
-      if (loads)
-        for (int j = 0; j < 2 && j < live; ++j) {
-          if (lane == 0) ask(j);
-          ++asked_no;
-        }
-      // gradient: this row's exponent bytes; forward: collected here, stored at the end
-      uint32_t eb4 = 0;
-      uint8_t* erow = p.exponents + static_cast<size_t>(row) * p.blocks + col0 / 32;
-      const bool word = nj == 4 && (p.blocks & 3) == 0;         // col0 / 32 is a multiple of 4 then
-      if (kLoadCodes && live > 0 && row < p.M) {
-        if (word) {
-          eb4 = __ldg(reinterpret_cast<const uint32_t*>(erow));
-        } else {
-          for (int j = 0; j < live; ++j) eb4 |= static_cast<uint32_t>(__ldg(erow + j)) << (8 * j);
+      } else if (col + vpart * 8 < p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = vrow + 8 * i;
+          if (row0 + r < p.M)
+            lin_copy16(ob + swz64(r, vpart), p.residual + static_cast<size_t>(row0 + r) * p.N + col + vpart * 8);
         }
       }
-      if (!wait_bounded(tfull_bar + 8 * acc, (local >> 1) & 1, ctl, true)) {
-        ok = false;
-      } else {
-        tc_fence_after();
-        const uint32_t t_row =
-            tmem_base + ((quarter * 32u) << 16) + acc * static_cast<uint32_t>(p.BN) + half * nj * 32;
-        for (int j = 0; j < live; ++j) {
-          const int col = col0 + 32 * j;
-          uint32_t raw[32];
-          tmem_ld_32x32b_x32(t_row + j * 32, raw);
-          float2 v[16];
-          if constexpr (kLoadCodes) {
-            const uint32_t b = load_no & 1;
-            if (!wait_bounded(lbar + 8 * b, (load_no >> 1) & 1, ctl, true)) {
-              ok = false;
-              tmem_ld_wait();
-              break;
-            }
-            ++load_no;
-            const float step = a8_step((eb4 >> (8 * j)) & 0xFFu);
-            const uint4 k0 = ld_shared_v4(cbuf + b * kLinCodeBytes + swz32(lane, 0));
-            const uint4 k1 = ld_shared_v4(cbuf + b * kLinCodeBytes + swz32(lane, 1));
-            a8_decode4(k0.x, step, v); a8_decode4(k0.y, step, v + 2);
-            a8_decode4(k0.z, step, v + 4); a8_decode4(k0.w, step, v + 6);
-            a8_decode4(k1.x, step, v + 8); a8_decode4(k1.y, step, v + 10);
-            a8_decode4(k1.z, step, v + 12); a8_decode4(k1.w, step, v + 14);
+      lin_copy_commit();
+      if constexpr (kLoadCodes) {
+        const int row = row0 + static_cast<int>(lane);
+        next_eb = row < p.M ? __ldg(p.exponents + static_cast<size_t>(row) * p.blocks + col / 32) : 0u;
+      }
+      ++next_j;
+    };
+    if (loads) ask();
+    int local = 0;
+    int bias_col = -1;
+    for (int t = unit; t < p.num_tiles; t += num_units, ++local) {
+      const uint32_t acc = local & 1;
+      int row0, col0;
+      const int live = place(t, row0, col0);
+      const int row = row0 + static_cast<int>(lane);
+      if (!kBwd && bias_col != col0 && live > 0) {              // this warp's biases, as fp32
+        bias_col = col0;
+        for (int c = static_cast<int>(lane); c < nj * 32; c += 32) {
+          const float v = p.bias != nullptr && col0 + c < p.N ? T::lo(__ldg(p.bias + col0 + c)) : 0.0f;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(bb + c * 4u), "f"(v) : "memory");
+        }
+        __syncwarp();
+      }
+      if (!wait_bounded(tfull_bar + 8 * acc, (local >> 1) & 1, ctl, true)) break;
+      tc_fence_after();
+      const uint32_t t_row =
+          tmem_base + ((quarter * 32u) << 16) + acc * static_cast<uint32_t>(p.BN) + share * nj * 32;
+      // this warp has read its part of the accumulator: the next products may have it
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar + 8 * acc, 0));
+      };
+      if (live == 0) release();
+      for (int j = 0; j < live; ++j) {
+        const int col = col0 + 32 * j;
+        uint32_t raw[32];
+        tmem_ld_32x32b_x32(t_row + j * 32, raw);
+        uint32_t packed[16];
+        if constexpr (kLoadCodes) {
+          lin_copy_wait();
+          __syncwarp();
+          const float step = a8_step(next_eb);
+          const uint4 k0 = ld_shared_v4(cb + swz32(lane, 0));
+          const uint4 k1 = ld_shared_v4(cb + swz32(lane, 1));
+          __syncwarp();
+          ask();
+          const uint32_t k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+          tmem_ld_wait();
+          if (j + 1 == live) release();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float2 v[4];
+            a8_decode4(k[2 * g], step, v);
+            a8_decode4(k[2 * g + 1], step, v + 2);
             act_limit(v, step);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = act_slope<kAct>(v[e]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              v[e] = mul2(v[e], make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1])));
-          } else {
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1]));
+            for (int e = 0; e < 4; ++e) {
+              v[e] = mul2(act_slope<kAct>(v[e]), make_float2(__uint_as_float(raw[8 * g + 2 * e]),
+                                                             __uint_as_float(raw[8 * g + 2 * e + 1])));
+              packed[4 * g + e] = T::pack(v[e].x, v[e].y);
+            }
           }
-          if (!kBwd && bias4 != nullptr) {
+        } else {
+          tmem_ld_wait();
+          if (j + 1 == live) release();
+          float2 v[16];
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (col + 8 * g < p.N) {
-                float2 f[4];
-                T::unpack8(__ldg(bias4 + col / 8 + g), f);
+          for (int e = 0; e < 16; ++e) v[e] = make_float2(__uint_as_float(raw[2 * e]), __uint_as_float(raw[2 * e + 1]));
+          if constexpr (!kBwd) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[4 * g + e] = add2(v[4 * g + e], f[e]);
-              }
+            for (int g = 0; g < 8; ++g) {
+              const uint4 b = ld_shared_v4(bb + (j * 32 + g * 4) * 4u);
+              v[2 * g] = add2(v[2 * g], make_float2(__uint_as_float(b.x), __uint_as_float(b.y)));
+              v[2 * g + 1] = add2(v[2 * g + 1], make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
+            }
           }
-          const uint32_t ob = obuf + (out_no & 1) * kLinOutBytes;
-          const uint32_t cb = cbuf + (out_no & 1) * kLinCodeBytes;
-          // the stores issued from these buffers two chunks ago must have read them
-          if (lane == 0) bulk_wait_group_read<1>();
-          __syncwarp();
           if constexpr (!kBwd && kQ) {
             float m = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) m = a8_max(a8_max(m, v[e].x), v[e].y);
-            const uint32_t eb = a8_exponent(__float_as_uint(m));
+            const uint32_t mag = __float_as_uint(m);
+            const uint32_t eb = a8_exponent(mag);
             const float inv = a8_inv_step(eb);
-            eb4 |= eb << (8 * j);
+            uint32_t q[8];
+            if (a8_clamps(mag)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              st_shared_v4(cb + swz32(lane, h), a8_code4(v[8 * h], v[8 * h + 1], inv),
-                           a8_code4(v[8 * h + 2], v[8 * h + 3], inv), a8_code4(v[8 * h + 4], v[8 * h + 5], inv),
-                           a8_code4(v[8 * h + 6], v[8 * h + 7], inv));
+              for (int e = 0; e < 8; ++e) q[e] = a8_code4(v[2 * e], v[2 * e + 1], inv);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) q[e] = a8_bytes(a8_round(v[2 * e], inv), a8_round(v[2 * e + 1], inv));
+            }
+            st_shared_v4(cb + swz32(lane, 0), q[0], q[1], q[2], q[3]);
+            st_shared_v4(cb + swz32(lane, 1), q[4], q[5], q[6], q[7]);
+            __syncwarp();
+            uint8_t* dst = p.codes + (static_cast<size_t>(row0 + crow) * p.blocks + col / 32) * 32 + cpart * 16;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (row0 + crow + 16 * i < p.M)
+                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(16 * i) * p.blocks * 32) =
+                    ld_shared_v4(cb + swz32(crow + 16 * i, cpart));
+            __syncwarp();
+            if (row < p.M) p.exponents[static_cast<size_t>(row) * p.blocks + col / 32] = static_cast<uint8_t>(eb);
           }
           if constexpr (!kBwd && kAct != kActNone) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = act_value<kAct>(v[e]);
           }
           if (has_res) {
-            const uint32_t b = load_no & 1;
-            if (!wait_bounded(lbar + 8 * b, (load_no >> 1) & 1, ctl, true)) {
-              ok = false;
-              break;
-            }
-            ++load_no;
+            lin_copy_wait();
+            __syncwarp();
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               float2 f[4];
-              T::unpack8(ld_shared_v4(abuf + b * kLinOutBytes + swz64(lane, g)), f);
+              T::unpack8(ld_shared_v4(ob + swz64(lane, g)), f);
 #pragma unroll
               for (int e = 0; e < 4; ++e) v[4 * g + e] = add2(v[4 * g + e], f[e]);
             }
           }
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            st_shared_v4(ob + swz64(lane, g), T::pack(v[4 * g].x, v[4 * g].y), T::pack(v[4 * g + 1].x, v[4 * g + 1].y),
-                         T::pack(v[4 * g + 2].x, v[4 * g + 2].y), T::pack(v[4 * g + 3].x, v[4 * g + 3].y));
-          fence_proxy_async_shared();
-          __syncwarp();   // the chunk is staged, and every lane has read its load buffer
-          if (lane == 0) {
-            tma_store_2d(&map_out, ob, col, row0);              // clips rows past M and columns past N
-            if constexpr (!kBwd && kQ) tma_store_2d(&map_codes, cb, col, row0);
-            bulk_commit_group();
-            if (loads && j + 2 < live) ask(j + 2);
-          }
-          if (loads && j + 2 < live) ++asked_no;
-          ++out_no;
+          for (int e = 0; e < 16; ++e) packed[e] = T::pack(v[e].x, v[e].y);
         }
-        if (!kBwd && kQ && ok && live > 0 && row < p.M) {
-          if (word) {
-            *reinterpret_cast<uint32_t*>(erow) = eb4;
-          } else {
-            for (int j = 0; j < live; ++j) erow[j] = static_cast<uint8_t>(eb4 >> (8 * j));
-          }
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          st_shared_v4(ob + swz64(lane, g), packed[4 * g], packed[4 * g + 1], packed[4 * g + 2], packed[4 * g + 3]);
+        __syncwarp();
+        if (col + vpart * 8 < p.N) {
+          uint16_t* dst = p.out + static_cast<size_t>(row0 + vrow) * p.N + col + vpart * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row0 + vrow + 8 * i < p.M)
+              *reinterpret_cast<uint4*>(dst + static_cast<size_t>(8 * i) * p.N) = ld_shared_v4(ob + swz64(vrow + 8 * i, vpart));
         }
+        __syncwarp();   // the buffer is free again
+        if (has_res) ask();
       }
-      if (!ok) {
-        // loads still in flight must land before exit
-        if (lane == 0)
-          for (; load_no != asked_no; ++load_no)
-            wait_bounded(lbar + 8 * (load_no & 1), (load_no >> 1) & 1, ctl, false);
-        break;
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty_bar + 8 * acc, 0));
     }
-    if (lane == 0) bulk_wait_group_all();
-    __syncwarp();
+    lin_copy_wait();
   }
 
   // ------------------------------------------------------------ teardown
@@ -625,7 +675,7 @@ __global__ void __launch_bounds__(kLinRowsThreads)
           if (lane == 0) p.exponents[row * p.blocks + block] = static_cast<uint8_t>(b);
         }
         v = act_value<kAct>(v);
-        if (p.has_aux && live) v += T::lo(p.residual[row * p.N + ch]);
+        if (p.residual != nullptr && live) v += T::lo(p.residual[row * p.N + ch]);
       }
       if (live) p.out[row * p.N + ch] = static_cast<uint16_t>(T::pack(v, 0.0f) & 0xFFFFu);
     }
