@@ -163,19 +163,21 @@ __device__ __forceinline__ float2 act_value(float2 v) {
   }
 }
 
+// The derivative in terms of h = v/2, which the checkpoint's values are decoded
+// to (half the step): with q = t^2 - 1,
+//   silu'(v) = (1 + t)/2 - (h/2) q,                      t = tanh(h)
+//   gelu'(v) = (1 + t)/2 - h (a + 12 c h^2) q,           t = tanh(h (2a + 8 c h^2)),
+// a = sqrt(2/pi), c = 0.044715 a.
 template <int kAct>
-__device__ __forceinline__ float2 act_slope(float2 v) {
+__device__ __forceinline__ float2 act_slope_of_half(float2 h) {
   if constexpr (kAct == kActSilu) {
-    const float2 t = tanh_hw2(mul2(both(0.5f), v));
-    const float2 c = mul2(both(0.25f), v);
-    const float2 n = mul2(t, both(-1.0f));
-    return fma2(c, fma2(n, t, both(1.0f)), fma2(both(0.5f), t, both(0.5f)));
+    const float2 t = tanh_hw2(h);
+    return fma2(mul2(h, both(-0.5f)), fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
   } else if constexpr (kAct == kActGelu) {
-    const float2 v2 = mul2(v, v);
-    const float2 t = tanh_hw2(mul2(v, fma2(both(kGeluC), v2, both(kGeluA))));
-    const float2 c = mul2(mul2(both(0.5f), v), fma2(both(3.0f * kGeluC), v2, both(kGeluA)));
-    const float2 n = mul2(t, both(-1.0f));
-    return fma2(c, fma2(n, t, both(1.0f)), fma2(both(0.5f), t, both(0.5f)));
+    const float2 h2 = mul2(h, h);
+    const float2 t = tanh_hw2(mul2(h, fma2(both(8.0f * kGeluC), h2, both(2.0f * kGeluA))));
+    const float2 c = mul2(h, fma2(both(-12.0f * kGeluC), h2, both(-kGeluA)));
+    return fma2(c, fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
   } else {
     return both(1.0f);
   }
@@ -190,28 +192,16 @@ __device__ __forceinline__ float act_slope_safe(float v) {
   const float s = act_slope<kAct>(fminf(fmaxf(v, -64.0f), 64.0f));
   return v == v ? s : v;
 }
-// For the values of one checkpoint block: only a step over 1/2 can hold one, and
-// a block marked as not finite (NaN step) fails the comparison and stays NaN.
-template <int N>
-__device__ __forceinline__ void act_limit(float2 (&v)[N], float step) {
-  if (step > 0.5f)
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      v[e].x = fminf(fmaxf(v[e].x, -64.0f), 64.0f);
-      v[e].y = fminf(fmaxf(v[e].y, -64.0f), 64.0f);
-    }
-}
-
 // ------------------------------------------------------------------ checkpoint code
 
 // Magnitude as an unsigned integer: ordered like the magnitudes, with
 // infinities and NaN above every finite one.
 __device__ __forceinline__ uint32_t a8_mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// The larger of a magnitude m and |v|, NaN if either is.
-__device__ __forceinline__ float a8_max(float m, float v) {
+// The largest of a magnitude m, |v.x| and |v.y|, NaN if any is.
+__device__ __forceinline__ float a8_max(float m, float2 v) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(v.x)), "f"(fabsf(v.y)));
   return r;
 }
 
@@ -219,7 +209,7 @@ __device__ __forceinline__ float a8_max(float m, float v) {
 __device__ __forceinline__ uint32_t a8_mag8(const float2 (&f)[4]) {
   float m = 0.0f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) m = a8_max(a8_max(m, f[e].x), f[e].y);
+  for (int e = 0; e < 4; ++e) m = a8_max(m, f[e]);
   return __float_as_uint(m);
 }
 
@@ -271,6 +261,32 @@ __device__ __forceinline__ void a8_decode4(uint32_t w, float step, float2* v) {
   for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440u + i));
   v[0] = mul2(add2(make_float2(f[0], f[1]), both(-8388736.0f)), both(step));
   v[1] = mul2(add2(make_float2(f[2], f[3]), both(-8388736.0f)), both(step));
+}
+
+// Halves of the values of 4 N codes under exponent byte b, brought back to +-32
+// (see act_slope_safe).  With a step of at most 1/2 no value exceeds 64, and the
+// subtraction and the product are one exact fused operation; a block marked as
+// not finite (NaN step) goes the same way and stays NaN.
+template <int N>
+__device__ __forceinline__ void a8_decode_halves(const uint32_t (&w)[N], uint32_t b, float2 (&h)[2 * N]) {
+  const float half = 0.5f * a8_step(b);
+  if (half > 0.25f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) a8_decode4(w[i], half, h + 2 * i);
+#pragma unroll
+    for (int e = 0; e < 2 * N; ++e)
+      h[e] = make_float2(fminf(fmaxf(h[e].x, -32.0f), 32.0f), fminf(fmaxf(h[e].y, -32.0f), 32.0f));
+    return;
+  }
+  const float off = -8388736.0f * half;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t x = w[i] ^ 0x80808080u;
+    h[2 * i] = fma2(make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7440u)),
+                                __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7441u))), both(half), both(off));
+    h[2 * i + 1] = fma2(make_float2(__uint_as_float(__byte_perm(x, 0x4B000000u, 0x7442u)),
+                                    __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7443u))), both(half), both(off));
+  }
 }
 
 }  // namespace conv3d

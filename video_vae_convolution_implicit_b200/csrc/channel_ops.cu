@@ -689,22 +689,23 @@ __global__ void __launch_bounds__(kThreads, kMode == Read::kGrad ? 3 : 4) act8_r
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       if (c[j] >= p.C) continue;
-      const float step = a8_step(eb[j]);
       float2 v[4];
-      a8_decode4(k[j].x, step, v);
-      a8_decode4(k[j].y, step, v + 2);
       if constexpr (kGrad) {
         float2 dy[4];
         T::unpack8(d[j], dy);
         if constexpr (kAct != kActNone) {
-          act_limit(v, step);
+          const uint32_t w[2] = {k[j].x, k[j].y};
+          a8_decode_halves(w, eb[j], v);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = mul2(dy[e], act_slope<kAct>(v[e]));
+          for (int e = 0; e < 4; ++e) v[e] = mul2(dy[e], act_slope_of_half<kAct>(v[e]));
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = dy[e];
         }
       } else {
+        const float step = a8_step(eb[j]);
+        a8_decode4(k[j].x, step, v);
+        a8_decode4(k[j].y, step, v + 2);
         if constexpr (kMode == Read::kAffine) {
           if (c[j] != of) {
             of = c[j];

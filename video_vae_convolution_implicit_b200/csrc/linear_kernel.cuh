@@ -91,6 +91,15 @@ __device__ __forceinline__ void lin_copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void lin_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void lin_copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
+// Arrive once on the mbarrier at this address in both CTAs of the pair when all
+// prior tcgen05 operations of this thread complete.
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
 // Arrive on an mbarrier of either CTA of the pair without ordering this
 // thread's memory operations: a release at cluster scope waits until its global
 // stores have been performed, a microsecond and more at every tile.  What it
@@ -273,16 +282,14 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k)   // 16 values along the contraction: 32 bytes of a K-major row, 16 rows of an MN-major block
             mma_f16_ss_pair(d_tmem, da + 2 * k, db + (kBwd ? (2048 >> 4) : 2) * k, p.idesc, (kb | k) != 0);
-          mma_commit_pair(empty_bar + 8 * stage);
-          mma_commit_pair(mapa_shared(empty_bar + 8 * stage, 1));
+          mma_commit_both(empty_bar + 8 * stage);
           if (++stage == static_cast<uint32_t>(p.stages)) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        mma_commit_pair(tfull_bar + 8 * acc);
-        mma_commit_pair(mapa_shared(tfull_bar + 8 * acc, 1));
+        mma_commit_both(tfull_bar + 8 * acc);
       }
       mma_commit_pair(drain_bar);
       wait_bounded(drain_bar, 0, ctl, false);
@@ -305,30 +312,48 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const int crow = static_cast<int>(lane >> 1), cpart = static_cast<int>(lane & 1);
     constexpr bool kLoadCodes = kBwd && kQ;
     const bool loads = has_res || kLoadCodes;
-    // where this warp's rows and columns of a tile begin, and how many of its
-    // chunks hold part of the result
-    auto place = [&](int t, int& row0, int& col0) {
-      const int mt = t / p.tiles_n;
-      row0 = mt * 2 * BM + static_cast<int>(rank) * BM + static_cast<int>(quarter) * 32;
-      col0 = (t - mt * p.tiles_n) * p.BN + share * nj * 32;
-      const int live = (p.N - col0 + 31) / 32;
-      return row0 >= p.M || live < 0 ? 0 : live > nj ? nj : live;
+    // A tile and where this warp's rows and columns of it begin; the next one is
+    // num_units further, found by addition.
+    struct Place {
+      int t, nt, row0, col0;
     };
+    const int step_m = num_units / p.tiles_n, step_n = num_units - step_m * p.tiles_n;
+    auto advance = [&](Place& a) {
+      a.t += num_units;
+      a.nt += step_n;
+      a.row0 += step_m * 2 * BM;
+      a.col0 += step_n * p.BN;
+      if (a.nt >= p.tiles_n) {
+        a.nt -= p.tiles_n;
+        a.row0 += 2 * BM;
+        a.col0 -= p.tiles_n * p.BN;
+      }
+    };
+    // how many of the warp's chunks hold part of the result
+    auto live_chunks = [&](const Place& a) {
+      const int live = (p.N - a.col0 + 31) >> 5;
+      return a.row0 >= p.M || live < 0 ? 0 : live > nj ? nj : live;
+    };
+    Place here;
+    here.t = unit;
+    here.nt = unit % p.tiles_n;
+    here.row0 = (unit / p.tiles_n) * 2 * BM + static_cast<int>(rank) * BM + static_cast<int>(quarter) * 32;
+    here.col0 = here.nt * p.BN + share * nj * 32;
     // The residual or the codes of the warp's next chunk are always under way:
     // the load is issued when the buffer is free (the residual's is the output
     // buffer, in which the sum replaces it), for the next live chunk, of this tile
-    // or a later one (next_t, next_j), and a chunk's exponent byte is fetched
-    // with it.
-    int next_t = unit, next_j = 0;
+    // or a later one, and a chunk's exponent byte is fetched with it.
+    Place next = here;
+    int next_j = 0;
     uint32_t next_eb = 0;
     auto ask = [&]() {
-      int row0, col0;
-      while (next_t < p.num_tiles && next_j >= place(next_t, row0, col0)) {
-        next_t += num_units;
+      while (next.t < p.num_tiles && next_j >= live_chunks(next)) {
+        advance(next);
         next_j = 0;
       }
-      if (next_t >= p.num_tiles) return;
-      const int col = col0 + 32 * next_j;
+      if (next.t >= p.num_tiles) return;
+      const int row0 = next.row0;
+      const int col = next.col0 + 32 * next_j;
       if constexpr (kLoadCodes) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -355,10 +380,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     if (loads) ask();
     int local = 0;
     int bias_col = -1;
-    for (int t = unit; t < p.num_tiles; t += num_units, ++local) {
+    for (; here.t < p.num_tiles; advance(here), ++local) {
       const uint32_t acc = local & 1;
-      int row0, col0;
-      const int live = place(t, row0, col0);
+      const int row0 = here.row0, col0 = here.col0;
+      const int live = live_chunks(here);
       const int row = row0 + static_cast<int>(lane);
       if (!kBwd && bias_col != col0 && live > 0) {              // this warp's biases, as fp32
         bias_col = col0;
@@ -379,6 +404,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(tempty_bar + 8 * acc, 0));
       };
       if (live == 0) release();
+      uint32_t first_eb = 0;
       for (int j = 0; j < live; ++j) {
         const int col = col0 + 32 * j;
         uint32_t raw[32];
@@ -387,25 +413,23 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         if constexpr (kLoadCodes) {
           lin_copy_wait();
           __syncwarp();
-          const float step = a8_step(next_eb);
+          const uint32_t eb = next_eb;
           const uint4 k0 = ld_shared_v4(cb + swz32(lane, 0));
           const uint4 k1 = ld_shared_v4(cb + swz32(lane, 1));
           __syncwarp();
           ask();
-          const uint32_t k[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+          const uint32_t ka[4] = {k0.x, k0.y, k0.z, k0.w}, kb[4] = {k1.x, k1.y, k1.z, k1.w};
           tmem_ld_wait();
           if (j + 1 == live) release();
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float2 v[4];
-            a8_decode4(k[2 * g], step, v);
-            a8_decode4(k[2 * g + 1], step, v + 2);
-            act_limit(v, step);
+          for (int h = 0; h < 2; ++h) {
+            float2 v[8];
+            a8_decode_halves(h ? kb : ka, eb, v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[e] = mul2(act_slope<kAct>(v[e]), make_float2(__uint_as_float(raw[8 * g + 2 * e]),
-                                                             __uint_as_float(raw[8 * g + 2 * e + 1])));
-              packed[4 * g + e] = T::pack(v[e].x, v[e].y);
+            for (int e = 0; e < 8; ++e) {
+              v[e] = mul2(act_slope_of_half<kAct>(v[e]), make_float2(__uint_as_float(raw[16 * h + 2 * e]),
+                                                                     __uint_as_float(raw[16 * h + 2 * e + 1])));
+              packed[8 * h + e] = T::pack(v[e].x, v[e].y);
             }
           }
         } else {
@@ -425,7 +449,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           if constexpr (!kBwd && kQ) {
             float m = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) m = a8_max(a8_max(m, v[e].x), v[e].y);
+            for (int e = 0; e < 16; ++e) m = a8_max(m, v[e]);
             const uint32_t mag = __float_as_uint(m);
             const uint32_t eb = a8_exponent(mag);
             const float inv = a8_inv_step(eb);
@@ -447,7 +471,15 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 *reinterpret_cast<uint4*>(dst + static_cast<size_t>(16 * i) * p.blocks * 32) =
                     ld_shared_v4(cb + swz32(crow + 16 * i, cpart));
             __syncwarp();
-            if (row < p.M) p.exponents[static_cast<size_t>(row) * p.blocks + col / 32] = static_cast<uint8_t>(eb);
+            // two chunks' bytes in one store where a row's blocks are even in number
+            // (col0 / 32 is even then, and the second chunk holds a block too)
+            uint8_t* e8 = p.exponents + static_cast<size_t>(row) * p.blocks + col / 32;
+            if (nj == 2 && (p.blocks & 1) == 0) {
+              if (j == 0) first_eb = eb;
+              else if (row < p.M) *reinterpret_cast<uint16_t*>(e8 - 1) = static_cast<uint16_t>(first_eb | eb << 8);
+            } else if (row < p.M) {
+              *e8 = static_cast<uint8_t>(eb);
+            }
           }
           if constexpr (!kBwd && kAct != kActNone) {
 #pragma unroll
