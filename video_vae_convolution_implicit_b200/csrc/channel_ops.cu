@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
 #pragma unroll
   for (int i = 0; i < V; ++i) in[i] = l + i * G < vecs;
   griddep_wait();
+  griddep_launch_dependents();
   // byte offsets of this thread's first vector in x and y, now and of the next fetch
   const long long first = (walk.first * p.C + l * 8) * 2, advance = walk.stride * p.C * 2;
   const int per_row = Walk<G, R, T>::kPerWarp * p.C * 2;
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_bwd_kernel(const LnBwdParam
 #pragma unroll
     for (int e = 0; e < 4; ++e) dg[i][e] = db[i][e] = both(0.0f);
   griddep_wait();
+  griddep_launch_dependents();
   const long long scale_bytes = p.rows * nb;
   // running byte offsets: the 16-bit tensors share one, the codes' is its own
   const long long first = (walk.first * p.C + l * 8) * 2, advance = walk.stride * p.C * 2;
@@ -547,6 +549,7 @@ __global__ void __launch_bounds__(1024) layernorm_param_kernel(const float* __re
   const int col = blockIdx.x * 32 + (threadIdx.x & 31);
   const int w = threadIdx.x >> 5;
   griddep_wait();
+  griddep_launch_dependents();
   float a = 0.0f;
   constexpr int kBatch = 10;   // loads in flight: all of a warp's 296 / 32
   if (col < 2 * C)
@@ -609,6 +612,7 @@ __global__ void __launch_bounds__(kThreads) act8_pack_kernel(const uint16_t* __r
   long long u = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
   UnitWalk w(u, stride, units);
   griddep_wait();
+  griddep_launch_dependents();
   // a warp's units end together (total is even and its lanes are consecutive), so the
   // exchange below always has both threads of a block
   for (long long u0 = u - (threadIdx.x & 31); u0 < total; u0 += kUnroll * stride) {
@@ -665,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, kMode == Read::kGrad ? 3 : 4) act8_r
   long long u = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
   UnitWalk w(u, stride, p.units);
   griddep_wait();
+  griddep_launch_dependents();
   // gamma and beta of this thread's channels; the host makes the stride a
   // multiple of a row where it can, and then they stay the same
   float2 g[4], b[4];

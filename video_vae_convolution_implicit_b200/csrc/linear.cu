@@ -53,9 +53,12 @@ uint32_t pow2(int v) {
   return p;
 }
 
-// Pair tiles of 256 rows when they fill most of the SM pairs; otherwise the
-// rows kernel, split along the contraction while that fills idle SMs and
-// leaves every piece a k-block.
+// Pair tiles of 256 rows x 256 or 128 columns when there are enough to keep
+// about half of the SM pairs busy, otherwise the rows kernel.  Measured on B200
+// (bf16, GELU, us; pair / rows kernel): 512 x 512 -> 2048 7.6 / 8.1, 256 rows of
+// it 7.5 / 7.3, 1024 x 2048 -> 512 15.7 / 10.6, 1000 x 1024 -> 1024 10.3 / 10.6.
+// A round of 128-column tiles takes about 0.65 of a round of 256-column ones
+// (4096 x 512 -> 2048: 18.5 / 12.9; 1024 rows of it: 8.7 / 9.0).
 Plan choose(const Product& P, const Device& dev) {
   Plan L{};
   const long long mt = (P.M + 255) / 256;
@@ -63,8 +66,9 @@ Plan choose(const Product& P, const Device& dev) {
   const int pairs = dev.num_sms / 2;
   const long long tiles256 = mt * ((P.N + 255) / 256), tiles128 = mt * ((P.N + 127) / 128);
   const int forced = env_int("CONV3D_LINEAR");   // tuning and tests: 1 rows kernel, 128 or 256 pair tiles
-  L.pair = P.M > 128 && tiles128 * 3 >= pairs * 2;
-  L.BN = tiles256 * 3 >= pairs * 2 && P.N > 128 ? 256 : 128;
+  L.pair = P.M > 128 && tiles128 * 7 >= pairs * 3;
+  const long long rounds256 = (tiles256 + pairs - 1) / pairs, rounds128 = (tiles128 + pairs - 1) / pairs;
+  L.BN = P.N > 128 && rounds256 * 20 <= rounds128 * 13 ? 256 : 128;
   if (forced == 1) L.pair = false;
   if (forced == 128 || forced == 256) {
     L.pair = true;
@@ -79,13 +83,15 @@ Plan choose(const Product& P, const Device& dev) {
     const size_t b_bytes = static_cast<size_t>(L.BN / 2) * BK * 2;
     const int tiles_n = (P.N + L.BN - 1) / L.BN;
     const long long tiles = mt * tiles_n;
-    // B resident where it leaves at least two stages for A and the pairs, a
-    // multiple of the column tiles then, need at most a tenth more rounds
+    // B resident where it leaves at least five stages for A (256 -> 1024 on
+    // 36864 rows: 23.9 us, streamed 25.7; with three stages, 512 -> 2048, 81 against 74)
+    // and the pairs, a multiple of the column tiles then, need at most a tenth
+    // more rounds
     const long long units = pairs / tiles_n * tiles_n;
     L.resident = false;
     L.units = static_cast<int>(tiles < pairs ? tiles : pairs);
     const char* env = getenv("CONV3D_LINEAR_RESIDENT");   // tuning and tests: 0 never, 1 wherever it fits
-    if (units > 0 && kblocks * b_bytes + 2 * kLinABytes <= room && (env == nullptr || env[0] != '0')) {
+    if (units > 0 && kblocks * b_bytes + 5 * kLinABytes <= room && (env == nullptr || env[0] != '0')) {
       const long long rounds = (tiles + pairs - 1) / pairs, rounds_r = (tiles + units - 1) / units;
       if (rounds_r * 10 <= rounds * 11 || (env != nullptr && env[0] == '1')) {
         L.resident = true;
@@ -99,11 +105,21 @@ Plan choose(const Product& P, const Device& dev) {
     L.smem = kReserve + epi + fixed + L.stages * stage;
     return L;
   }
-  L.BN = 16;
-  while (L.BN < 128 && L.BN < P.M) L.BN *= 2;
-  const long long tiles = static_cast<long long>((P.N + 127) / 128) * ((P.M + L.BN - 1) / L.BN);
+  // Rows per tile: those there are, up to 64, or 128 where 64 make more tiles
+  // than SMs.  Pieces: while they fill idle SMs and keep two k-blocks each (few
+  // rows: the call is latency) or four; eight CTAs of a cluster need room in one
+  // GPC, so eight pieces only for a few tiles (64 x 2048 -> 2048: 8.1 us in four
+  // pieces, over 9.4 in eight; 1 x 2048 -> 512: 6.2 and 4.9).
+  const long long nt = (P.N + 127) / 128;
+  L.BN = P.M <= 16 ? 16 : P.M <= 32 ? 32 : nt * ((P.M + 63) / 64) <= dev.num_sms ? 64 : 128;
+  const int forced_rows = env_int("CONV3D_LINEAR_ROWS");   // tuning and tests: rows per tile
+  if (forced_rows == 16 || forced_rows == 32 || forced_rows == 64 || forced_rows == 128) L.BN = forced_rows;
+  const long long tiles = nt * ((P.M + L.BN - 1) / L.BN);
+  const int least = L.BN <= 32 ? 2 : 4;
   L.split = 1;
-  while (L.split < 8 && tiles * L.split * 2 <= dev.num_sms && L.split * 2 <= kblocks) L.split *= 2;
+  while (L.split < 8 && tiles * L.split * 2 <= (L.split < 4 ? dev.num_sms : dev.num_sms * 2 / 3) &&
+         L.split * 2 * least <= kblocks)
+    L.split *= 2;
   const int forced_split = env_int("CONV3D_LINEAR_SPLIT");   // tuning and tests
   if (forced_split >= 1 && forced_split <= 8) L.split = forced_split <= kblocks ? forced_split : kblocks;
   const int per = (kblocks + L.split - 1) / L.split;
@@ -197,7 +213,7 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
   static std::atomic<unsigned long long> ready{0};
   auto kern = linear_rows_kernel<kBF16, kBwd, kAct, kQ>;
   if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
-  const cudaError_t e = launch(kern, static_cast<unsigned>(ctas), kLinRowsThreads, L.smem, static_cast<unsigned>(L.split),
+  const cudaError_t e = launch(kern, static_cast<unsigned>(ctas), L.BN > 32 ? kLinRowsThreads : kLinFewThreads, L.smem, static_cast<unsigned>(L.split),
                                stream, map_w, map_a, p);
   return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "channel product launch");
 }

@@ -42,7 +42,8 @@ namespace conv3d {
 
 constexpr int kLinEpiWarps = 16;
 constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;   // producer, issuer, epilogue
-constexpr int kLinRowsThreads = 64 + 32 * 4;
+// rows kernel: producer, issuer and 16 finishing warps, or 4 where a tile has few rows
+constexpr int kLinRowsThreads = 64 + 32 * 16, kLinFewThreads = 64 + 32 * 4;
 constexpr uint32_t kLinABytes = BM * BK * 2;           // one CTA's A rows of a k-block
 constexpr uint32_t kLinOutBytes = 32 * 32 * 2;         // a 32 x 32 chunk of 16-bit values
 constexpr uint32_t kLinCodeBytes = 32 * 32;            // the same chunk's codes
@@ -207,6 +208,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   griddep_wait();   // no global memory is touched before the previous kernel has finished
+  griddep_launch_dependents();   // a dependent's set-up may overlap this kernel; it waits in the same place
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -535,10 +537,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // [row][128 channels] fp32, and finishes the rows r, r + split, ...: the sum of
 // the ranks' partials in rank order, then the epilogue with one channel per
 // thread (a warp is one checkpoint block of the row, and its stores are
-// contiguous).  The partials take the place of the operand ring, which nothing
-// reads any more once the accumulator is complete.
+// contiguous), kBatch rows of a warp at a time.  The partials take the place of
+// the operand ring, which nothing reads any more once the accumulator is
+// complete.  These calls last a few microseconds, so the first copies are issued
+// by the thread that initialises the barriers, before the other warps have met.
 template <bool kBF16, bool kBwd, int kAct, bool kQ>
-__global__ void __launch_bounds__(kLinRowsThreads)
+__global__ void __launch_bounds__(kLinRowsThreads, 1)
     linear_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                        const LinearParams p) {
   using T = Val16<kBF16>;
@@ -565,6 +569,27 @@ __global__ void __launch_bounds__(kLinRowsThreads)
   const uint32_t tfull_bar = empty_bar + 8 * p.stages;
   SharedCtl ctl{&s_abort, p.status, p.timeout_ns, 0u};
 
+  uint32_t stage = 0, phase = 0;   // producer and issuer
+  long long issued = 0;
+  auto load = [&](int kb) {
+    const uint32_t fb = full_bar + 8 * stage;
+    if (!(p.test_stall != 0 && issued == 0)) {
+      mbar_arrive_expect_tx(fb, kLinABytes + x_bytes);
+      if constexpr (kBwd) {
+        for (int i = 0; i < BM / 64; ++i)
+          tma_load_2d(w_ring + stage * kLinABytes + i * kMnBlockBytes, &map_w, fb, ch0 + 64 * i, kb * BK);
+      } else {
+        tma_load_2d(w_ring + stage * kLinABytes, &map_w, fb, kb * BK, ch0);
+      }
+      tma_load_2d(x_ring + stage * x_bytes, &map_x, fb, kb * BK, row0);
+    }
+    ++issued;
+    if (++stage == static_cast<uint32_t>(p.stages)) {
+      stage = 0;
+      phase ^= 1;
+    }
+  };
+  int first = kb_lo;               // producer: the next k-block to load
   if (threadIdx.x == 0) {
     s_abort = 0;
     for (int s = 0; s < p.stages; ++s) {
@@ -573,8 +598,8 @@ __global__ void __launch_bounds__(kLinRowsThreads)
     }
     mbar_init(tfull_bar, 1);
     fence_mbar_init();
-    prefetch_tensormap(&map_w);
-    prefetch_tensormap(&map_x);
+    griddep_wait();                // no global memory is touched before the previous kernel has finished
+    for (; first < kb_hi && first < kb_lo + p.stages; ++first) load(first);
   }
   if (warp == 1) {
     tmem_alloc(smem_addr(&s_tmem_base), p.tmem_cols);
@@ -585,40 +610,19 @@ __global__ void __launch_bounds__(kLinRowsThreads)
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   griddep_wait();
+  griddep_launch_dependents();
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      long long issued = 0;
       bool ok = true;
-      const bool stall = p.test_stall != 0;
-      for (int kb = kb_lo; kb < kb_hi; ++kb) {
-        if (!wait_bounded(empty_bar + 8 * stage, phase ^ 1, ctl, true)) {
-          ok = false;
-          break;
-        }
-        const uint32_t fb = full_bar + 8 * stage;
-        if (!(stall && issued == 0)) {
-          mbar_arrive_expect_tx(fb, kLinABytes + x_bytes);
-          if constexpr (kBwd) {
-            for (int i = 0; i < BM / 64; ++i)
-              tma_load_2d(w_ring + stage * kLinABytes + i * kMnBlockBytes, &map_w, fb, ch0 + 64 * i, kb * BK);
-          } else {
-            tma_load_2d(w_ring + stage * kLinABytes, &map_w, fb, kb * BK, ch0);
-          }
-          tma_load_2d(x_ring + stage * x_bytes, &map_x, fb, kb * BK, row0);
-        }
-        ++issued;
-        if (++stage == static_cast<uint32_t>(p.stages)) {
-          stage = 0;
-          phase ^= 1;
-        }
+      for (int kb = first; ok && kb < kb_hi; ++kb) {
+        ok = wait_bounded(empty_bar + 8 * stage, phase ^ 1, ctl, true);
+        if (ok) load(kb);
       }
-      producer_finish<false>(!ok, issued, stall, p.stages, full_bar, kLinABytes + x_bytes, 0, 0, ctl, true);
+      producer_finish<false>(!ok, issued, p.test_stall != 0, p.stages, full_bar, kLinABytes + x_bytes, 0, 0, ctl, true);
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         if (!wait_bounded(full_bar + 8 * stage, phase, ctl, true)) break;
         tc_fence_after();
@@ -638,7 +642,7 @@ __global__ void __launch_bounds__(kLinRowsThreads)
       mma_commit(tfull_bar);
       wait_bounded(tfull_bar, 0, ctl, false);
     }
-  } else {
+  } else if (warp < 6) {
     const uint32_t quarter = warp & 3;
     // (not watching the abort flag: the commit above always arrives)
     if (wait_bounded(tfull_bar, 0, ctl, false) && !s_abort) {
@@ -667,6 +671,7 @@ __global__ void __launch_bounds__(kLinRowsThreads)
   __syncthreads();
   if (p.split > 1) cluster_sync();   // every rank's partials are in its shared memory
   if (warp >= 2) {
+    constexpr int kBatch = 4;
     const uint32_t quarter = warp & 3;
     const int ch = ch0 + static_cast<int>(quarter * 32u + lane);
     const bool live = ch < p.N;
@@ -677,39 +682,66 @@ __global__ void __launch_bounds__(kLinRowsThreads)
     int rows = p.M - row0;
     if (rows > p.BN) rows = p.BN;
     if (block >= p.blocks) rows = 0;
-    for (int m = rank; m < rows; m += p.split) {
-      float v = 0.0f;
-      if (p.split == 1) {
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(mine + m * (BM * 4u)) : "memory");
-      } else {
-        float part[8];
+    // this warp's rows: every `lanes`-th of the rank's
+    const int group = (static_cast<int>(warp) - 2) / 4, groups = (static_cast<int>(blockDim.x) / 32 - 2) / 4;
+    const int step = p.split * groups;
+    for (int m0 = rank + p.split * group; m0 < rows; m0 += kBatch * step) {
+      float v[kBatch], aux[kBatch];
+      uint32_t eb[kBatch];
+      // what each row reads, all in flight before any of it is used
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < p.split)
-            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                         : "=f"(part[r])
-                         : "r"(mapa_shared(mine + m * (BM * 4u), r))
-                         : "memory");
-#pragma unroll
-        for (int r = 0; r < 8; ++r)
-          if (r < p.split) v += part[r];
-      }
-      const size_t row = static_cast<size_t>(row0 + m);
-      if constexpr (kBwd && kQ) {
-        const uint32_t b = __ldg(p.exponents + row * p.blocks + block);
-        const int k = static_cast<int8_t>(__ldg(p.codes + row * p.blocks * 32 + ch));
-        v *= act_slope_safe<kAct>(static_cast<float>(k) * a8_step(b));
-      } else if constexpr (!kBwd) {
-        v += bv;
-        if constexpr (kQ) {
-          const uint32_t b = a8_exponent(__reduce_max_sync(0xFFFFFFFFu, a8_mag(v)));
-          p.codes[row * p.blocks * 32 + ch] = static_cast<uint8_t>(a8_code4(make_float2(v, 0.0f), both(0.0f), a8_inv_step(b)) & 0xFFu);
-          if (lane == 0) p.exponents[row * p.blocks + block] = static_cast<uint8_t>(b);
+      for (int i = 0; i < kBatch; ++i) {
+        const int m = m0 + i * step;
+        v[i] = aux[i] = 0.0f;
+        eb[i] = 7u;
+        if (m < rows) {
+          const size_t row = static_cast<size_t>(row0 + m);
+          if constexpr (kBwd && kQ) {
+            eb[i] = __ldg(p.exponents + row * p.blocks + block);
+            aux[i] = static_cast<float>(static_cast<int8_t>(__ldg(p.codes + row * p.blocks * 32 + ch)));
+          } else if (!kBwd && p.residual != nullptr && live) {
+            aux[i] = T::lo(p.residual[row * p.N + ch]);
+          }
+          if (p.split == 1)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(mine + m * (BM * 4u)) : "memory");
         }
-        v = act_value<kAct>(v);
-        if (p.residual != nullptr && live) v += T::lo(p.residual[row * p.N + ch]);
       }
-      if (live) p.out[row * p.N + ch] = static_cast<uint16_t>(T::pack(v, 0.0f) & 0xFFFFu);
+      if (p.split > 1) {
+        for (int r = 0; r < p.split; ++r) {
+          float part[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            part[i] = 0.0f;
+            if (m0 + i * step < rows)
+              asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                           : "=f"(part[i])
+                           : "r"(mapa_shared(mine + (m0 + i * step) * (BM * 4u), r))
+                           : "memory");
+          }
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) v[i] += part[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int m = m0 + i * step;
+        if (m >= rows) break;
+        const size_t row = static_cast<size_t>(row0 + m);
+        float y = v[i];
+        if constexpr (kBwd && kQ) {
+          y *= act_slope_safe<kAct>(aux[i] * a8_step(eb[i]));
+        } else if constexpr (!kBwd) {
+          y += bv;
+          if constexpr (kQ) {
+            const uint32_t b = a8_exponent(__reduce_max_sync(0xFFFFFFFFu, a8_mag(y)));
+            p.codes[row * p.blocks * 32 + ch] =
+                static_cast<uint8_t>(a8_code4(make_float2(y, 0.0f), both(0.0f), a8_inv_step(b)) & 0xFFu);
+            if (lane == 0) p.exponents[row * p.blocks + block] = static_cast<uint8_t>(b);
+          }
+          y = act_value<kAct>(y) + aux[i];
+        }
+        if (live) p.out[row * p.N + ch] = static_cast<uint16_t>(T::pack(y, 0.0f) & 0xFFFFu);
+      }
     }
   }
   if (p.split > 1) cluster_sync();   // no CTA leaves while its peers may read its partials
