@@ -83,6 +83,11 @@ if not os.path.exists(lib_path):
     raise ImportError(f"{lib_path} is missing: build it with "
                       "`python video_vae_convolution_implicit_b200/build.py` (nvcc, sm_100a)")
 _lib = ctypes.CDLL(lib_path)
+try:
+    from . import _channel   # the native calls of the channel-wise operators (csrc/binding.cpp)
+except ImportError as e:
+    raise ImportError("the native binding _channel.so is missing or does not load: build it with "
+                      "`python video_vae_convolution_implicit_b200/build.py`") from e
 
 _i3 = ctypes.c_int * 3
 _vp = ctypes.c_void_p
@@ -154,6 +159,9 @@ _lib.conv3d_linear_fwd.restype = _c
 _lib.conv3d_linear_fwd.argtypes = [_vp] * 7 + [_ll, _c, _c, _c, _c, _vp]
 _lib.conv3d_linear_bwd_data.restype = _c
 _lib.conv3d_linear_bwd_data.argtypes = [_vp] * 4 + [_c, _vp, _ll, _c, _c, _c, _vp]
+
+
+_channel.set_error_class(Conv3dError)
 
 
 def raw_library() -> ctypes.CDLL:
@@ -579,7 +587,9 @@ def conv3d_autograd(x, w, bias=None, residual=None, stride=(1, 1, 1), pad=(0, 1,
 #
 # Tensors are [..., C], contiguous, bf16 or fp16; every leading extent counts as
 # rows.  All tensors of a call live on one CUDA device, which need not be the
-# current one; the default stream is that device's current stream.
+# current one; the default stream is that device's current stream.  The calls go
+# through the native binding, which checks the operands (ValueError, TypeError),
+# allocates the outputs and raises Conv3dError for a status of the library.
 
 
 def layernorm_fwd_ptr(x, gamma, beta, y, mean, rstd, codes, exponents, rows, C, eps, dtype, stream) -> int:
@@ -632,117 +642,33 @@ class Act8(NamedTuple):
 
     @staticmethod
     def empty(shape, device) -> "Act8":
+        """An uninitialised checkpoint of a tensor of ``shape``."""
         blocks = -(-shape[-1] // 32)
         lead = tuple(shape[:-1])
         return Act8(torch.empty((*lead, blocks * 32), dtype=torch.int8, device=device),
                     torch.empty((*lead, blocks), dtype=torch.uint8, device=device), int(shape[-1]))
 
 
-# The current stream of a device as a raw handle.  The direct accessor takes 0.1 us where building a
-# torch.cuda.Stream takes 2.2, as long as the whole of a small kernel.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
-
-
-def _call(fn, device, stream, *args) -> None:
-    """Runs the library call ``fn(*args, stream)`` with ``device`` current, and checks its status."""
-    s = _raw_stream(device) if stream is None else _stream_handle(stream)
-    if device == torch.cuda.current_device():
-        status = fn(*args, s)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, s)
-    if status:
-        _check(status)
-
-
-def _refuse(name, t, device, dtype, shape):
-    """Says what is wrong with an operand that failed the check of :func:`_tensor`."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _tensor(name, t, device, dtype, shape):
-    """Checks one operand (a contiguous tensor on CUDA device ``device``); returns its address."""
-    if t.get_device() != device or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(name, t, device, dtype, shape)
-    return t.data_ptr()
-
-
-def _main(name, t):
-    """Checks a call's leading operand; returns (rows, channels, device, dtype, dtype code)."""
-    device = t.get_device()
-    if device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() < 1 or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous [..., C] tensor")
-    dtype = t.dtype
-    C = t.shape[-1]
-    return t.numel() // C if C else 0, C, device, dtype, BF16 if dtype is torch.bfloat16 else _dtype_code(dtype)
-
-
-def _act8(name, a, shape, device):
-    """Checks a checkpoint of a tensor of ``shape``; returns the two addresses."""
-    codes, exponents, C = a
-    if C != shape[-1]:
-        raise ValueError(f"{name} holds {C} channels, expected {shape[-1]}")
-    lead, blocks = shape[:-1], -(-C // 32)
-    return (_tensor(f"{name}.codes", codes, device, torch.int8, (*lead, blocks * 32)),
-            _tensor(f"{name}.exponents", exponents, device, torch.uint8, (*lead, blocks)))
-
-
-def _new_act8(like, shape):
-    blocks = -(-shape[-1] // 32)
-    lead = shape[:-1]
-    return Act8(like.new_empty((*lead, blocks * 32), dtype=torch.int8),
-                like.new_empty((*lead, blocks), dtype=torch.uint8), shape[-1])
+def _on(stream):
+    """A stream argument for the native binding: None is the device's current stream."""
+    return None if stream is None else _stream_handle(stream)
 
 
 def act8_pack(x: torch.Tensor, stream=None) -> Act8:
     """The 8-bit checkpoint of x [..., C]."""
-    rows, C, device, _, code = _main("x", x)
-    a = _new_act8(x, x.shape)
-    _call(_lib.conv3d_act8_pack, device, stream, x.data_ptr(), a.codes.data_ptr(), a.exponents.data_ptr(), rows, C,
-          code)
-    return a
+    codes, exponents = _channel.act8_pack(x, _on(stream))
+    return Act8(codes, exponents, x.shape[-1])
 
 
 def act8_unpack(a: Act8, dtype: torch.dtype, gamma=None, beta=None, act: int = ACT_NONE,
                 y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """act(v * gamma + beta) of the checkpoint's values v, as a ``dtype`` tensor."""
-    C = a.channels
-    shape = (*a.codes.shape[:-1], C)
-    device = a.codes.get_device()
-    if device < 0:
-        raise ValueError("a must hold CUDA tensors")
-    codes, exponents = _act8("a", a, shape, device)
-    code = _dtype_code(dtype)
-    if y is None:
-        y = a.codes.new_empty(shape, dtype=dtype)
-    else:
-        _tensor("y", y, device, dtype, shape)
-    g = None if gamma is None else _tensor("gamma", gamma, device, dtype, (C,))
-    b = None if beta is None else _tensor("beta", beta, device, dtype, (C,))
-    _call(_lib.conv3d_act8_unpack, device, stream, codes, exponents, g, b, act, y.data_ptr(),
-          y.numel() // C if C else 0, C, code)
-    return y
+    return _channel.act8_unpack(a[0], a[1], a[2], dtype, gamma, beta, act, y, _on(stream))
 
 
 def act8_bwd(dy: torch.Tensor, a: Act8, act: int, dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dy * act'(v) of the checkpoint's values v (``dx`` may be ``dy``)."""
-    rows, C, device, dtype, code = _main("dy", dy)
-    codes, exponents = _act8("a", a, dy.shape, device)
-    if dx is None:
-        dx = torch.empty_like(dy)
-    else:
-        _tensor("dx", dx, device, dtype, dy.shape)
-    _call(_lib.conv3d_act8_bwd, device, stream, dy.data_ptr(), codes, exponents, act, dx.data_ptr(), rows, C, code)
-    return dx
+    return _channel.act8_bwd(dy, a[0], a[1], a[2], act, dx, _on(stream))
 
 
 def layernorm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-6, with_stats: bool = False,
@@ -753,30 +679,8 @@ def layernorm(x: torch.Tensor, gamma=None, beta=None, eps: float = 1e-6, with_st
     ``checkpoint8`` (y, xhat, rstd), xhat the :class:`Act8` of (x - mean) * rstd:
     either is what :func:`layernorm_bwd` needs.  ``y`` may be ``x``.
     """
-    rows, C, device, dtype, code = _main("x", x)
-    g = None if gamma is None else _tensor("gamma", gamma, device, dtype, (C,))
-    b = None if beta is None else _tensor("beta", beta, device, dtype, (C,))
-    if y is None:
-        y = torch.empty_like(x)
-    else:
-        _tensor("y", y, device, dtype, x.shape)
-    fn = _lib.conv3d_layernorm_fwd
-    if with_stats:
-        if checkpoint8:
-            raise ValueError("with_stats and checkpoint8 exclude each other")
-        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
-        mean = torch.empty_like(rstd)
-        _call(fn, device, stream, x.data_ptr(), g, b, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), None, None, rows,
-              C, eps, code)
-        return y, mean, rstd
-    if checkpoint8:
-        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
-        a = _new_act8(x, x.shape)
-        _call(fn, device, stream, x.data_ptr(), g, b, y.data_ptr(), None, rstd.data_ptr(), a.codes.data_ptr(),
-              a.exponents.data_ptr(), rows, C, eps, code)
-        return y, a, rstd
-    _call(fn, device, stream, x.data_ptr(), g, b, y.data_ptr(), None, None, None, None, rows, C, eps, code)
-    return y
+    out = _channel.layernorm(x, gamma, beta, eps, with_stats, checkpoint8, y, _on(stream))
+    return (out[0], Act8(out[1], out[2], x.shape[-1]), out[3]) if checkpoint8 else out
 
 
 def layernorm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, mean: torch.Tensor | None = None, gamma=None,
@@ -788,50 +692,9 @@ def layernorm_bwd(dy: torch.Tensor, saved, rstd: torch.Tensor, mean: torch.Tenso
     dres: added to dx (the gradient of a skip connection around the norm).
     ``dx`` may be ``dy``, ``dres`` or x.
     """
-    rows, C, device, dtype, code = _main("dy", dy)
-    shape = dy.shape
-    lead = shape[:-1]
-    r = _tensor("rstd", rstd, device, torch.float32, lead)
-    x = m = codes = exponents = None
-    if isinstance(saved, Act8):
-        if mean is not None:
-            raise ValueError("mean belongs to x: a checkpoint holds the normalised values")
-        codes, exponents = _act8("saved", saved, shape, device)
-    else:
-        x = _tensor("saved", saved, device, dtype, shape)
-        if mean is None:
-            raise ValueError("x needs its mean")
-        m = _tensor("mean", mean, device, torch.float32, lead)
-    g = None if gamma is None else _tensor("gamma", gamma, device, dtype, (C,))
-    s = None if dres is None else _tensor("dres", dres, device, dtype, shape)
-    if dx is None:
-        dx = torch.empty_like(dy)
-    else:
-        _tensor("dx", dx, device, dtype, shape)
-    if not with_params:
-        _call(_lib.conv3d_layernorm_bwd, device, stream, dy.data_ptr(), x, m, codes, exponents, r, g, s, dx.data_ptr(),
-              None, None, rows, C, code, None, 0)
-        return dx, None, None
-    dgamma = dy.new_empty((C,))
-    dbeta = torch.empty_like(dgamma)
-    if workspace is None:
-        workspace = dy.new_empty((layernorm_bwd_workspace_bytes(rows, C),), dtype=torch.uint8)
-    elif workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on device {device}")
-    _call(_lib.conv3d_layernorm_bwd, device, stream, dy.data_ptr(), x, m, codes, exponents, r, g, s, dx.data_ptr(),
-          dgamma.data_ptr(), dbeta.data_ptr(), rows, C, code, workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
-    return dx, dgamma, dbeta
-
-
-def _weight(w, device, dtype, K, N=None):
-    """Checks a [N, K] weight (or a 1x1x1 convolution's [N, 1, 1, 1, K]); returns (N, address)."""
-    shape = w.shape
-    if len(shape) not in (2, 5) or shape[-1] != K or (N is not None and shape[0] != N) or (
-            len(shape) == 5 and shape[1:4] != (1, 1, 1)):
-        raise ValueError(f"w must be [N, {K}] or [N, 1, 1, 1, {K}]" + ("" if N is None else f" with N = {N}") +
-                         f", got {tuple(shape)}")
-    return shape[0], _tensor("w", w, device, dtype, shape)
+    x, a = (None, saved) if isinstance(saved, Act8) else (saved, (None, None, 0))
+    return _channel.layernorm_bwd(dy, x, mean, a[0], a[1], a[2], rstd, gamma, dres, with_params, dx, workspace,
+                                  _on(stream))
 
 
 def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: int = ACT_NONE,
@@ -841,66 +704,23 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: int 
     With ``checkpoint8`` returns (y, pre): pre is the :class:`Act8` of x w^T + bias.
     ``y`` may be ``residual``.
     """
-    rows, K, device, dtype, code = _main("x", x)
-    N, wp = _weight(w, device, dtype, K)
-    shape = (*x.shape[:-1], N)
-    b = None if bias is None else _tensor("bias", bias, device, dtype, (N,))
-    r = None if residual is None else _tensor("residual", residual, device, dtype, shape)
-    if y is None:
-        y = x.new_empty(shape)
-    else:
-        _tensor("y", y, device, dtype, shape)
-    if checkpoint8:
-        a = _new_act8(x, shape)
-        _call(_lib.conv3d_linear_fwd, device, stream, x.data_ptr(), wp, b, r, y.data_ptr(), a.codes.data_ptr(),
-              a.exponents.data_ptr(), rows, K, N, act, code)
-        return y, a
-    _call(_lib.conv3d_linear_fwd, device, stream, x.data_ptr(), wp, b, r, y.data_ptr(), None, None, rows, K, N, act,
-          code)
-    return y
+    out = _channel.linear(x, w, bias, residual, act, checkpoint8, y, _on(stream))
+    return (out[0], Act8(out[1], out[2], w.shape[0])) if checkpoint8 else out
 
 
 def linear_bwd_data(dy: torch.Tensor, w: torch.Tensor, pre: Act8 | None = None, act: int = ACT_NONE,
                     dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """dx = (dy w) * act'(pre) for dy [..., N], w [N, K]: the gradient of x, or, with the
     checkpoint ``pre`` of what ``act`` was applied to (x = act(pre)), of that argument."""
-    rows, N, device, dtype, code = _main("dy", dy)
-    K = w.shape[-1] if w.dim() else 0
-    _, wp = _weight(w, device, dtype, K, N)
-    shape = (*dy.shape[:-1], K)
-    codes = exponents = None
-    if pre is not None:
-        codes, exponents = _act8("pre", pre, shape, device)
-    elif act != ACT_NONE:
-        raise ValueError("the derivative of an activation needs the checkpoint of its argument")
-    if dx is None:
-        dx = dy.new_empty(shape)
-    else:
-        _tensor("dx", dx, device, dtype, shape)
-    _call(_lib.conv3d_linear_bwd_data, device, stream, dy.data_ptr(), wp, codes, exponents, act, dx.data_ptr(), rows, K,
-          N, code)
-    return dx
+    a = pre if pre is not None else (None, None, 0)
+    return _channel.linear_bwd_data(dy, w, a[0], a[1], a[2], act, dx, _on(stream))
 
 
 def linear_bwd_weight(x: torch.Tensor, dy: torch.Tensor, with_bias: bool = True,
                       workspace: torch.Tensor | None = None, stream=None):
     """(dw [N, K], dbias [N]) of :func:`linear` without activation: the weight
     gradient of a 1x1x1 convolution over the rows as pixels (conv3d_bwd_weight)."""
-    rows, K, device, dtype, code = _main("x", x)
-    N = dy.shape[-1] if dy.dim() else 0
-    d = _tensor("dy", dy, device, dtype, (*x.shape[:-1], N))
-    if rows < 1 or rows > 0x7FFFFFFF:
-        raise ValueError(f"rows must be in [1, 2^31), got {rows}")
-    dw = x.new_empty((N, K))
-    db = x.new_empty((N,)) if with_bias else None
-    one = _i3(1, 1, 1)
-    if workspace is None:
-        workspace = x.new_empty((bwd_weight_workspace_bytes(K, N, (1, 1, 1)),), dtype=torch.uint8)
-    elif workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on device {device}")
-    _call(_lib.conv3d_bwd_weight, device, stream, x.data_ptr(), d, dw.data_ptr(), _ptr(db), 1, K, 1, 1, rows, N, one,
-          one, _i3(0, 0, 0), TPAD_ZERO, code, workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    return dw, db
+    return _channel.linear_bwd_weight(x, dy, with_bias, workspace, _on(stream))
 
 
 class ChannelMlpSaved(NamedTuple):
@@ -932,15 +752,9 @@ def channel_mlp_bwd(dy: torch.Tensor, saved: ChannelMlpSaved, gamma, beta, w1: t
     checkpoints (one pass each); act' rides in the epilogue of dy w2 and the skip
     connection's gradient in the layer norm's.
     """
-    _main("dy", dy)
-    h = act8_unpack(saved.pre, dy.dtype, None, None, act, stream=stream)
-    dw2, db2 = linear_bwd_weight(h, dy, stream=stream)
-    dpre = linear_bwd_data(dy, w2, saved.pre, act, dx=h, stream=stream)   # h is read by then
-    n = act8_unpack(saved.xhat, dy.dtype, gamma, beta, stream=stream)
-    dw1, db1 = linear_bwd_weight(n, dpre, stream=stream)
-    dn = linear_bwd_data(dpre, w1, dx=n, stream=stream)
-    dx, dgamma, dbeta = layernorm_bwd(dn, saved.xhat, saved.rstd, gamma=gamma, dres=dy, dx=dn, stream=stream)
-    return dx, dgamma, dbeta, dw1, db1, dw2, db2
+    x, pre = saved.xhat, saved.pre
+    return _channel.channel_mlp_bwd(dy, x[0], x[1], x[2], saved.rstd, pre[0], pre[1], pre[2], gamma, beta, w1, w2, act,
+                                    _on(stream))
 
 
 class LayerNormFunction(torch.autograd.Function):

@@ -1,7 +1,8 @@
 """Build libconv3d.so (the CUDA library) in-tree with nvcc for sm_100a.
 
 The translation units are compiled side by side into build/ (one object each,
-recompiled when it or a header is newer) and linked.
+recompiled when it or a header is newer) and linked; then the native Python
+binding of the channel-wise operators, _channel.so, against torch's headers.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "build")
 LIB = os.path.join(PKG, "libconv3d.so")
+BINDING = os.path.join(PKG, "_channel.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("conv3d_api.cu", "groupnorm.cu", "channel_ops.cu", "linear.cu")]
 # the headers that each unit includes (besides the public one)
 HEADERS = {
@@ -36,23 +38,40 @@ def _newer(deps: list[str], than: str) -> bool:
     return not os.path.exists(than) or any(os.path.getmtime(d) > os.path.getmtime(than) for d in deps)
 
 
+def binding_command() -> list[str]:
+    import sysconfig
+    import torch
+    root = os.path.dirname(torch.__file__)
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
+                sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(a for i in includes for a in ("-isystem", i)), "-I", os.path.join(ROOT, "include"),
+            "-o", BINDING, os.path.join(CSRC, "binding.cpp"),
+            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-L", PKG, "-l:libconv3d.so", "-Wl,-rpath,$ORIGIN"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _newer([d for s in SOURCES for d in _deps(s)], LIB):
-        return LIB
-    os.makedirs(OBJ, exist_ok=True)
-    extra = ["-Xptxas", "-v"] if verbose else []
-    running, objects = [], []
-    for src in SOURCES:
-        obj = os.path.join(OBJ, os.path.basename(src) + ".o")
-        objects.append(obj)
-        if force or _newer(_deps(src), obj):
-            cmd = ["nvcc", *FLAGS, *extra, "-c", "-o", obj, src]
-            running.append((cmd, subprocess.Popen(cmd)))
-    failed = [cmd for cmd, p in running if p.wait() != 0]
-    if failed:
-        raise subprocess.CalledProcessError(1, failed[0])
-    subprocess.run(["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "--shared", "-o", LIB, *objects],
-                   check=True)
+    if force or _newer([d for s in SOURCES for d in _deps(s)], LIB):
+        os.makedirs(OBJ, exist_ok=True)
+        extra = ["-Xptxas", "-v"] if verbose else []
+        running, objects = [], []
+        for src in SOURCES:
+            obj = os.path.join(OBJ, os.path.basename(src) + ".o")
+            objects.append(obj)
+            if force or _newer(_deps(src), obj):
+                cmd = ["nvcc", *FLAGS, *extra, "-c", "-o", obj, src]
+                running.append((cmd, subprocess.Popen(cmd)))
+        failed = [cmd for cmd, p in running if p.wait() != 0]
+        if failed:
+            raise subprocess.CalledProcessError(1, failed[0])
+        subprocess.run(["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "--shared", "-o", LIB, *objects],
+                       check=True)
+    binding_deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "conv3d.h")]
+    if force or _newer(binding_deps, BINDING):
+        subprocess.run(binding_command(), check=True)
     return LIB
 
 
