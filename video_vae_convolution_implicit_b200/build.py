@@ -49,7 +49,7 @@ def binding_command() -> list[str]:
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *(a for i in includes for a in ("-isystem", i)), "-I", os.path.join(ROOT, "include"),
             "-o", BINDING, os.path.join(CSRC, "binding.cpp"),
-            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+            "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
             "-L", PKG, "-l:libconv3d.so", "-Wl,-rpath,$ORIGIN"]
 
 
