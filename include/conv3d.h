@@ -465,13 +465,27 @@ CONV3D_API conv3d_status_t conv3d_linear_fwd(const void* x, const void* w, const
  * conv3d_linear_bwd_data -- dx = (dy w) * act'(v), dy [rows, N], w [N, K], dx
  * [rows, K], v the checkpoint [rows, K] of what the activation that produced x
  * was applied to (x = act(v)); CONV3D_ACT_NONE: dx = dy w, codes and exponents
- * unused.  w is read as it lies; no workspace.  The weight's and the bias's
- * gradients are conv3d_bwd_weight's with kernel {1,1,1}, D = H = 1, W = rows.
+ * unused.  w is read as it lies; no workspace.
  */
 CONV3D_API conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void* codes,
                                                   const void* exponents, conv3d_act_t act, void* dx,
                                                   long long rows, int K, int N, conv3d_dtype_t dtype,
                                                   struct CUstream_st* stream);
+
+/*
+ * conv3d_linear_bwd_weight -- dw = dy^T x [N, K] and, unless dbias is NULL, dbias
+ * [N], the column sums of dy, for x [rows, K] and dy [rows, N] (without an
+ * activation: the gradient of act(pre) is multiplied by act'(pre) first,
+ * conv3d_act8_bwd).  fp32 sums over ranges of rows, kept in the workspace
+ * (conv3d_linear_bwd_weight_workspace_bytes(), device, 256-byte aligned; 0 bytes
+ * when one range does, and then it may be NULL) and added in their order: the same
+ * inputs give the same bits.  One launch, or two.
+ */
+CONV3D_API conv3d_status_t conv3d_linear_bwd_weight(const void* x, const void* dy, void* dw,
+                                                    void* dbias, long long rows, int K, int N,
+                                                    conv3d_dtype_t dtype, void* workspace,
+                                                    size_t ws_bytes, struct CUstream_st* stream);
+CONV3D_API size_t conv3d_linear_bwd_weight_workspace_bytes(long long rows, int K, int N);
 
 /* Device scratch bytes conv3d_fwd_ws needs for this problem: the folded
  * first-frame weight for CONV3D_TPAD_CAUSAL_REPLICATE with D == 1 and kt > 1,

@@ -228,10 +228,7 @@ def test_block_in_a_graph_and_on_another_stream():
         assert c3.poll_status() == c3.Status.OK
         for name, a, b, c in zip(("y", *NAMES), want, out, other):
             for got in (b, c):
-                if name in ("dw1", "dw2", "db1", "db2"):           # fp32 atomics: rounded once after any order
-                    ref.check(got, a.double(), 2.0 ** -7 * a.double().abs() + 2.0 ** -10, name)
-                else:
-                    assert torch.equal(got, a), name
+                assert torch.equal(got, a), name
 
 
 def test_two_streams_at_once():
@@ -242,8 +239,7 @@ def test_two_streams_at_once():
 
     def step(p, dy):
         y, saved = c3.channel_mlp(**p, save=True)
-        dx, dg, db, *_ = c3.channel_mlp_bwd(dy, saved, p["gamma"], p["beta"], p["w1"], p["w2"])
-        return y, dx, dg, db
+        return (y, *c3.channel_mlp_bwd(dy, saved, p["gamma"], p["beta"], p["w1"], p["w2"]))
     alone = [step(p, dy) for p, dy in zip(ps, ys)]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in sizes]
@@ -351,6 +347,22 @@ def test_product_kernels_time_out_and_recover(variant, monkeypatch, _disarm):
     y, a = run_linear(p, 2, True, True, True)
     sync_ok()
     check_linear(p, BF, 2, True, True, y, a)
+
+
+@pytest.mark.parametrize("splits", ["1", "2"])
+def test_weight_gradient_kernel_times_out_and_recovers(splits, monkeypatch, _disarm):
+    monkeypatch.setenv("CONV3D_LINEAR_WGRAD_SPLITS", splits)
+    x, dy = rand((30000, 264), 38, 0), rand((30000, 520), 38, 1)
+    want = c3.linear_bwd_weight(x, dy)
+    sync_ok()
+    c3.test_arm_stall(1, 50)
+    t0 = time.perf_counter()
+    c3.linear_bwd_weight(x, dy)
+    assert c3.poll_status() == c3.Status.TIMEOUT
+    assert time.perf_counter() - t0 < 5.0
+    again = c3.linear_bwd_weight(x, dy)
+    sync_ok()
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
 
 
 @pytest.mark.parametrize("M,K,N", [(300, 64, 512), (2000, 256, 264), (5000, 448, 520), (20000, 320, 1032)])

@@ -39,8 +39,12 @@ def lin_bwd(dy=DY, w=W, q=None, e=None, act=0, dx=DX, rows=4, K=64, N=64, dt=c3.
     return c3.linear_bwd_data_ptr(dy, w, q, e, act, dx, rows, K, N, dt, None)
 
 
+def lin_dw(x=X, dy=DY, dw=W, db=B, rows=4, K=64, N=64, dt=c3.BF16, ws=R, ws_bytes=1 << 30):
+    return c3.linear_bwd_weight_ptr(x, dy, dw, db, rows, K, N, dt, ws, ws_bytes, None)
+
+
 CALLS = [ln_fwd, ln_bwd, pack, unpack, act_bwd]
-PRODUCTS = [lin, lin_bwd]
+PRODUCTS = [lin, lin_bwd, lin_dw]
 
 
 @pytest.mark.parametrize("call", CALLS + PRODUCTS)
@@ -97,7 +101,7 @@ def test_nulls():
                          [(pack, n) for n in ("x", "q", "e")] + [(unpack, n) for n in ("q", "e", "y")] +
                          [(act_bwd, n) for n in ("dy", "q", "e", "dx")] +
                          [(lin, n) for n in ("x", "w", "bias", "res", "y")] +
-                         [(lin_bwd, n) for n in ("dy", "w", "dx")])
+                         [(lin_bwd, n) for n in ("dy", "w", "dx")] + [(lin_dw, n) for n in ("x", "dy", "dw", "db")])
 def test_alignment(call, name):
     defaults = dict(zip(call.__code__.co_varnames, call.__defaults__))
     assert call(**{name: defaults[name] + 8}) == Status.ALIGNMENT
@@ -119,8 +123,24 @@ def test_workspace():
     assert str(need) in c3.last_error()
 
 
+def test_weight_gradient_workspace():
+    assert c3.linear_bwd_weight_workspace_bytes(4, 64, 64) == 0                 # one row range
+    need = c3.linear_bwd_weight_workspace_bytes(100000, 512, 2048)
+    assert need > 0 and need % 256 == 0
+    big = dict(rows=100000, K=512, N=2048)
+    assert lin_dw(**big, ws=None) == Status.WORKSPACE
+    assert lin_dw(**big, ws_bytes=need - 1) == Status.WORKSPACE
+    assert lin_dw(**big, ws=R + 64) == Status.ALIGNMENT
+    assert lin_dw(**big, ws=DY) == Status.INVALID_ARG
+    assert c3.linear_bwd_weight_workspace_bytes(0, 64, 64) == 0
+
+
 def test_overlaps():
     n = 4 * 64 * 2
+    assert lin_dw(dw=X) == Status.INVALID_ARG
+    assert lin_dw(dw=DY + 16) == Status.INVALID_ARG
+    assert lin_dw(db=W + 16) == Status.INVALID_ARG
+    assert lin_dw(x=None) == Status.INVALID_ARG and lin_dw(dw=None) == Status.INVALID_ARG
     assert ln_fwd(y=X + 16) == Status.INVALID_ARG
     assert ln_fwd(y=G) == Status.INVALID_ARG
     assert ln_fwd(q=X, e=E) == Status.INVALID_ARG

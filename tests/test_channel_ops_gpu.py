@@ -392,14 +392,42 @@ def test_linear_data_gradient(M, K, N, dtype, kernel, monkeypatch):
         ref.check(dx, want, ref.rounding(want, dt) * 1.01 + bound + 2.0 ** -23 * want.abs(), "dx")
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 64, 72), (37, 520, 136), (3000, 256, 512)])
-def test_linear_weight_gradient(M, K, N):
-    x, dy = rand((M, K), 16, 0), rand((M, N), 16, 1)
+@pytest.mark.parametrize("splits", ["", "1", "2", "5"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,N", [(1, 8, 8), (1, 64, 72), (37, 520, 136), (128, 256, 256), (129, 264, 40), (3000, 256, 512),
+                                   (20001, 72, 1000), (70000, 64, 96)])
+def test_linear_weight_gradient(M, K, N, dtype, splits, monkeypatch):
+    if splits:
+        monkeypatch.setenv("CONV3D_LINEAR_WGRAD_SPLITS", splits)
+    dt = DT[dtype]
+    x, dy = rand((M, K), 16, 0, 1.0, dt), rand((M, N), 16, 1, 1.0, dt)
     dw, db = c3.linear_bwd_weight(x, dy)
+    dw2, none = c3.linear_bwd_weight(x, dy, with_bias=False)
+    dw3, db3 = c3.linear_bwd_weight(x, dy)
     sync_ok()
     rdw, rdb = dy.double().t() @ x.double(), dy.double().sum(0)
-    ref.check(dw, rdw, ref.rounding(rdw, x.dtype) * 1.01 + (M + 8) * 2.0 ** -23 * (dy.double().abs().t() @ x.double().abs()), "dw")
-    ref.check(db, rdb, ref.rounding(rdb, x.dtype) * 1.01 + (M + 8) * 2.0 ** -23 * dy.double().abs().sum(0), "dbias")
+    ref.check(dw, rdw, ref.rounding(rdw, dt) * 1.01 + (M + 8) * 2.0 ** -23 * (dy.double().abs().t() @ x.double().abs()), "dw")
+    ref.check(db, rdb, ref.rounding(rdb, dt) * 1.01 + (M + 8) * 2.0 ** -23 * dy.double().abs().sum(0), "dbias")
+    assert none is None and torch.equal(dw2, dw) and torch.equal(dw3, dw) and torch.equal(db3, db)
+
+
+@pytest.mark.parametrize("splits", ["1", "3"])
+def test_linear_weight_gradient_writes_nothing_outside(splits, monkeypatch):
+    monkeypatch.setenv("CONV3D_LINEAR_WGRAD_SPLITS", splits)
+    M, K, N = 5000, 136, 264
+    x, dy = rand((M, K), 18, 0), rand((M, N), 18, 1)
+    dw, dw_ok = guarded(N * K, torch.bfloat16)
+    db, db_ok = guarded(N, torch.bfloat16)
+    need = c3.linear_bwd_weight_workspace_bytes(M, K, N)
+    ws, ws_ok = guarded(max(need, 256), torch.uint8)
+    ws.fill_(0xFF)                                         # NaN in every place that is read before it is written
+    assert c3.linear_bwd_weight_ptr(x.data_ptr(), dy.data_ptr(), dw.data_ptr(), db.data_ptr(), M, K, N, c3.BF16,
+                                    ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream) == c3.Status.OK
+    sync_ok()
+    want = c3.linear_bwd_weight(x, dy)
+    assert torch.equal(dw.view(N, K), want[0]) and torch.equal(db, want[1])
+    for ok in (dw_ok, db_ok, ws_ok):
+        ok()
 
 
 def test_offsets_beyond_32_bits(monkeypatch):

@@ -45,6 +45,7 @@ __all__ = [
     "linear_autograd", "ChannelMlpSaved", "channel_mlp", "channel_mlp_bwd", "ChannelMlpFunction",
     "channel_mlp_autograd", "layernorm_fwd_ptr", "layernorm_bwd_ptr", "act8_pack_ptr",
     "act8_unpack_ptr", "act8_bwd_ptr", "linear_fwd_ptr", "linear_bwd_data_ptr",
+    "linear_bwd_weight_ptr", "linear_bwd_weight_workspace_bytes",
     "poll_status", "selftest_wait_timeout", "release", "test_arm_stall",
 ]
 
@@ -160,6 +161,11 @@ _lib.conv3d_linear_fwd.argtypes = [_vp] * 7 + [_ll, _c, _c, _c, _c, _vp]
 _lib.conv3d_linear_bwd_data.restype = _c
 _lib.conv3d_linear_bwd_data.argtypes = [_vp] * 4 + [_c, _vp, _ll, _c, _c, _c, _vp]
 
+
+_lib.conv3d_linear_bwd_weight.restype = _c
+_lib.conv3d_linear_bwd_weight.argtypes = [_vp] * 4 + [_ll, _c, _c, _c, _vp, ctypes.c_size_t, _vp]
+_lib.conv3d_linear_bwd_weight_workspace_bytes.restype = ctypes.c_size_t
+_lib.conv3d_linear_bwd_weight_workspace_bytes.argtypes = [_ll, _c, _c]
 
 _channel.set_error_class(Conv3dError)
 
@@ -633,6 +639,15 @@ def linear_bwd_data_ptr(dy, w, codes, exponents, act, dx, rows, K, N, dtype, str
     return _lib.conv3d_linear_bwd_data(dy, w, codes, exponents, act, dx, rows, K, N, dtype, stream)
 
 
+def linear_bwd_weight_ptr(x, dy, dw, dbias, rows, K, N, dtype, workspace, ws_bytes, stream) -> int:
+    """Raw-pointer call of conv3d_linear_bwd_weight; returns the status code."""
+    return _lib.conv3d_linear_bwd_weight(x, dy, dw, dbias, rows, K, N, dtype, workspace, ws_bytes, stream)
+
+
+def linear_bwd_weight_workspace_bytes(rows: int, K: int, N: int) -> int:
+    return int(_lib.conv3d_linear_bwd_weight_workspace_bytes(rows, K, N))
+
+
 class Act8(NamedTuple):
     """An 8-bit activation checkpoint of a [..., C] tensor: int8 codes
     [..., 32 * ceil(C/32)] and uint8 exponents [..., ceil(C/32)] (conv3d.h)."""
@@ -718,8 +733,8 @@ def linear_bwd_data(dy: torch.Tensor, w: torch.Tensor, pre: Act8 | None = None, 
 
 def linear_bwd_weight(x: torch.Tensor, dy: torch.Tensor, with_bias: bool = True,
                       workspace: torch.Tensor | None = None, stream=None):
-    """(dw [N, K], dbias [N]) of :func:`linear` without activation: the weight
-    gradient of a 1x1x1 convolution over the rows as pixels (conv3d_bwd_weight)."""
+    """(dw [N, K], dbias [N]) of :func:`linear` without activation (dbias is None without
+    ``with_bias``): fp32 sums in a fixed order, so the same inputs give the same bits."""
     return _channel.linear_bwd_weight(x, dy, with_bias, workspace, _on(stream))
 
 

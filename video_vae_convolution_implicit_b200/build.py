@@ -22,7 +22,7 @@ HEADERS = {
     "conv3d_api.cu": ("conv3d_kernel.cuh", "wgrad_kernel.cuh", "pipeline.cuh", "ptx.cuh", "internal.h"),
     "groupnorm.cu": (),
     "channel_ops.cu": ("act8.cuh", "ptx.cuh", "internal.h"),
-    "linear.cu": ("linear_kernel.cuh", "act8.cuh", "pipeline.cuh", "ptx.cuh", "internal.h"),
+    "linear.cu": ("linear_kernel.cuh", "linear_wgrad.cuh", "act8.cuh", "pipeline.cuh", "ptx.cuh", "internal.h"),
 }
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -289,8 +289,6 @@ std::tuple<Tensor, OptTensor> linear_bwd_weight(const Tensor& x, const Tensor& d
   TORCH_CHECK_VALUE(dy.dim() >= 1, "dy must be [..., N]");
   const int N = Lead::narrow(dy.size(-1));
   const void* d = operand("dy", dy, l.device, l.type, l.with(N));
-  TORCH_CHECK_VALUE(l.rows >= 1 && l.rows <= INT_MAX, "rows must be in [1, 2^31), got ", l.rows);
-  const int one[3] = {1, 1, 1}, zero[3] = {0, 0, 0};
   Tensor dw = l.empty({N, l.C}), db, ws;
   if (with_bias) db = l.empty({N});
   if (workspace.has_value()) {
@@ -298,12 +296,13 @@ std::tuple<Tensor, OptTensor> linear_bwd_weight(const Tensor& x, const Tensor& d
                       "workspace must be a contiguous CUDA tensor on ", l.device);
     ws = *workspace;
   } else {
-    ws = l.empty({static_cast<int64_t>(conv3d_bwd_weight_workspace_bytes(l.C, N, one))}, at::kByte);
+    const size_t need = conv3d_linear_bwd_weight_workspace_bytes(l.rows, l.C, N);
+    if (need > 0) ws = l.empty({static_cast<int64_t>(need)}, at::kByte);
   }
   const On on(l.device, stream);
-  check_status(conv3d_bwd_weight(x.data_ptr(), d, dw.data_ptr(), with_bias ? db.data_ptr() : nullptr, 1, l.C, 1, 1,
-                                 static_cast<int>(l.rows), N, one, one, zero, CONV3D_TPAD_ZERO, l.code, ws.data_ptr(),
-                                 ws.nbytes(), on.stream));
+  check_status(conv3d_linear_bwd_weight(x.data_ptr(), d, dw.data_ptr(), with_bias ? db.data_ptr() : nullptr, l.rows, l.C,
+                                        N, l.code, ws.defined() ? ws.data_ptr() : nullptr,
+                                        ws.defined() ? ws.nbytes() : 0, on.stream));
   if (!with_bias) return {dw, std::nullopt};
   return {dw, db};
 }

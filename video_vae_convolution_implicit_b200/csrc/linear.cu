@@ -11,6 +11,7 @@
 #include "conv3d.h"
 #include "internal.h"
 #include "linear_kernel.cuh"
+#include "linear_wgrad.cuh"
 
 namespace conv3d_linear {
 
@@ -235,6 +236,83 @@ conv3d_status_t dispatch(const Product& P, cudaStream_t stream) {
   }
 }
 
+// ------------------------------------------------------------------ weight gradient
+
+constexpr int kWgPairs = 74;   // CTA pairs the row ranges are planned for (148 SMs)
+
+// Row ranges: the fewest rounds of units times a range's stages, plus what a
+// unit's epilogue costs (about three stages), a second launch (eight) and the
+// parts' way through memory (a sixth of a stage each).  By sizes alone, so that
+// the workspace and the order of the sums depend on nothing else.
+int wgrad_splits(long long rows, int K, int N) {
+  const long long chunks = (rows + kWgRows - 1) / kWgRows;
+  const long long tiles = static_cast<long long>((N + kWgTile - 1) / kWgTile) * ((K + kWgTile - 1) / kWgTile);
+  long long best = 1, best_cost = -1;
+  for (long long s = 1; s <= chunks && s <= 148; ++s) {
+    const long long rounds = (tiles * s + kWgPairs - 1) / kWgPairs;
+    const long long cost = 6 * (rounds * ((chunks + s - 1) / s + 3) + (s > 1 ? 8 : 0)) + (s > 1 ? tiles * s : 0);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+    if (rounds > 8) break;
+  }
+  const int forced = env_int("CONV3D_LINEAR_WGRAD_SPLITS");   // tuning and tests
+  if (forced >= 1 && forced <= chunks && forced <= best) return forced;
+  return static_cast<int>(best);
+}
+
+size_t wgrad_part_bytes(long long rows, int K, int N) {
+  const int s = wgrad_splits(rows, K, N);
+  if (s == 1) return 0;
+  const size_t tiles_n = (N + kWgTile - 1) / kWgTile, tiles_k = (K + kWgTile - 1) / kWgTile;
+  return s * tiles_n * tiles_k * kWgSlotFloats * sizeof(float);
+}
+size_t wgrad_bias_bytes(long long rows, int K, int N) {
+  const int s = wgrad_splits(rows, K, N);
+  return s == 1 ? 0 : static_cast<size_t>(s) * ((N + kWgTile - 1) / kWgTile) * kWgTile * sizeof(float);
+}
+
+template <bool kBF16>
+conv3d_status_t run_wgrad(const void* x, const void* dy, LinearWgradParams p, cudaStream_t stream) {
+  Device dev;
+  conv3d_status_t st = current_device(dev);
+  if (st != CONV3D_OK) return st;
+  const CUtensorMapDataType dt = kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap map_dy, map_x;
+  const unsigned long long M = p.M, N = p.N, K = p.K;
+  if ((st = encode_matrix(map_dy, dt, dy, N, M, N * 2, 64, kWgRows, CU_TENSOR_MAP_SWIZZLE_128B, "dy")) != CONV3D_OK) return st;
+  if ((st = encode_matrix(map_x, dt, x, K, M, K * 2, 64, kWgRows, CU_TENSOR_MAP_SWIZZLE_128B, "x")) != CONV3D_OK) return st;
+  p.idesc = idesc_f16(kBF16, 2 * BM, kWgTile) | (1u << 15) | (1u << 16);   // both operands MN-major
+  p.idesc_bias = idesc_f16(kBF16, 2 * BM, 32) | (1u << 15) | (1u << 16);
+  p.status = dev.status;
+  p.timeout_ns = wait_limit_ns();
+  p.test_stall = take_stall(p.timeout_ns) ? 1 : 0;
+  const long long units = static_cast<long long>(p.tiles) * p.splits;
+  const int pairs = dev.num_sms / 2;
+  const unsigned grid = 2u * static_cast<unsigned>(units < pairs ? units : pairs);
+  const size_t smem = 1024 + kWgStages * kWgStageBytes + kWgOnesBytes + 8 * (2 * kWgStages + 3);
+  if (plan_log())
+    fprintf(stderr, "libconv3d: channel product weight gradient %d x %d x %d, %d tiles, %d row ranges of %d chunks\n", p.N,
+            p.K, p.M, p.tiles, p.splits, p.chunks);
+  cudaError_t e;
+  if (p.splits == 1) {
+    static std::atomic<unsigned long long> ready{0};
+    auto kern = linear_wgrad_kernel<kBF16, true>;
+    if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
+    e = launch(kern, grid, kWgThreads, smem, 2, stream, map_dy, map_x, p);
+    return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "weight gradient launch");
+  }
+  static std::atomic<unsigned long long> ready{0};
+  auto kern = linear_wgrad_kernel<kBF16, false>;
+  if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
+  e = launch(kern, grid, kWgThreads, smem, 2, stream, map_dy, map_x, p);
+  if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
+  const unsigned sum_blocks = static_cast<unsigned>(p.tiles) * 16 + (p.dbias ? static_cast<unsigned>((p.N + 31) / 32) : 0u);
+  e = launch(linear_wgrad_sum_kernel<kBF16>, sum_blocks, 256, 0, 1, stream, p);
+  return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "weight gradient sum launch");
+}
+
 conv3d_status_t check(long long rows, int K, int N, conv3d_act_t act, conv3d_dtype_t dtype) {
   if (rows < 1 || K < 1 || N < 1) {
     set_error("sizes must be >= 1");
@@ -328,6 +406,65 @@ conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void
   const Product P{dy, w, nullptr, nullptr, dx, q ? const_cast<void*>(codes) : nullptr,
                   q ? const_cast<void*>(exponents) : nullptr, static_cast<int>(rows), N, K, true, act, dtype};
   return dtype == CONV3D_BF16 ? dispatch<true>(P, stream) : dispatch<false>(P, stream);
+}
+
+size_t conv3d_linear_bwd_weight_workspace_bytes(long long rows, int K, int N) {
+  if (rows < 1 || rows > INT_MAX - 512 || K < 1 || N < 1 || K > INT_MAX - 512 || N > INT_MAX - 512) return 0;
+  const size_t b = wgrad_part_bytes(rows, K, N) + wgrad_bias_bytes(rows, K, N);
+  return (b + 255) & ~static_cast<size_t>(255);
+}
+
+conv3d_status_t conv3d_linear_bwd_weight(const void* x, const void* dy, void* dw, void* dbias, long long rows,
+                                         int K, int N, conv3d_dtype_t dtype, void* workspace, size_t ws_bytes,
+                                         struct CUstream_st* stream) {
+  conv3d_status_t st = check(rows, K, N, CONV3D_ACT_NONE, dtype);
+  if (st != CONV3D_OK) return st;
+  if (!x || !dy || !dw) {
+    set_error("x, dy and dw must be non-null");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(x, 16) || !aligned(dy, 16) || !aligned(dw, 16) || !aligned(dbias, 16)) return misaligned();
+  const size_t need = conv3d_linear_bwd_weight_workspace_bytes(rows, K, N);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) {
+    set_error("workspace of %zu bytes required", need);
+    return CONV3D_ERR_WORKSPACE;
+  }
+  if (need > 0 && !aligned(workspace, 256)) {
+    set_error("workspace must be 256-byte aligned");
+    return CONV3D_ERR_ALIGNMENT;
+  }
+  const size_t xb = static_cast<size_t>(rows) * K * 2, yb = static_cast<size_t>(rows) * N * 2,
+               wb = static_cast<size_t>(N) * K * 2, bb = static_cast<size_t>(N) * 2;
+  const void* ws = need > 0 ? workspace : nullptr;
+  if (overlaps(dw, wb, x, xb) || overlaps(dw, wb, dy, yb) || overlaps(dbias, bb, x, xb) || overlaps(dbias, bb, dy, yb) ||
+      overlaps(dw, wb, dbias, bb) || overlaps(ws, need, x, xb) || overlaps(ws, need, dy, yb) ||
+      overlaps(ws, need, dw, wb) || overlaps(ws, need, dbias, bb)) {
+    set_error("x, dy, dw, dbias and the workspace must not overlap");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  LinearWgradParams p{};
+  p.M = static_cast<int>(rows);
+  p.N = N;
+  p.K = K;
+  p.chunks = static_cast<int>((rows + kWgRows - 1) / kWgRows);
+  p.tiles_n = (N + kWgTile - 1) / kWgTile;
+  const long long tiles = static_cast<long long>(p.tiles_n) * ((K + kWgTile - 1) / kWgTile);
+  p.splits = wgrad_splits(rows, K, N);
+  if (tiles * p.splits > INT_MAX / 32) {
+    set_error("problem too large for 32-bit tile indexing");
+    return CONV3D_ERR_UNSUPPORTED;
+  }
+  p.tiles = static_cast<int>(tiles);
+  for (int r = 0; r < 2; ++r) {
+    const int n = (N - r * BM + 63) / 64, k = (K - r * BM + 63) / 64;
+    p.boxes_n[r] = p.tiles_n > 1 || n > 2 ? 2 : n < 0 ? 0 : n;
+    p.boxes_k[r] = K > kWgTile || k > 2 ? 2 : k < 0 ? 0 : k;
+  }
+  p.part = static_cast<float*>(workspace);
+  p.bias_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + wgrad_part_bytes(rows, K, N));
+  p.dw = static_cast<uint16_t*>(dw);
+  p.dbias = static_cast<uint16_t*>(dbias);
+  return dtype == CONV3D_BF16 ? run_wgrad<true>(x, dy, p, stream) : run_wgrad<false>(x, dy, p, stream);
 }
 
 }  // extern "C"
