@@ -283,7 +283,7 @@ conv3d_status_t run_wgrad(const void* x, const void* dy, LinearWgradParams p, cu
   const unsigned long long M = p.M, N = p.N, K = p.K;
   if ((st = encode_matrix(map_dy, dt, dy, N, M, N * 2, 64, kWgRows, CU_TENSOR_MAP_SWIZZLE_128B, "dy")) != CONV3D_OK) return st;
   if ((st = encode_matrix(map_x, dt, x, K, M, K * 2, 64, kWgRows, CU_TENSOR_MAP_SWIZZLE_128B, "x")) != CONV3D_OK) return st;
-  p.idesc = idesc_f16(kBF16, 2 * BM, kWgTile) | (1u << 15) | (1u << 16);   // both operands MN-major
+  p.idesc = idesc_f16(kBF16, 2 * BM, p.kw) | (1u << 15) | (1u << 16);   // both operands MN-major
   p.idesc_bias = idesc_f16(kBF16, 2 * BM, 32) | (1u << 15) | (1u << 16);
   p.status = dev.status;
   p.timeout_ns = wait_limit_ns();
@@ -308,7 +308,7 @@ conv3d_status_t run_wgrad(const void* x, const void* dy, LinearWgradParams p, cu
   if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
   e = launch(kern, grid, kWgThreads, smem, 2, stream, map_dy, map_x, p);
   if (e != cudaSuccess) return cuda_fail(e, "weight gradient launch");
-  const unsigned sum_blocks = static_cast<unsigned>(p.tiles) * 16 + (p.dbias ? static_cast<unsigned>((p.N + 31) / 32) : 0u);
+  const unsigned sum_blocks = static_cast<unsigned>(p.tiles) * 64 + (p.dbias ? static_cast<unsigned>((p.N + 31) / 32) : 0u);
   e = launch(linear_wgrad_sum_kernel<kBF16>, sum_blocks, 256, 0, 1, stream, p);
   return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "weight gradient sum launch");
 }
@@ -450,15 +450,17 @@ conv3d_status_t conv3d_linear_bwd_weight(const void* x, const void* dy, void* dw
   p.tiles_n = (N + kWgTile - 1) / kWgTile;
   const long long tiles = static_cast<long long>(p.tiles_n) * ((K + kWgTile - 1) / kWgTile);
   p.splits = wgrad_splits(rows, K, N);
-  if (tiles * p.splits > INT_MAX / 32) {
+  if (tiles * p.splits > INT_MAX / 128) {
     set_error("problem too large for 32-bit tile indexing");
     return CONV3D_ERR_UNSUPPORTED;
   }
   p.tiles = static_cast<int>(tiles);
+  p.kw = K <= BM ? BM : kWgTile;
+  const int most_k = p.kw / 128;
   for (int r = 0; r < 2; ++r) {
-    const int n = (N - r * BM + 63) / 64, k = (K - r * BM + 63) / 64;
+    const int n = (N - r * BM + 63) / 64, k = (K - r * p.kw / 2 + 63) / 64;
     p.boxes_n[r] = p.tiles_n > 1 || n > 2 ? 2 : n < 0 ? 0 : n;
-    p.boxes_k[r] = K > kWgTile || k > 2 ? 2 : k < 0 ? 0 : k;
+    p.boxes_k[r] = K > kWgTile || k > most_k ? most_k : k < 0 ? 0 : k;
   }
   p.part = static_cast<float*>(workspace);
   p.bias_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + wgrad_part_bytes(rows, K, N));
