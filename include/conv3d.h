@@ -372,7 +372,8 @@ CONV3D_API conv3d_status_t conv3d_bwd_weight_cached(const void* x, const void* p
  * mixes the channels of each pixel by itself.  Activations are matrices
  * [rows, C], one row a pixel (rows = N*D*H*W of an NDHWC tensor) or token, and
  * C (or K and N) a multiple of 8; 16-bit tensors, fp32 statistics and sums, one
- * round-to-nearest-even to the dtype.  Any number of rows from 1 up.  The pages
+ * round-to-nearest-even to the dtype.  Any number of rows from 1 up (the products:
+ * below 2^31 - 65536).  The pages
  * name the operators next to their convolutions (Metal FlashAttention post:
  * GEMM and layer norm shaders with backward passes; LoRA post: training on
  * device, where activation memory is short); the interface is this library's.

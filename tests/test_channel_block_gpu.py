@@ -271,6 +271,30 @@ def test_stream_argument_and_leading_extents():
     assert tuple(a.codes.shape) == (2, 3, 4, 5, 96) and torch.equal(a.codes.view(-1, 96), b.codes)
 
 
+def test_memory_of_a_call_on_a_given_stream_belongs_to_that_stream():
+    """What a call allocates must not go to the current stream's next tensor when it is
+    freed: the kernels that write or read it may still be waiting on theirs."""
+    x, w = rand((64, 64), 35, 0), rand((64, 64), 35, 1, 0.125)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c3.linear(x, w, stream=s)   # the allocator's pools of both streams hold blocks
+    torch.empty_like(x)
+    for call in (lambda: c3.layernorm(x, stream=s), lambda: c3.linear(x, w, stream=s.cuda_stream),
+                 lambda: c3.act8_unpack(c3.act8_pack(x, stream=s), BF, stream=s),
+                 lambda: c3.linear_bwd_weight(x, x, stream=s)[0]):
+        y = call()
+        at = y.data_ptr()
+        del y
+        other = [torch.empty_like(x) for _ in range(4)]
+        assert at not in [t.data_ptr() for t in other]
+    for handle in (0, 1, 2):   # the default streams by CUDA's handles
+        torch.cuda.synchronize()
+        y = c3.linear(x, w, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(y, c3.linear(x, w))
+    sync_ok()
+
+
 def test_refusals_on_the_gpu():
     x = rand((4, 64), 34, 0)
     with pytest.raises(TypeError):

@@ -70,6 +70,14 @@ def test_product_extents(call):
     assert call(rows=1 << 31) == Status.UNSUPPORTED
 
 
+@pytest.mark.parametrize("call", PRODUCTS)
+def test_product_row_limit(call):
+    """A persistent pair's next tile may lie 74 tiles of 256 rows behind the last one: its row stays an int."""
+    assert call(rows=2 ** 31 - 65535) == Status.UNSUPPORTED
+    assert call(rows=2 ** 31 - 18944) == Status.UNSUPPORTED
+    assert c3.linear_bwd_weight_workspace_bytes(2 ** 31 - 65535, 64, 64) == 0
+
+
 def test_layernorm_channel_limit():
     assert ln_fwd(C=8200) == Status.UNSUPPORTED
     assert ln_bwd(C=8200) == Status.UNSUPPORTED
@@ -133,6 +141,15 @@ def test_weight_gradient_workspace():
     assert lin_dw(**big, ws=R + 64) == Status.ALIGNMENT
     assert lin_dw(**big, ws=DY) == Status.INVALID_ARG
     assert c3.linear_bwd_weight_workspace_bytes(0, 64, 64) == 0
+
+
+def test_layernorm_outputs_overlap_nothing():
+    assert ln_fwd(y=G) == Status.INVALID_ARG
+    for name in ("mean", "rstd"):
+        assert ln_fwd(**{name: G + 64}) == Status.INVALID_ARG
+        assert ln_fwd(**{name: B}) == Status.INVALID_ARG
+    assert ln_fwd(q=G, e=E) == Status.INVALID_ARG
+    assert ln_fwd(q=Q, e=B + 16) == Status.INVALID_ARG
 
 
 def test_overlaps():

@@ -46,14 +46,7 @@ struct Val16 {
     __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t*>(&h);
   }
-  static __device__ __forceinline__ void unpack8(const uint4& q, float (&f)[8]) {
-    f[0] = lo(q.x); f[1] = hi(q.x); f[2] = lo(q.y); f[3] = hi(q.y);
-    f[4] = lo(q.z); f[5] = hi(q.z); f[6] = lo(q.w); f[7] = hi(q.w);
-  }
-  static __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
-  }
-  // the same with the eight values as four pairs
+  // eight values as four pairs
   static __device__ __forceinline__ float2 pair(uint32_t w) {
     if constexpr (kBF16) return make_float2(lo(w), hi(w));
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -192,6 +185,7 @@ __device__ __forceinline__ float act_slope_safe(float v) {
   const float s = act_slope<kAct>(fminf(fmaxf(v, -64.0f), 64.0f));
   return v == v ? s : v;
 }
+
 // ------------------------------------------------------------------ checkpoint code
 
 // Magnitude as an unsigned integer: ordered like the magnitudes, with

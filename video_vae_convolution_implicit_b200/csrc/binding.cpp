@@ -106,13 +106,22 @@ Act8 checkpoint(const char* name, const Tensor& codes, const Tensor& exponents, 
   return {c, operand((std::string(name) + ".exponents").c_str(), exponents, device, at::kByte, s)};
 }
 
-// The library's calls run on the operands' device and, unless one is given, its current stream.
+// The call's device and stream, which become the current ones while it lasts, so
+// that what it allocates belongs to the stream its kernels run on: a temporary
+// freed at its end is not handed to other streams before they have.  (1 and 2 are
+// CUDA's names for the default streams, which torch's allocator does not know.)
 struct On {
-  c10::cuda::CUDAGuard guard;
+  c10::cuda::CUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard current;
   CUstream_st* stream;
-  On(const c10::Device& d, const OptStream& s)
-      : guard(d.index()),
-        stream(s.has_value() ? reinterpret_cast<CUstream_st*>(*s) : c10::cuda::getCurrentCUDAStream(d.index()).stream()) {}
+  On(const c10::Device& d, const OptStream& s) : device(d.index()) {
+    if (!s.has_value()) {
+      stream = c10::cuda::getCurrentCUDAStream(d.index()).stream();
+      return;
+    }
+    stream = reinterpret_cast<CUstream_st*>(*s);
+    if (*s != 1 && *s != 2) current.reset_stream(c10::cuda::getStreamFromExternal(stream, d.index()));
+  }
 };
 
 conv3d_act_t act_of(int act) { return static_cast<conv3d_act_t>(act); }
@@ -124,8 +133,8 @@ std::tuple<Tensor, Tensor> new_act8(const Lead& l, int64_t channels) {
 
 std::tuple<Tensor, Tensor> act8_pack(const Tensor& x, const OptStream& stream) {
   const Lead l("x", x);
-  auto [codes, exponents] = new_act8(l, l.C);
   const On on(l.device, stream);
+  auto [codes, exponents] = new_act8(l, l.C);
   check_status(conv3d_act8_pack(x.data_ptr(), codes.data_ptr(), exponents.data_ptr(), l.rows, l.C, l.code, on.stream));
   return {codes, exponents};
 }
@@ -135,6 +144,7 @@ Tensor act8_unpack(const Tensor& codes, const Tensor& exponents, int64_t channel
   TORCH_CHECK_VALUE(codes.is_cuda(), "a must hold CUDA tensors");
   TORCH_CHECK_VALUE(codes.dim() >= 1, "a.codes must be [..., 32 * blocks]");
   const c10::Device device = codes.device();
+  const On on(device, stream);
   const conv3d_dtype_t code = Lead::dtype_code(type);
   at::DimVector shape(codes.sizes().begin(), codes.sizes().end());
   shape.back() = channels;
@@ -144,7 +154,6 @@ Tensor act8_unpack(const Tensor& codes, const Tensor& exponents, int64_t channel
   const int C = Lead::narrow(channels);
   const void* g = gamma.has_value() ? operand("gamma", *gamma, device, type, {channels}) : nullptr;
   const void* b = beta.has_value() ? operand("beta", *beta, device, type, {channels}) : nullptr;
-  const On on(device, stream);
   check_status(conv3d_act8_unpack(a.codes, a.exponents, g, b, act_of(act), out.data_ptr(), C > 0 ? out.numel() / C : 0,
                                   C, code, on.stream));
   return out;
@@ -153,10 +162,10 @@ Tensor act8_unpack(const Tensor& codes, const Tensor& exponents, int64_t channel
 Tensor act8_bwd(const Tensor& dy, const Tensor& codes, const Tensor& exponents, int64_t channels, int act,
                 const OptTensor& dx, const OptStream& stream) {
   const Lead l("dy", dy);
+  const On on(l.device, stream);
   const Act8 a = checkpoint("a", codes, exponents, channels, l.device, dy.sizes());
   operand("dx", dx, l, dy.sizes());
   Tensor out = dx.has_value() ? *dx : l.empty(dy.sizes());
-  const On on(l.device, stream);
   check_status(conv3d_act8_bwd(dy.data_ptr(), a.codes, a.exponents, act_of(act), out.data_ptr(), l.rows, l.C, l.code,
                                on.stream));
   return out;
@@ -167,6 +176,7 @@ py::object layernorm(const Tensor& x, const OptTensor& gamma, const OptTensor& b
                      bool checkpoint8, const OptTensor& y, const OptStream& stream) {
   TORCH_CHECK_VALUE(!(with_stats && checkpoint8), "with_stats and checkpoint8 exclude each other");
   const Lead l("x", x);
+  const On on(l.device, stream);
   const void* g = operand("gamma", gamma, l, {l.C});
   const void* b = operand("beta", beta, l, {l.C});
   operand("y", y, l, x.sizes());
@@ -175,13 +185,10 @@ py::object layernorm(const Tensor& x, const OptTensor& gamma, const OptTensor& b
   if (with_stats || checkpoint8) rstd = l.empty(l.lead(), at::kFloat);
   if (with_stats) mean = l.empty(l.lead(), at::kFloat);
   if (checkpoint8) std::tie(codes, exponents) = new_act8(l, l.C);
-  {
-    const On on(l.device, stream);
-    check_status(conv3d_layernorm_fwd(
-        x.data_ptr(), g, b, out.data_ptr(), with_stats ? mean.data_ptr<float>() : nullptr,
-        with_stats || checkpoint8 ? rstd.data_ptr<float>() : nullptr, checkpoint8 ? codes.data_ptr() : nullptr,
-        checkpoint8 ? exponents.data_ptr() : nullptr, l.rows, l.C, static_cast<float>(eps), l.code, on.stream));
-  }
+  check_status(conv3d_layernorm_fwd(
+      x.data_ptr(), g, b, out.data_ptr(), with_stats ? mean.data_ptr<float>() : nullptr,
+      with_stats || checkpoint8 ? rstd.data_ptr<float>() : nullptr, checkpoint8 ? codes.data_ptr() : nullptr,
+      checkpoint8 ? exponents.data_ptr() : nullptr, l.rows, l.C, static_cast<float>(eps), l.code, on.stream));
   if (checkpoint8) return py::make_tuple(out, codes, exponents, rstd);
   if (with_stats) return py::make_tuple(out, mean, rstd);
   return py::cast(out);
@@ -194,6 +201,7 @@ std::tuple<Tensor, OptTensor, OptTensor> layernorm_bwd(const Tensor& dy, const O
                                                        const OptTensor& dres, bool with_params, const OptTensor& dx,
                                                        const OptTensor& workspace, const OptStream& stream) {
   const Lead l("dy", dy);
+  const On on(l.device, stream);
   const void* r = operand("rstd", rstd, l.device, at::kFloat, l.lead());
   const void *xp = nullptr, *m = nullptr;
   Act8 a{nullptr, nullptr};
@@ -223,7 +231,6 @@ std::tuple<Tensor, OptTensor, OptTensor> layernorm_bwd(const Tensor& dy, const O
     }
     ws_bytes = ws.nbytes();
   }
-  const On on(l.device, stream);
   check_status(conv3d_layernorm_bwd(dy.data_ptr(), xp, static_cast<const float*>(m), a.codes, a.exponents,
                                     static_cast<const float*>(r), g, s, out.data_ptr(),
                                     with_params ? dgamma.data_ptr() : nullptr, with_params ? dbeta.data_ptr() : nullptr,
@@ -245,6 +252,7 @@ const void* weight(const Tensor& w, const Lead& l, int64_t K, int64_t n) {
 py::object linear(const Tensor& x, const Tensor& w, const OptTensor& bias, const OptTensor& residual, int act,
                   bool checkpoint8, const OptTensor& y, const OptStream& stream) {
   const Lead l("x", x);
+  const On on(l.device, stream);
   const void* wp = weight(w, l, l.C, -1);
   const int N = Lead::narrow(w.size(0));
   const at::DimVector shape = l.with(N);
@@ -254,12 +262,9 @@ py::object linear(const Tensor& x, const Tensor& w, const OptTensor& bias, const
   Tensor out = y.has_value() ? *y : l.empty(shape);
   Tensor codes, exponents;
   if (checkpoint8) std::tie(codes, exponents) = new_act8(l, N);
-  {
-    const On on(l.device, stream);
-    check_status(conv3d_linear_fwd(x.data_ptr(), wp, b, r, out.data_ptr(), checkpoint8 ? codes.data_ptr() : nullptr,
-                                   checkpoint8 ? exponents.data_ptr() : nullptr, l.rows, l.C, N, act_of(act), l.code,
-                                   on.stream));
-  }
+  check_status(conv3d_linear_fwd(x.data_ptr(), wp, b, r, out.data_ptr(), checkpoint8 ? codes.data_ptr() : nullptr,
+                                 checkpoint8 ? exponents.data_ptr() : nullptr, l.rows, l.C, N, act_of(act), l.code,
+                                 on.stream));
   if (checkpoint8) return py::make_tuple(out, codes, exponents);
   return py::cast(out);
 }
@@ -267,6 +272,7 @@ py::object linear(const Tensor& x, const Tensor& w, const OptTensor& bias, const
 Tensor linear_bwd_data(const Tensor& dy, const Tensor& w, const OptTensor& codes, const OptTensor& exponents,
                        int64_t channels, int act, const OptTensor& dx, const OptStream& stream) {
   const Lead l("dy", dy);
+  const On on(l.device, stream);
   TORCH_CHECK_VALUE(w.dim() >= 1, "w must be [N, K]");
   const int K = Lead::narrow(w.size(-1));
   const void* wp = weight(w, l, K, l.C);
@@ -277,7 +283,6 @@ Tensor linear_bwd_data(const Tensor& dy, const Tensor& w, const OptTensor& codes
                     "the derivative of an activation needs the checkpoint of its argument");
   operand("dx", dx, l, shape);
   Tensor out = dx.has_value() ? *dx : l.empty(shape);
-  const On on(l.device, stream);
   check_status(conv3d_linear_bwd_data(dy.data_ptr(), wp, a.codes, a.exponents, act_of(act), out.data_ptr(), l.rows, K,
                                       l.C, l.code, on.stream));
   return out;
@@ -286,6 +291,7 @@ Tensor linear_bwd_data(const Tensor& dy, const Tensor& w, const OptTensor& codes
 std::tuple<Tensor, OptTensor> linear_bwd_weight(const Tensor& x, const Tensor& dy, bool with_bias,
                                                 const OptTensor& workspace, const OptStream& stream) {
   const Lead l("x", x);
+  const On on(l.device, stream);
   TORCH_CHECK_VALUE(dy.dim() >= 1, "dy must be [..., N]");
   const int N = Lead::narrow(dy.size(-1));
   const void* d = operand("dy", dy, l.device, l.type, l.with(N));
@@ -299,7 +305,6 @@ std::tuple<Tensor, OptTensor> linear_bwd_weight(const Tensor& x, const Tensor& d
     const size_t need = conv3d_linear_bwd_weight_workspace_bytes(l.rows, l.C, N);
     if (need > 0) ws = l.empty({static_cast<int64_t>(need)}, at::kByte);
   }
-  const On on(l.device, stream);
   check_status(conv3d_linear_bwd_weight(x.data_ptr(), d, dw.data_ptr(), with_bias ? db.data_ptr() : nullptr, l.rows, l.C,
                                         N, l.code, ws.defined() ? ws.data_ptr() : nullptr,
                                         ws.defined() ? ws.nbytes() : 0, on.stream));

@@ -143,9 +143,6 @@ template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
 __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParams p) {
   using H = Val16<kBF16>;
   constexpr uint32_t kSlot = R * V * T * 16;
-  // gamma and beta as fp32: in registers, or in shared memory behind the ring
-  // ([2][C] floats) where a thread holds more than three vectors
-  constexpr bool kRegParams = V <= 3;
   extern __shared__ __align__(16) uint8_t ring_mem[];
   __shared__ float red[G > 32 ? 2 * (T / 32) * R : 1];
   int flip = 0;
@@ -155,7 +152,6 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
   const float inv_c = 1.0f / static_cast<float>(p.C);
   const Walk<G, R, T> walk(p.rows);
   const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16u;
-  const uint32_t params = smem_addr(ring_mem) + D * kSlot;
   bool in[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) in[i] = l + i * G < vecs;
@@ -177,25 +173,16 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
   };
 #pragma unroll
   for (int k = 0; k < D - 1; ++k) fetch(k, k);
-  float2 gm[kRegParams ? V : 1][4], bt[kRegParams ? V : 1][4];
-  if constexpr (kRegParams) {
+  float2 gm[V][4], bt[V][4];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+  for (int i = 0; i < V; ++i) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        gm[i][e] = both(1.0f);
-        bt[i][e] = both(0.0f);
-      }
-      if (p.gamma && in[i]) H::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma) + l + i * G), gm[i]);
-      if (p.beta && in[i]) H::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta) + l + i * G), bt[i]);
+    for (int e = 0; e < 4; ++e) {
+      gm[i][e] = both(1.0f);
+      bt[i][e] = both(0.0f);
     }
-  } else {
-    for (int c = threadIdx.x; c < p.C; c += T) {
-      const float g = p.gamma ? H::lo(p.gamma[c]) : 1.0f, b = p.beta ? H::lo(p.beta[c]) : 0.0f;
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(params + c * 4u), "f"(g) : "memory");
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(params + (p.C + c) * 4u), "f"(b) : "memory");
-    }
-    __syncthreads();
+    if (p.gamma && in[i]) H::unpack8(__ldg(reinterpret_cast<const uint4*>(p.gamma) + l + i * G), gm[i]);
+    if (p.beta && in[i]) H::unpack8(__ldg(reinterpret_cast<const uint4*>(p.beta) + l + i * G), bt[i]);
   }
   char* out = reinterpret_cast<char*>(p.y) + first;
   long long row0 = walk.first;
@@ -268,20 +255,8 @@ __global__ void __launch_bounds__(T, kOcc) layernorm_fwd_kernel(const LnFwdParam
           }
         }
         if (in[i] && live) {
-          if constexpr (kRegParams) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = fma2(f[e], gm[i][e], bt[i][e]);
-          } else {
-            const uint32_t at = params + (l + i * G) * 32u;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 g = ld_shared_v4(at + h * 16u), b = ld_shared_v4(at + p.C * 4u + h * 16u);
-              f[2 * h] = fma2(f[2 * h], make_float2(__uint_as_float(g.x), __uint_as_float(g.y)),
-                              make_float2(__uint_as_float(b.x), __uint_as_float(b.y)));
-              f[2 * h + 1] = fma2(f[2 * h + 1], make_float2(__uint_as_float(g.z), __uint_as_float(g.w)),
-                                  make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
-            }
-          }
+          for (int e = 0; e < 4; ++e) f[e] = fma2(f[e], gm[i][e], bt[i][e]);
           st_global_v4(out + r * per_row + i * (G * 16), H::pack8(f));
         }
       }
@@ -797,7 +772,7 @@ cudaError_t run_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
   static std::atomic<unsigned long long> ready{0};
   auto kern = layernorm_fwd_kernel<kBF16, G, V, R, T, D, kOcc, kCkpt>;
   const unsigned blocks = blocks_for(p.rows, rows_per_step(G, R, T), static_cast<long long>(sms) * kOcc);
-  const size_t smem = static_cast<size_t>(D) * R * V * T * 16 + (V <= 3 ? 0 : 2 * p.C * sizeof(float));
+  const size_t smem = static_cast<size_t>(D) * R * V * T * 16;
   const cudaError_t e = allow_smem(kern, ready, smem);
   if (e != cudaSuccess) return e;
   return launch(kern, blocks, T, smem, 1, stream, p);
@@ -819,8 +794,7 @@ cudaError_t dispatch_fwd(const LnFwdParams& p, int sms, cudaStream_t stream) {
 }
 
 // The ring is as deep as shared memory allows kOcc blocks an SM, which differs
-// with and without dres: with three steps instead of five, 16381 x 520 from x
-// took 18.6 us against DEEPER.
+// with and without dres.
 template <bool kBF16, int G, int V, int R, int T, int D, int kOcc, bool kCkpt>
 cudaError_t run_bwd_depth(const LnBwdParams& p, unsigned blocks, cudaStream_t stream) {
   static std::atomic<unsigned long long> ready{0};
@@ -911,12 +885,14 @@ conv3d_status_t conv3d_layernorm_fwd(const void* x, const void* gamma, const voi
     return misaligned();
   const size_t n = static_cast<size_t>(rows) * C * 2, cb = act8_code_bytes(rows, C),
                sb = act8_scale_bytes(rows, C), rb = static_cast<size_t>(rows) * 4, pb = C * 2ull;
-  if ((y != x && overlaps(y, n, x, n)) || overlaps(y, n, gamma, pb) || overlaps(y, n, beta, pb) ||
-      overlaps(codes, cb, x, n) || overlaps(codes, cb, y, n) || overlaps(exponents, sb, x, n) ||
-      overlaps(exponents, sb, y, n) || overlaps(codes, cb, exponents, sb) || overlaps(mean, rb, y, n) ||
-      overlaps(rstd, rb, y, n) || overlaps(mean, rb, x, n) || overlaps(rstd, rb, x, n) ||
-      overlaps(mean, rb, rstd, rb) || overlaps(mean, rb, codes, cb) || overlaps(rstd, rb, codes, cb) ||
-      overlaps(mean, rb, exponents, sb) || overlaps(rstd, rb, exponents, sb))
+  const struct { const void* p; size_t n; } outs[] = {{y, n}, {codes, cb}, {exponents, sb}, {mean, rb}, {rstd, rb}},
+                                            ins[] = {{x, n}, {gamma, pb}, {beta, pb}};
+  bool clash = false;
+  for (const auto& o : outs) {
+    for (const auto& i : ins) clash = clash || (overlaps(o.p, o.n, i.p, i.n) && !(o.p == y && i.p == x && x == y));
+    for (const auto& q : outs) clash = clash || (&o != &q && overlaps(o.p, o.n, q.p, q.n));
+  }
+  if (clash)
     return overlapping("y must be exactly x or not overlap it; the other outputs must overlap nothing");
   Device dev;
   if ((st = current_device(dev)) != CONV3D_OK) return st;

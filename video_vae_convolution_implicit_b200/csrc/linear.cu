@@ -236,6 +236,9 @@ conv3d_status_t dispatch(const Product& P, cudaStream_t stream) {
   }
 }
 
+// A persistent pair's next tile may lie this many rows behind the last one.
+constexpr long long kMaxRows = INT_MAX - 65536;
+
 // ------------------------------------------------------------------ weight gradient
 
 constexpr int kWgPairs = 74;   // CTA pairs the row ranges are planned for (148 SMs)
@@ -330,7 +333,7 @@ conv3d_status_t check(long long rows, int K, int N, conv3d_act_t act, conv3d_dty
     set_error("K and N must be multiples of 8 (got %d, %d)", K, N);
     return CONV3D_ERR_UNSUPPORTED;
   }
-  if (rows > INT_MAX - 512 || K > INT_MAX - 512 || N > INT_MAX - 512) {
+  if (rows > kMaxRows || K > INT_MAX - 512 || N > INT_MAX - 512) {
     set_error("problem too large for 32-bit tile indexing");
     return CONV3D_ERR_UNSUPPORTED;
   }
@@ -409,7 +412,7 @@ conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void
 }
 
 size_t conv3d_linear_bwd_weight_workspace_bytes(long long rows, int K, int N) {
-  if (rows < 1 || rows > INT_MAX - 512 || K < 1 || N < 1 || K > INT_MAX - 512 || N > INT_MAX - 512) return 0;
+  if (rows < 1 || rows > kMaxRows || K < 1 || N < 1 || K > INT_MAX - 512 || N > INT_MAX - 512) return 0;
   const size_t b = wgrad_part_bytes(rows, K, N) + wgrad_bias_bytes(rows, K, N);
   return (b + 255) & ~static_cast<size_t>(255);
 }

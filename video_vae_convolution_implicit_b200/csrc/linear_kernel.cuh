@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         }
         __syncwarp();
       }
-      if (!wait_bounded(tfull_bar + 8 * acc, (local >> 1) & 1, ctl, true)) break;
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar + 8 * acc, (local >> 1) & 1, ctl, true))) break;   // the warp leaves as one
       tc_fence_after();
       const uint32_t t_row =
           tmem_base + ((quarter * 32u) << 16) + acc * static_cast<uint32_t>(p.BN) + share * nj * 32;
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
   } else if (warp < 6) {
     const uint32_t quarter = warp & 3;
     // (not watching the abort flag: the commit above always arrives)
-    if (wait_bounded(tfull_bar, 0, ctl, false) && !s_abort) {
+    if (__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar, 0, ctl, false) && !s_abort)) {   // the warp as one
       tc_fence_after();
       const uint32_t t_row = tmem_base + ((quarter * 32u) << 16);
       for (int j = 0; j < p.BN; j += 16) {

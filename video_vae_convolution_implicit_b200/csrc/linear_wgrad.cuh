@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
       const Unit w = unit_of(u);
       const int n = w.n0 + static_cast<int>(rank) * BM + r;
       const bool rows_live = n - static_cast<int>(lane) < p.N;   // some row of this warp is a channel of dy
-      if (!wait_bounded(tfull_bar, phase, ctl, true)) break;
+      if (!__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar, phase, ctl, true))) break;   // the warp leaves as one
       tc_fence_after();
       if (p.dbias != nullptr && w.k0 == 0 && half == 0 && rows_live) {
         uint32_t sum;
