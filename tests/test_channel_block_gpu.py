@@ -1,6 +1,7 @@
 """The channel-wise operators as they are used together: the channel MLP block and its backward pass from 8-bit
 checkpoints, the autograd wrappers against 64-bit formulas and differences, graphs, streams, launch counts and the
 bounded waits of the product kernels."""
+import threading
 import time
 
 import pytest
@@ -269,6 +270,36 @@ def test_stream_argument_and_leading_extents():
     sync_ok()
     assert tuple(z.shape) == (2, 3, 4, 5, 96) and torch.equal(z.view(-1, 96), flat)
     assert tuple(a.codes.shape) == (2, 3, 4, 5, 96) and torch.equal(a.codes.view(-1, 96), b.codes)
+
+
+def test_first_call_of_a_thread():
+    """A thread without a CUDA context of its own (autograd's, a worker) makes a call whose first step
+    on the device is a tensor map: the driver needs a context to encode it."""
+    x, w = rand((64, 64), 38, 0), rand((64, 64), 38, 1, 0.125)
+    clip, kernel = rand((1, 2, 8, 8, 64), 38, 2), rand((64, 1, 3, 3, 64), 38, 3, 0.04)
+    calls = [lambda: c3.linear(x, w), lambda: c3.linear_bwd_data(x, w), lambda: c3.linear_bwd_weight(x, x)[0],
+             lambda: c3.conv3d(clip, kernel)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    for call, expect in zip(calls, want):
+        got = []
+
+        def work():
+            try:
+                got.append(call())
+            except Exception as e:   # noqa: BLE001 -- shown by the assertion below
+                got.append(e)
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert torch.is_tensor(got[0]), got[0]
+        assert torch.equal(got[0], expect)
+    a, b = x.clone().requires_grad_(), w.clone().requires_grad_()
+    c3.linear_autograd(a, b).backward(x)   # autograd's thread: the first call is the product
+    assert torch.equal(a.grad, c3.linear_bwd_data(x, w))
+    sync_ok()
 
 
 def test_memory_of_a_call_on_a_given_stream_belongs_to_that_stream():

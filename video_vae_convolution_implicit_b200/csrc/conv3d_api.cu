@@ -474,6 +474,13 @@ conv3d_status_t device_state(DeviceState*& out, int& dev) {
     set_error("device ordinal %d out of range", dev);
     return CONV3D_ERR_CUDA;
   }
+  // A thread that has made no CUDA call yet (autograd's, a user's worker) has no
+  // current context, which the tensor-map encoder needs; cudaSetDevice makes it so.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if ((e = cudaSetDevice(dev)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState& s = g_dev[dev];
   if (!s.init) {
