@@ -466,10 +466,12 @@ CONV3D_API conv3d_status_t conv3d_linear_fwd(const void* x, const void* w, const
  * conv3d_linear_bwd_data -- dx = (dy w) * act'(v), dy [rows, N], w [N, K], dx
  * [rows, K], v the checkpoint [rows, K] of what the activation that produced x
  * was applied to (x = act(v)); CONV3D_ACT_NONE: dx = dy w, codes and exponents
- * unused.  w is read as it lies; no workspace.
+ * unused.  With an activation x itself, which the weight gradient needs, may be
+ * asked for as well (x [rows, K] or NULL): conv3d_act8_unpack's bits, from the
+ * same read of the checkpoint.  w is read as it lies; no workspace.
  */
 CONV3D_API conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void* codes,
-                                                  const void* exponents, conv3d_act_t act, void* dx,
+                                                  const void* exponents, conv3d_act_t act, void* dx, void* x,
                                                   long long rows, int K, int N, conv3d_dtype_t dtype,
                                                   struct CUstream_st* stream);
 

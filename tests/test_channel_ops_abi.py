@@ -35,8 +35,8 @@ def lin(x=X, w=W, bias=B, res=R, y=Y, q=None, e=None, rows=4, K=64, N=64, act=0,
     return c3.linear_fwd_ptr(x, w, bias, res, y, q, e, rows, K, N, act, dt, None)
 
 
-def lin_bwd(dy=DY, w=W, q=None, e=None, act=0, dx=DX, rows=4, K=64, N=64, dt=c3.BF16):
-    return c3.linear_bwd_data_ptr(dy, w, q, e, act, dx, rows, K, N, dt, None)
+def lin_bwd(dy=DY, w=W, q=None, e=None, act=0, dx=DX, x=None, rows=4, K=64, N=64, dt=c3.BF16):
+    return c3.linear_bwd_data_ptr(dy, w, q, e, act, dx, x, rows, K, N, dt, None)
 
 
 def lin_dw(x=X, dy=DY, dw=W, db=B, rows=4, K=64, N=64, dt=c3.BF16, ws=R, ws_bytes=1 << 30):
@@ -181,6 +181,11 @@ def test_overlaps():
     assert lin(q=R, e=E) == Status.INVALID_ARG
     assert lin_bwd(dx=DY) == Status.INVALID_ARG
     assert lin_bwd(act=1, q=DX, e=E) == Status.INVALID_ARG
+    assert lin_bwd(act=1, q=Q, e=E, x=DX) == Status.INVALID_ARG
+    assert lin_bwd(act=1, q=Q, e=E, x=DY + 16) == Status.INVALID_ARG
+    assert lin_bwd(act=1, q=Q, e=E, x=E) == Status.INVALID_ARG
+    assert lin_bwd(act=1, q=Q, e=E, x=X + 8) == Status.ALIGNMENT
+    assert lin_bwd(act=0, q=Q, e=E, x=X) == Status.INVALID_ARG
 
 
 def test_python_checks_need_no_gpu():

@@ -390,6 +390,33 @@ def test_linear_data_gradient(M, K, N, dtype, kernel, monkeypatch):
         want = plain * s
         bound = off * (s.abs() + ref.slope_error(v, act)) + plain.abs() * ref.slope_error(v, act) * (act != 0)
         ref.check(dx, want, ref.rounding(want, dt) * 1.01 + bound + 2.0 ** -23 * want.abs(), "dx")
+        if act:
+            again, x = c3.linear_bwd_data(dy, w, pre, act, with_x=True)
+            sync_ok()
+            assert torch.equal(again, dx) and torch.equal(x, c3.act8_unpack(pre, dt, act=act))
+
+
+@pytest.mark.parametrize("act", [1, 2])
+@pytest.mark.parametrize("M", [37, 700])
+def test_linear_data_gradient_recomputes_any_checkpoint(M, act):
+    """Blocks whose values pass 64 (where the derivative's argument is cut off and the
+    value's is not), tiny ones, and ones that hold an infinity or a NaN."""
+    K, N = 1032, 256
+    v = rand((M, K), 18, 0, 1.5)
+    v[1::7] *= 100.0
+    v[2::7] *= 1e30
+    v[3::7] *= 1e-37
+    v[4::7, 40] = float("inf")
+    v[5::7, 1031] = float("nan")
+    v[6::7, ::3] *= 50.0
+    pre = c3.act8_pack(v)
+    dy, w = rand((M, N), 18, 1), rand((N, K), 18, 2, K ** -0.5)
+    dx = c3.linear_bwd_data(dy, w, pre, act)
+    again, x = c3.linear_bwd_data(dy, w, pre, act, with_x=True)
+    sync_ok()
+    torch.testing.assert_close(again, dx, rtol=0, atol=0, equal_nan=True)
+    torch.testing.assert_close(x, c3.act8_unpack(pre, v.dtype, act=act), rtol=0, atol=0, equal_nan=True)
+    assert torch.isnan(x[4::7, 32:64]).all() and torch.isfinite(x[4::7, :32]).all()
 
 
 @pytest.mark.parametrize("splits", ["", "1", "2", "5"])

@@ -159,9 +159,7 @@ _lib.conv3d_act8_bwd.argtypes = [_vp] * 3 + [_c, _vp, _ll, _c, _c, _vp]
 _lib.conv3d_linear_fwd.restype = _c
 _lib.conv3d_linear_fwd.argtypes = [_vp] * 7 + [_ll, _c, _c, _c, _c, _vp]
 _lib.conv3d_linear_bwd_data.restype = _c
-_lib.conv3d_linear_bwd_data.argtypes = [_vp] * 4 + [_c, _vp, _ll, _c, _c, _c, _vp]
-
-
+_lib.conv3d_linear_bwd_data.argtypes = [_vp] * 4 + [_c, _vp, _vp, _ll, _c, _c, _c, _vp]
 _lib.conv3d_linear_bwd_weight.restype = _c
 _lib.conv3d_linear_bwd_weight.argtypes = [_vp] * 4 + [_ll, _c, _c, _c, _vp, ctypes.c_size_t, _vp]
 _lib.conv3d_linear_bwd_weight_workspace_bytes.restype = ctypes.c_size_t
@@ -634,9 +632,9 @@ def linear_fwd_ptr(x, w, bias, residual, y, codes, exponents, rows, K, N, act, d
     return _lib.conv3d_linear_fwd(x, w, bias, residual, y, codes, exponents, rows, K, N, act, dtype, stream)
 
 
-def linear_bwd_data_ptr(dy, w, codes, exponents, act, dx, rows, K, N, dtype, stream) -> int:
+def linear_bwd_data_ptr(dy, w, codes, exponents, act, dx, x, rows, K, N, dtype, stream) -> int:
     """Raw-pointer call of conv3d_linear_bwd_data; returns the status code."""
-    return _lib.conv3d_linear_bwd_data(dy, w, codes, exponents, act, dx, rows, K, N, dtype, stream)
+    return _lib.conv3d_linear_bwd_data(dy, w, codes, exponents, act, dx, x, rows, K, N, dtype, stream)
 
 
 def linear_bwd_weight_ptr(x, dy, dw, dbias, rows, K, N, dtype, workspace, ws_bytes, stream) -> int:
@@ -724,11 +722,13 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, act: int 
 
 
 def linear_bwd_data(dy: torch.Tensor, w: torch.Tensor, pre: Act8 | None = None, act: int = ACT_NONE,
-                    dx: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                    dx: torch.Tensor | None = None, with_x: bool = False, stream=None):
     """dx = (dy w) * act'(pre) for dy [..., N], w [N, K]: the gradient of x, or, with the
-    checkpoint ``pre`` of what ``act`` was applied to (x = act(pre)), of that argument."""
+    checkpoint ``pre`` of what ``act`` was applied to (x = act(pre)), of that argument.
+    ``with_x`` returns (dx, x): act8_unpack's x, for the weight gradient, in the same pass."""
     a = pre if pre is not None else (None, None, 0)
-    return _channel.linear_bwd_data(dy, w, a[0], a[1], a[2], act, dx, _on(stream))
+    dx, x = _channel.linear_bwd_data(dy, w, a[0], a[1], a[2], act, dx, with_x, _on(stream))
+    return (dx, x) if with_x else dx
 
 
 def linear_bwd_weight(x: torch.Tensor, dy: torch.Tensor, with_bias: bool = True,
@@ -764,8 +764,9 @@ def channel_mlp_bwd(dy: torch.Tensor, saved: ChannelMlpSaved, gamma, beta, w1: t
     """(dx, dgamma, dbeta, dw1, db1, dw2, db2) of :func:`channel_mlp` from its checkpoints.
 
     The two inputs that the weight gradients need are recomputed from the
-    checkpoints (one pass each); act' rides in the epilogue of dy w2 and the skip
-    connection's gradient in the layer norm's.
+    checkpoints: the activation by the product dy w2, whose epilogue reads them for
+    act' (:func:`linear_bwd_data`), the normalised input by a pass of its own.  The
+    skip connection's gradient rides in the layer norm's.
     """
     x, pre = saved.xhat, saved.pre
     return _channel.channel_mlp_bwd(dy, x[0], x[1], x[2], saved.rstd, pre[0], pre[1], pre[2], gamma, beta, w1, w2, act,

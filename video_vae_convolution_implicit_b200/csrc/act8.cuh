@@ -176,6 +176,23 @@ __device__ __forceinline__ float2 act_slope_of_half(float2 h) {
   }
 }
 
+// The derivative and the value, h + h t, from one tanh.  `hc` is h brought back
+// to +-32 (the same h where the block's step keeps it there).
+template <int kAct>
+__device__ __forceinline__ float2 act_slope_and_value(float2 h, float2 hc, float2& value) {
+  if constexpr (kAct == kActSilu) {
+    const float2 t = tanh_hw2(hc);
+    value = fma2(h, t, h);
+    return fma2(mul2(hc, both(-0.5f)), fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
+  } else {
+    const float2 h2 = mul2(hc, hc);
+    const float2 t = tanh_hw2(mul2(hc, fma2(both(8.0f * kGeluC), h2, both(2.0f * kGeluA))));
+    value = fma2(h, t, h);
+    const float2 c = mul2(hc, fma2(both(-12.0f * kGeluC), h2, both(-kGeluA)));
+    return fma2(c, fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
+  }
+}
+
 // Beyond |v| = 64 both derivatives are 0 or 1, t has long been -1 or 1 exactly,
 // and v^3 may overflow, which would leave infinity times zero: such arguments
 // are brought back to +-64.  (NaN stays: fminf and fmaxf would drop it.)
@@ -257,19 +274,24 @@ __device__ __forceinline__ void a8_decode4(uint32_t w, float step, float2* v) {
   v[1] = mul2(add2(make_float2(f[2], f[3]), both(-8388736.0f)), both(step));
 }
 
-// Halves of the values of 4 N codes under exponent byte b, brought back to +-32
-// (see act_slope_safe).  With a step of at most 1/2 no value exceeds 64, and the
-// subtraction and the product are one exact fused operation; a block marked as
-// not finite (NaN step) goes the same way and stays NaN.
-template <int N>
-__device__ __forceinline__ void a8_decode_halves(const uint32_t (&w)[N], uint32_t b, float2 (&h)[2 * N]) {
-  const float half = 0.5f * a8_step(b);
-  if (half > 0.25f) {
+// Whether halves of values under exponent byte b can lie outside +-32: not with a
+// step of at most 1/2, nor in a block marked as not finite (NaN step).
+__device__ __forceinline__ bool a8_wide(float half) { return half > 0.25f; }
+__device__ __forceinline__ float2 a8_narrow(float2 h) {
+  return make_float2(fminf(fmaxf(h.x, -32.0f), 32.0f), fminf(fmaxf(h.y, -32.0f), 32.0f));
+}
+
+// Halves of the values of 4 N codes, `half` the half step, brought back to +-32
+// (see act_slope_safe) if kNarrow.  Where the step is at most 1/2 the subtraction and
+// the product are one exact fused operation; NaN steps go the same way and stay NaN.
+template <bool kNarrow, int N>
+__device__ __forceinline__ void a8_decode_halves(const uint32_t (&w)[N], float half, float2 (&h)[2 * N]) {
+  if (a8_wide(half)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) a8_decode4(w[i], half, h + 2 * i);
+    if constexpr (kNarrow)
 #pragma unroll
-    for (int e = 0; e < 2 * N; ++e)
-      h[e] = make_float2(fminf(fmaxf(h[e].x, -32.0f), 32.0f), fminf(fmaxf(h[e].y, -32.0f), 32.0f));
+      for (int e = 0; e < 2 * N; ++e) h[e] = a8_narrow(h[e]);
     return;
   }
   const float off = -8388736.0f * half;

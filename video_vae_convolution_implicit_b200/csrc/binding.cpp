@@ -269,8 +269,10 @@ py::object linear(const Tensor& x, const Tensor& w, const OptTensor& bias, const
   return py::cast(out);
 }
 
-Tensor linear_bwd_data(const Tensor& dy, const Tensor& w, const OptTensor& codes, const OptTensor& exponents,
-                       int64_t channels, int act, const OptTensor& dx, const OptStream& stream) {
+// (dx, x or None)
+std::tuple<Tensor, OptTensor> linear_bwd_data(const Tensor& dy, const Tensor& w, const OptTensor& codes, const OptTensor& exponents,
+                       int64_t channels, int act, const OptTensor& dx, bool with_x,
+                       const OptStream& stream) {
   const Lead l("dy", dy);
   const On on(l.device, stream);
   TORCH_CHECK_VALUE(w.dim() >= 1, "w must be [N, K]");
@@ -281,11 +283,15 @@ Tensor linear_bwd_data(const Tensor& dy, const Tensor& w, const OptTensor& codes
   if (codes.has_value()) a = checkpoint("pre", *codes, exponents.value(), channels, l.device, shape);
   TORCH_CHECK_VALUE(codes.has_value() || act == CONV3D_ACT_NONE,
                     "the derivative of an activation needs the checkpoint of its argument");
+  TORCH_CHECK_VALUE(!with_x || act != CONV3D_ACT_NONE, "with_x recomputes what an activation made");
   operand("dx", dx, l, shape);
   Tensor out = dx.has_value() ? *dx : l.empty(shape);
-  check_status(conv3d_linear_bwd_data(dy.data_ptr(), wp, a.codes, a.exponents, act_of(act), out.data_ptr(), l.rows, K,
-                                      l.C, l.code, on.stream));
-  return out;
+  Tensor x;
+  if (with_x) x = l.empty(shape);
+  check_status(conv3d_linear_bwd_data(dy.data_ptr(), wp, a.codes, a.exponents, act_of(act), out.data_ptr(),
+                                      with_x ? x.data_ptr() : nullptr, l.rows, K, l.C, l.code, on.stream));
+  if (!with_x) return {out, std::nullopt};
+  return {out, x};
 }
 
 std::tuple<Tensor, OptTensor> linear_bwd_weight(const Tensor& x, const Tensor& dy, bool with_bias,
@@ -318,13 +324,17 @@ py::tuple channel_mlp_bwd(const Tensor& dy, const Tensor& x_codes, const Tensor&
                           const OptTensor& gamma, const OptTensor& beta, const Tensor& w1, const Tensor& w2, int act,
                           const OptStream& stream) {
   const at::ScalarType type = dy.scalar_type();
-  Tensor h = act8_unpack(pre_codes, pre_exponents, hidden, type, std::nullopt, std::nullopt, act, std::nullopt, stream);
-  auto [dw2, db2] = linear_bwd_weight(h, dy, true, std::nullopt, stream);
-  // h and n have been read by the time their gradients take their place
-  Tensor dpre = linear_bwd_data(dy, w2, pre_codes, pre_exponents, hidden, act, h, stream);
+  const bool curved = act != CONV3D_ACT_NONE;   // then the product with act' leaves the activation h too
+  auto [dpre, h] = linear_bwd_data(dy, w2, pre_codes, pre_exponents, hidden, act, std::nullopt, curved, stream);
+  if (!curved)
+    h = act8_unpack(pre_codes, pre_exponents, hidden, type, std::nullopt, std::nullopt, act, std::nullopt, stream);
+  auto [dw2, db2] = linear_bwd_weight(*h, dy, true, std::nullopt, stream);
+  h.reset();
   Tensor n = act8_unpack(x_codes, x_exponents, channels, type, gamma, beta, CONV3D_ACT_NONE, std::nullopt, stream);
   auto [dw1, db1] = linear_bwd_weight(n, dpre, true, std::nullopt, stream);
-  Tensor dn = linear_bwd_data(dpre, w1, std::nullopt, std::nullopt, 0, CONV3D_ACT_NONE, n, stream);
+  // n has been read by the time its gradient takes its place
+  Tensor dn = std::get<0>(
+      linear_bwd_data(dpre, w1, std::nullopt, std::nullopt, 0, CONV3D_ACT_NONE, n, false, stream));
   auto [dx, dgamma, dbeta] = layernorm_bwd(dn, std::nullopt, std::nullopt, x_codes, x_exponents, channels, rstd, gamma,
                                            dy, true, dn, std::nullopt, stream);
   return py::make_tuple(dx, dgamma, dbeta, dw1, db1, dw2, db2);

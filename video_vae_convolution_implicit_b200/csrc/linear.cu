@@ -29,6 +29,7 @@ struct Product {
   void* out;
   void* codes;
   void* exponents;
+  void* value;        // gradient: act(checkpoint), also written
   int M, K, N;
   bool bwd;
   int act;
@@ -147,7 +148,7 @@ conv3d_status_t allow_smem(K kern, std::atomic<unsigned long long>& done, int by
   return CONV3D_OK;
 }
 
-template <bool kBF16, bool kBwd, int kAct, bool kQ>
+template <bool kBF16, bool kBwd, int kAct, bool kQ, bool kValue = false>
 conv3d_status_t run(const Product& P, cudaStream_t stream) {
   Device dev;
   conv3d_status_t st = current_device(dev);
@@ -169,6 +170,7 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
   p.out = static_cast<uint16_t*>(P.out);
   p.codes = static_cast<uint8_t*>(P.codes);
   p.exponents = static_cast<uint8_t*>(P.exponents);
+  p.value = static_cast<uint16_t*>(P.value);
   p.blocks = (P.N + 31) / 32;
   p.status = dev.status;
   p.timeout_ns = wait_limit_ns();
@@ -193,7 +195,7 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
     p.tmem_cols = pow2(2 * L.BN);
     p.idesc = idesc_f16(kBF16, 2 * BM, L.BN) | (kBwd ? 1u << 16 : 0u);   // bit 16: B is MN-major
     static std::atomic<unsigned long long> ready{0};
-    auto kern = linear_pair_kernel<kBF16, kBwd, kAct, kQ>;
+    auto kern = linear_pair_kernel<kBF16, kBwd, kAct, kQ, kValue>;
     if ((st = allow_smem(kern, ready, dev.max_smem_optin - 64)) != CONV3D_OK) return st;
     const unsigned grid = 2u * static_cast<unsigned>(L.units);
     const cudaError_t e = launch(kern, grid, kLinThreads, L.smem, 2, stream, map_a, map_w, p);
@@ -224,6 +226,8 @@ conv3d_status_t dispatch(const Product& P, cudaStream_t stream) {
   const bool q = P.codes != nullptr;
   if (P.bwd) {
     if (!q) return run<kBF16, true, kActNone, false>(P, stream);
+    if (P.value)
+      return P.act == kActSilu ? run<kBF16, true, kActSilu, true, true>(P, stream) : run<kBF16, true, kActGelu, true, true>(P, stream);
     return P.act == kActSilu ? run<kBF16, true, kActSilu, true>(P, stream) : run<kBF16, true, kActGelu, true>(P, stream);
   }
   switch (P.act) {
@@ -380,13 +384,13 @@ conv3d_status_t conv3d_linear_fwd(const void* x, const void* w, const void* bias
         return CONV3D_ERR_INVALID_ARG;
       }
   }
-  const Product P{x, w, bias, residual, y, codes, exponents, static_cast<int>(rows), K, N, false, act, dtype};
+  const Product P{x, w, bias, residual, y, codes, exponents, nullptr, static_cast<int>(rows), K, N, false, act, dtype};
   return dtype == CONV3D_BF16 ? dispatch<true>(P, stream) : dispatch<false>(P, stream);
 }
 
 conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void* codes,
-                                       const void* exponents, conv3d_act_t act, void* dx, long long rows,
-                                       int K, int N, conv3d_dtype_t dtype, struct CUstream_st* stream) {
+                                       const void* exponents, conv3d_act_t act, void* dx, void* x,
+                                       long long rows, int K, int N, conv3d_dtype_t dtype, struct CUstream_st* stream) {
   conv3d_status_t st = check(rows, K, N, act, dtype);
   if (st != CONV3D_OK) return st;
   if (!dy || !w || !dx || (codes == nullptr) != (exponents == nullptr)) {
@@ -397,17 +401,26 @@ conv3d_status_t conv3d_linear_bwd_data(const void* dy, const void* w, const void
     set_error("the derivative of an activation needs the checkpoint of its argument");
     return CONV3D_ERR_INVALID_ARG;
   }
-  if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(codes, 16) || !aligned(exponents, 16) || !aligned(dx, 16))
+  if (act == CONV3D_ACT_NONE && x) {
+    set_error("x is recomputed where an activation made it (CONV3D_ACT_NONE: conv3d_act8_unpack)");
+    return CONV3D_ERR_INVALID_ARG;
+  }
+  if (!aligned(dy, 16) || !aligned(w, 16) || !aligned(codes, 16) || !aligned(exponents, 16) || !aligned(dx, 16) ||
+      !aligned(x, 16))
     return misaligned();
   const size_t n = static_cast<size_t>(rows) * K * 2;
-  if (overlaps(dx, n, dy, static_cast<size_t>(rows) * N * 2) || overlaps(dx, n, w, static_cast<size_t>(N) * K * 2) ||
-      overlaps(dx, n, codes, act8_code_bytes(rows, K)) || overlaps(dx, n, exponents, act8_scale_bytes(rows, K))) {
-    set_error("dx must not overlap the inputs");
+  bool clash = overlaps(dx, n, x, n);
+  for (const void* o : {static_cast<const void*>(dx), static_cast<const void*>(x)})
+    clash = clash || overlaps(o, n, dy, static_cast<size_t>(rows) * N * 2) ||
+            overlaps(o, n, w, static_cast<size_t>(N) * K * 2) || overlaps(o, n, codes, act8_code_bytes(rows, K)) ||
+            overlaps(o, n, exponents, act8_scale_bytes(rows, K));
+  if (clash) {
+    set_error("dx and x must not overlap the inputs or each other");
     return CONV3D_ERR_INVALID_ARG;
   }
   const bool q = act != CONV3D_ACT_NONE;   // without an activation the derivative is 1
   const Product P{dy, w, nullptr, nullptr, dx, q ? const_cast<void*>(codes) : nullptr,
-                  q ? const_cast<void*>(exponents) : nullptr, static_cast<int>(rows), N, K, true, act, dtype};
+                  q ? const_cast<void*>(exponents) : nullptr, x, static_cast<int>(rows), N, K, true, act, dtype};
   return dtype == CONV3D_BF16 ? dispatch<true>(P, stream) : dispatch<false>(P, stream);
 }
 

@@ -62,6 +62,7 @@ struct LinearParams {
   const uint16_t* bias;     // [N] or null
   const uint16_t* residual; // [M][N] or null
   uint16_t* out;            // [M][N]
+  uint16_t* value;          // gradient: act(checkpoint), [M][N], or null (pair kernel: kValue says which)
   uint8_t* codes;           // written (forward) or read (gradient), [M][32 * blocks], or null
   uint8_t* exponents;       // the same, [M][blocks]
   int blocks;               // ceil(N / 32)
@@ -130,7 +131,8 @@ __device__ __forceinline__ uint32_t swz32(uint32_t r, uint32_t h) { return r * 3
 // ------------------------------------------------------------------ many rows
 
 // kBwd: the gradient (B MN-major, no bias; the chunk is multiplied by
-// act'(checkpoint) when kQ).  Forward: kQ writes the checkpoint.  Shared
+// act'(checkpoint) when kQ, and kValue writes act(checkpoint) too).  Forward: kQ
+// writes the checkpoint.  Shared
 // memory: A ring, B ring (or the whole column tile of B), then per epilogue warp
 // an output buffer, a code buffer (kQ, where it cannot share) and 64 fp32
 // biases, then the barriers.
@@ -140,7 +142,7 @@ __device__ __forceinline__ uint32_t swz32(uint32_t r, uint32_t h) { return r * 3
 // loads only A, which halves what each tile draws from L2: with both operands
 // streamed that traffic and the stores of a short-K tile together outlast the
 // products.
-template <bool kBF16, bool kBwd, int kAct, bool kQ>
+template <bool kBF16, bool kBwd, int kAct, bool kQ, bool kValue = false>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                        const LinearParams p) {
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
         const int col = col0 + 32 * j;
         uint32_t raw[32];
         tmem_ld_32x32b_x32(t_row + j * 32, raw);
-        uint32_t packed[16];
+        uint32_t packed[16], packed_value[kValue ? 16 : 1];
         if constexpr (kLoadCodes) {
           lin_copy_wait();
           __syncwarp();
@@ -426,12 +428,29 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float2 v[8];
-            a8_decode_halves(h ? kb : ka, eb, v);
+            const float half = 0.5f * a8_step(eb);
+            a8_decode_halves<!kValue>(h ? kb : ka, half, v);
+            auto multiply = [&](int e, float2 slope) {
+              const float2 d = mul2(slope, make_float2(__uint_as_float(raw[16 * h + 2 * e]),
+                                                       __uint_as_float(raw[16 * h + 2 * e + 1])));
+              packed[8 * h + e] = T::pack(d.x, d.y);
+            };
+            if constexpr (kValue) {
+              auto both_of = [&](int e, float2 narrowed) {
+                float2 value;
+                multiply(e, act_slope_and_value<kAct>(v[e], narrowed, value));
+                packed_value[8 * h + e] = T::pack(value.x, value.y);
+              };
+              if (a8_wide(half)) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              v[e] = mul2(act_slope_of_half<kAct>(v[e]), make_float2(__uint_as_float(raw[16 * h + 2 * e]),
-                                                                     __uint_as_float(raw[16 * h + 2 * e + 1])));
-              packed[8 * h + e] = T::pack(v[e].x, v[e].y);
+                for (int e = 0; e < 8; ++e) both_of(e, a8_narrow(v[e]));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) both_of(e, v[e]);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) multiply(e, act_slope_of_half<kAct>(v[e]));
             }
           }
         } else {
@@ -501,18 +520,21 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) packed[e] = T::pack(v[e].x, v[e].y);
         }
+        auto put = [&](uint16_t* to, const uint32_t* w) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          st_shared_v4(ob + swz64(lane, g), packed[4 * g], packed[4 * g + 1], packed[4 * g + 2], packed[4 * g + 3]);
-        __syncwarp();
-        if (col + vpart * 8 < p.N) {
-          uint16_t* dst = p.out + static_cast<size_t>(row0 + vrow) * p.N + col + vpart * 8;
+          for (int g = 0; g < 4; ++g) st_shared_v4(ob + swz64(lane, g), w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+          __syncwarp();
+          if (col + vpart * 8 < p.N) {
+            uint16_t* dst = to + static_cast<size_t>(row0 + vrow) * p.N + col + vpart * 8;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row0 + vrow + 8 * i < p.M)
-              *reinterpret_cast<uint4*>(dst + static_cast<size_t>(8 * i) * p.N) = ld_shared_v4(ob + swz64(vrow + 8 * i, vpart));
-        }
-        __syncwarp();   // the buffer is free again
+            for (int i = 0; i < 4; ++i)
+              if (row0 + vrow + 8 * i < p.M)
+                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(8 * i) * p.N) = ld_shared_v4(ob + swz64(vrow + 8 * i, vpart));
+          }
+          __syncwarp();   // the buffer is free again
+        };
+        put(p.out, packed);
+        if constexpr (kValue) put(p.value, packed_value);
         if (has_res) ask();
       }
     }
@@ -729,7 +751,10 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
         const size_t row = static_cast<size_t>(row0 + m);
         float y = v[i];
         if constexpr (kBwd && kQ) {
-          y *= act_slope_safe<kAct>(aux[i] * a8_step(eb[i]));
+          const float pre = aux[i] * a8_step(eb[i]);
+          y *= act_slope_safe<kAct>(pre);
+          if (p.value != nullptr && live)
+            p.value[row * p.N + ch] = static_cast<uint16_t>(T::pack(act_value<kAct>(pre), 0.0f) & 0xFFFFu);
         } else if constexpr (!kBwd) {
           y += bv;
           if constexpr (kQ) {
