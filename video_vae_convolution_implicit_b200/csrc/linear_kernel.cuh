@@ -110,6 +110,11 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The cluster barrier in two halves; the arrival orders no memory operations (one
+// with release semantics waits for this thread's global stores).
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
 // MN-major operand in 64-element x 8-row atoms with the 128-byte swizzle:
 // 64-element blocks `block_bytes` apart along M/N, 8-row groups 1 KB apart
 // along the contraction.
@@ -634,6 +639,41 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
 
+  // The finishing warps' part: channel `ch` of every `step`-th of the rank's rows.
+  // What they read beside the sums is asked for now.
+  constexpr int kBatch = 4;
+  const uint32_t quarter = warp & 3;
+  const int ch = ch0 + static_cast<int>(quarter * 32u + lane);
+  const bool live = ch < p.N;
+  const int block = (ch0 + static_cast<int>(quarter) * 32) / 32;
+  int rows = p.M - row0;
+  if (rows > p.BN) rows = p.BN;
+  if (block >= p.blocks || warp < 2) rows = 0;
+  const int group = (static_cast<int>(warp) - 2) / 4, groups = (static_cast<int>(blockDim.x) / 32 - 2) / 4;
+  const int step = p.split * groups;
+  const int m_first = rank + p.split * group;
+  float bv = 0.0f, aux[kBatch];
+  uint32_t eb[kBatch];
+  if (!kBwd && p.bias != nullptr && live) bv = T::lo(p.bias[ch]);
+  auto ask = [&](int m0) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int m = m0 + i * step;
+      aux[i] = 0.0f;
+      eb[i] = 7u;
+      if (m < rows) {
+        const size_t row = static_cast<size_t>(row0 + m);
+        if constexpr (kBwd && kQ) {
+          eb[i] = __ldg(p.exponents + row * p.blocks + block);
+          aux[i] = static_cast<float>(static_cast<int8_t>(__ldg(p.codes + row * p.blocks * 32 + ch)));
+        } else if (!kBwd && p.residual != nullptr && live) {
+          aux[i] = T::lo(p.residual[row * p.N + ch]);
+        }
+      }
+    }
+  };
+  ask(m_first);
+
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
@@ -665,7 +705,6 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
       wait_bounded(tfull_bar, 0, ctl, false);
     }
   } else if (warp < 6) {
-    const uint32_t quarter = warp & 3;
     // (not watching the abort flag: the commit above always arrives)
     if (__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar, 0, ctl, false) && !s_abort)) {   // the warp as one
       tc_fence_after();
@@ -693,55 +732,39 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
   __syncthreads();
   if (p.split > 1) cluster_sync();   // every rank's partials are in its shared memory
   if (warp >= 2) {
-    constexpr int kBatch = 4;
-    const uint32_t quarter = warp & 3;
-    const int ch = ch0 + static_cast<int>(quarter * 32u + lane);
-    const bool live = ch < p.N;
-    const int block = (ch0 + static_cast<int>(quarter) * 32) / 32;
-    float bv = 0.0f;
-    if (!kBwd && p.bias != nullptr && live) bv = T::lo(p.bias[ch]);
     const uint32_t mine = base + (quarter * 32u + lane) * 4u;
-    int rows = p.M - row0;
-    if (rows > p.BN) rows = p.BN;
-    if (block >= p.blocks) rows = 0;
-    // this warp's rows: every `lanes`-th of the rank's
-    const int group = (static_cast<int>(warp) - 2) / 4, groups = (static_cast<int>(blockDim.x) / 32 - 2) / 4;
-    const int step = p.split * groups;
-    for (int m0 = rank + p.split * group; m0 < rows; m0 += kBatch * step) {
-      float v[kBatch], aux[kBatch];
-      uint32_t eb[kBatch];
-      // what each row reads, all in flight before any of it is used
+    for (int m0 = m_first; m0 < rows; m0 += kBatch * step) {
+      if (m0 != m_first) ask(m0);
+      float v[kBatch];
+      if (p.split == 1) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int m = m0 + i * step;
-        v[i] = aux[i] = 0.0f;
-        eb[i] = 7u;
-        if (m < rows) {
-          const size_t row = static_cast<size_t>(row0 + m);
-          if constexpr (kBwd && kQ) {
-            eb[i] = __ldg(p.exponents + row * p.blocks + block);
-            aux[i] = static_cast<float>(static_cast<int8_t>(__ldg(p.codes + row * p.blocks * 32 + ch)));
-          } else if (!kBwd && p.residual != nullptr && live) {
-            aux[i] = T::lo(p.residual[row * p.N + ch]);
-          }
-          if (p.split == 1)
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(mine + m * (BM * 4u)) : "memory");
+        for (int i = 0; i < kBatch; ++i) {
+          v[i] = 0.0f;
+          if (m0 + i * step < rows)
+            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(mine + (m0 + i * step) * (BM * 4u)) : "memory");
         }
-      }
-      if (p.split > 1) {
-        for (int r = 0; r < p.split; ++r) {
-          float part[kBatch];
+      } else {
+        // The partials of four ranks at a time are all in flight.  (Read where the sum is
+        // stored, and only there: a load that nothing waits for could outlast its peer.)
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            part[i] = 0.0f;
-            if (m0 + i * step < rows)
-              asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                           : "=f"(part[i])
-                           : "r"(mapa_shared(mine + (m0 + i * step) * (BM * 4u), r))
-                           : "memory");
-          }
+        for (int i = 0; i < kBatch; ++i) v[i] = 0.0f;
+        for (int r0 = 0; r0 < p.split; r0 += 4) {
+          float part[4][kBatch];
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) v[i] += part[i];
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              part[r][i] = 0.0f;
+              if (live && r0 + r < p.split && m0 + i * step < rows)
+                asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                             : "=f"(part[r][i])
+                             : "r"(mapa_shared(mine + (m0 + i * step) * (BM * 4u), r0 + r))
+                             : "memory");
+            }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) v[i] += part[r][i];
         }
       }
 #pragma unroll
@@ -769,8 +792,13 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
       }
     }
   }
-  if (p.split > 1) cluster_sync();   // no CTA leaves while its peers may read its partials
-  __syncthreads();
+  if (p.split > 1) {   // no CTA leaves while its peers may read its partials
+    __syncwarp();
+    cluster_arrive_relaxed();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, p.tmem_cols);
