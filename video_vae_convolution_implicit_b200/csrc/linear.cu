@@ -42,6 +42,7 @@ struct Plan {
   bool resident;      // pair kernel: B's column tile stays in shared memory
   int units;          // pair kernel: CTA pairs
   size_t smem;
+  unsigned part;      // rows kernel: bytes of the partials
 };
 
 int env_int(const char* name) {
@@ -126,11 +127,12 @@ Plan choose(const Product& P, const Device& dev) {
   if (forced_split >= 1 && forced_split <= 8) L.split = forced_split <= kblocks ? forced_split : kblocks;
   const int per = (kblocks + L.split - 1) / L.split;
   const size_t stage = kLinABytes + static_cast<size_t>(L.BN) * BK * 2;
+  const size_t part = static_cast<size_t>(L.split) * ((L.BN + 4 * L.split - 1) / (4 * L.split)) * BM * 16;
+  L.part = static_cast<unsigned>(part);
+  const size_t fit = (dev.max_smem_optin - 64 - kReserve - part) / stage;
   L.stages = per < 6 ? per : 6;
-  size_t ring = L.stages * stage;
-  const size_t part = static_cast<size_t>(L.BN) * BM * 4;
-  if (ring < part) ring = part;
-  L.smem = kReserve + ring;
+  if (static_cast<size_t>(L.stages) > fit) L.stages = static_cast<int>(fit);
+  L.smem = kReserve + L.stages * stage + part;
   return L;
 }
 
@@ -165,6 +167,7 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
   p.split = L.split;
   p.resident = L.resident ? 1 : 0;
   p.stages = L.stages;
+  p.part_bytes = L.part;
   p.bias = static_cast<const uint16_t*>(P.bias);
   p.residual = static_cast<const uint16_t*>(P.residual);
   p.out = static_cast<uint16_t*>(P.out);

@@ -55,6 +55,7 @@ struct LinearParams {
   int BN;                   // columns per tile (pair) / rows per tile (rows kernel)
   int tiles_n, num_tiles;
   int split;                // CTAs per cluster along the contraction (rows kernel)
+  uint32_t part_bytes;      // rows kernel: shared memory of the partials
   int resident;             // pair kernel: the CTA keeps its half of B's column tile in shared memory
   int stages;
   uint32_t tmem_cols;
@@ -108,6 +109,11 @@ __device__ __forceinline__ void mma_commit_both(uint32_t bar) {
 // signals, that tensor memory has been read, is complete by tcgen05.wait::ld.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 // The cluster barrier in two halves; the arrival orders no memory operations (one
@@ -560,14 +566,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 // ------------------------------------------------------------------ few rows
 
 // Cluster rank r of tile t sums k-blocks [r * kblocks / split, (r+1) * kblocks /
-// split) of 128 channels x BN rows, leaves them in its shared memory as
-// [row][128 channels] fp32, and finishes the rows r, r + split, ...: the sum of
-// the ranks' partials in rank order, then the epilogue with one channel per
-// thread (a warp is one checkpoint block of the row, and its stores are
-// contiguous), kBatch rows of a warp at a time.  The partials take the place of
-// the operand ring, which nothing reads any more once the accumulator is
-// complete.  These calls last a few microseconds, so the first copies are issued
-// by the thread that initialises the barriers, before the other warps have met.
+// split) of 128 channels x BN rows and hands each rank an equal share of the rows
+// of its fp32 sums; that rank adds the partials of its rows in rank order and
+// finishes them with one channel per thread (a warp is one checkpoint block of the
+// row, and its stores are contiguous), four rows of a warp at a time, which are
+// one 16-byte access of a partial.  These calls last a
+// few microseconds, most of it one latency after the other, so: the first copies
+// are issued by the thread that initialises the barriers, before the other warps
+// have met; what the epilogue reads is asked for before the products; partials
+// are written into their owner's shared memory (beside its operand ring, which it
+// may still be reading) and not fetched from the ranks after a barrier, a round
+// trip more; and nothing waits for global stores but the end of the grid.
 template <bool kBF16, bool kBwd, int kAct, bool kQ>
 __global__ void __launch_bounds__(kLinRowsThreads, 1)
     linear_rows_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
@@ -589,9 +598,11 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
   const uint32_t w_ring = base;
   const uint32_t x_ring = w_ring + p.stages * kLinABytes;
   const uint32_t ring_end = x_ring + p.stages * x_bytes;
-  const uint32_t part_end = base + static_cast<uint32_t>(p.BN) * BM * 4;
-  const uint32_t bars = ring_end > part_end ? ring_end : part_end;
-  const uint32_t full_bar = bars;
+  // a rank's share of the tile's rows, whole fours; its partials as [rank][fours][128 channels][4]
+  const int tile_rows = p.M - row0 < p.BN ? p.M - row0 : p.BN;
+  const int share = (tile_rows + 4 * p.split - 1) / (4 * p.split) * 4;
+  const uint32_t parts = ring_end;
+  const uint32_t full_bar = parts + p.part_bytes;
   const uint32_t empty_bar = full_bar + 8 * p.stages;
   const uint32_t tfull_bar = empty_bar + 8 * p.stages;
   SharedCtl ctl{&s_abort, p.status, p.timeout_ns, 0u};
@@ -635,30 +646,30 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.split > 1) cluster_arrive_relaxed();   // this CTA runs: its shared memory may be written
   const uint32_t tmem_base = s_tmem_base;
   griddep_wait();
   griddep_launch_dependents();
 
-  // The finishing warps' part: channel `ch` of every `step`-th of the rank's rows.
-  // What they read beside the sums is asked for now.
+  // The finishing warps' part: channel `ch` of every `groups`-th four of the rank's
+  // rows.  What they read beside the sums is asked for now.
   constexpr int kBatch = 4;
   const uint32_t quarter = warp & 3;
   const int ch = ch0 + static_cast<int>(quarter * 32u + lane);
   const bool live = ch < p.N;
   const int block = (ch0 + static_cast<int>(quarter) * 32) / 32;
-  int rows = p.M - row0;
-  if (rows > p.BN) rows = p.BN;
+  int rows = (rank + 1) * share;   // the end of this warp's rows
+  if (rows > tile_rows) rows = tile_rows;
   if (block >= p.blocks || warp < 2) rows = 0;
   const int group = (static_cast<int>(warp) - 2) / 4, groups = (static_cast<int>(blockDim.x) / 32 - 2) / 4;
-  const int step = p.split * groups;
-  const int m_first = rank + p.split * group;
+  const int m_first = rank * share + kBatch * group;
   float bv = 0.0f, aux[kBatch];
   uint32_t eb[kBatch];
   if (!kBwd && p.bias != nullptr && live) bv = T::lo(p.bias[ch]);
   auto ask = [&](int m0) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const int m = m0 + i * step;
+      const int m = m0 + i;
       aux[i] = 0.0f;
       eb[i] = 7u;
       if (m < rows) {
@@ -704,12 +715,18 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
       mma_commit(tfull_bar);
       wait_bounded(tfull_bar, 0, ctl, false);
     }
-  } else if (warp < 6) {
+  }
+  if (p.split > 1) {
+    __syncwarp();
+    cluster_wait();
+  }
+  if (warp >= 2) {
     // (not watching the abort flag: the commit above always arrives)
     if (__all_sync(0xFFFFFFFFu, wait_bounded(tfull_bar, 0, ctl, false) && !s_abort)) {   // the warp as one
       tc_fence_after();
       const uint32_t t_row = tmem_base + ((quarter * 32u) << 16);
-      for (int j = 0; j < p.BN; j += 16) {
+      const uint32_t at = parts + (static_cast<uint32_t>(rank * share / 4) * BM + quarter * 32u + lane) * 16u;
+      for (int j = 16 * group; j < tile_rows; j += 16 * groups) {
         uint32_t raw[16];
         asm volatile(
             "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -719,57 +736,44 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
               "=r"(raw[14]), "=r"(raw[15])
             : "r"(t_row + j)
             : "memory");
+        int owner = j / share, four = (j - owner * share) / 4;
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((j + e) * BM + quarter * 32u + lane) * 4u), "r"(raw[e])
-                       : "memory");
+        for (int e = 0; e < 16; e += 4) {
+          if (j + e < tile_rows) {
+            const uint32_t to = at + static_cast<uint32_t>(four) * (BM * 16u);
+            if (p.split == 1)
+              st_shared_v4(to, raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
+            else
+              st_cluster_v4(mapa_shared(to, static_cast<uint32_t>(owner)), raw[e], raw[e + 1], raw[e + 2], raw[e + 3]);
+          }
+          if (4 * ++four == share) {
+            four = 0;
+            ++owner;
+          }
+        }
       }
     }
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
-  if (p.split > 1) cluster_sync();   // every rank's partials are in its shared memory
+  if (p.split > 1) cluster_sync();   // every rank's partials of this rank's rows are here
+  else __syncthreads();
   if (warp >= 2) {
-    const uint32_t mine = base + (quarter * 32u + lane) * 4u;
-    for (int m0 = m_first; m0 < rows; m0 += kBatch * step) {
+    uint32_t mine = parts + (static_cast<uint32_t>(group) * BM + quarter * 32u + lane) * 16u;
+    for (int m0 = m_first; m0 < rows; m0 += kBatch * groups, mine += groups * (BM * 16u)) {
       if (m0 != m_first) ask(m0);
-      float v[kBatch];
-      if (p.split == 1) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          v[i] = 0.0f;
-          if (m0 + i * step < rows)
-            asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[i]) : "r"(mine + (m0 + i * step) * (BM * 4u)) : "memory");
-        }
-      } else {
-        // The partials of four ranks at a time are all in flight.  (Read where the sum is
-        // stored, and only there: a load that nothing waits for could outlast its peer.)
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) v[i] = 0.0f;
-        for (int r0 = 0; r0 < p.split; r0 += 4) {
-          float part[4][kBatch];
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              part[r][i] = 0.0f;
-              if (live && r0 + r < p.split && m0 + i * step < rows)
-                asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                             : "=f"(part[r][i])
-                             : "r"(mapa_shared(mine + (m0 + i * step) * (BM * 4u), r0 + r))
-                             : "memory");
-            }
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) v[i] += part[r][i];
-        }
+      float v[kBatch] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int r = 0; r < p.split; ++r) {
+        const uint4 part = ld_shared_v4(mine + static_cast<uint32_t>(r * share / 4) * (BM * 16u));
+        v[0] += __uint_as_float(part.x);
+        v[1] += __uint_as_float(part.y);
+        v[2] += __uint_as_float(part.z);
+        v[3] += __uint_as_float(part.w);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int m = m0 + i * step;
+        const int m = m0 + i;
         if (m >= rows) break;
         const size_t row = static_cast<size_t>(row0 + m);
         float y = v[i];
@@ -791,13 +795,6 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
         if (live) p.out[row * p.N + ch] = static_cast<uint16_t>(T::pack(y, 0.0f) & 0xFFFFu);
       }
     }
-  }
-  if (p.split > 1) {   // no CTA leaves while its peers may read its partials
-    __syncwarp();
-    cluster_arrive_relaxed();
-    cluster_wait();
-  } else {
-    __syncthreads();
   }
   if (warp == 1) {
     tc_fence_after();
