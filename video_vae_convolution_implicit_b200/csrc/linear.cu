@@ -109,19 +109,19 @@ Plan choose(const Product& P, const Device& dev) {
     return L;
   }
   // Rows per tile: those there are, up to 64, or 128 where 64 make more tiles
-  // than SMs.  Pieces: while they fill idle SMs and keep two k-blocks each (few
-  // rows: the call is latency) or four; eight CTAs of a cluster need room in one
-  // GPC, so eight pieces only for a few tiles (64 x 2048 -> 2048: 8.1 us in four
-  // pieces, over 9.4 in eight; 1 x 2048 -> 512: 6.2 and 4.9).
+  // than SMs.  Pieces: while they fill idle SMs and keep two k-blocks each (61 x
+  // 512 -> 2048: 5.3 us in two pieces, 4.4 in four).  Eight CTAs of a cluster need
+  // room in one GPC, so eight pieces only for a few tiles, or where two CTAs fit an
+  // SM (64 x 2048 -> 2048: 6.7 us in four pieces, 11.3 in eight; 16 rows of it 5.9
+  // and 5.1; 1 x 2048 -> 512: 5.4 and 4.1).
   const long long nt = (P.N + 127) / 128;
   L.BN = P.M <= 16 ? 16 : P.M <= 32 ? 32 : nt * ((P.M + 63) / 64) <= dev.num_sms ? 64 : 128;
   const int forced_rows = env_int("CONV3D_LINEAR_ROWS");   // tuning and tests: rows per tile
   if (forced_rows == 16 || forced_rows == 32 || forced_rows == 64 || forced_rows == 128) L.BN = forced_rows;
   const long long tiles = nt * ((P.M + L.BN - 1) / L.BN);
-  const int least = L.BN <= 32 ? 2 : 4;
+  const int most8 = L.BN == 16 ? dev.num_sms : dev.num_sms * 2 / 3;
   L.split = 1;
-  while (L.split < 8 && tiles * L.split * 2 <= (L.split < 4 ? dev.num_sms : dev.num_sms * 2 / 3) &&
-         L.split * 2 * least <= kblocks)
+  while (L.split < 8 && tiles * L.split * 2 <= (L.split < 4 ? dev.num_sms : most8) && L.split * 4 <= kblocks)
     L.split *= 2;
   const int forced_split = env_int("CONV3D_LINEAR_SPLIT");   // tuning and tests
   if (forced_split >= 1 && forced_split <= 8) L.split = forced_split <= kblocks ? forced_split : kblocks;

@@ -87,6 +87,11 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       "r"(r)
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int c, int r) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c), "r"(r)
+               : "memory");
+}
 // Asynchronous 16-byte copy global -> shared and its group bookkeeping.
 __device__ __forceinline__ void lin_copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -636,6 +641,15 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
     }
     mbar_init(tfull_bar, 1);
     fence_mbar_init();
+    // the weight's way from HBM to L2 may overlap the previous kernel (L2 stays
+    // coherent should that write it)
+    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      if constexpr (kBwd) {
+        for (int i = 0; i < BM / 64; ++i) tma_prefetch_2d(&map_w, ch0 + 64 * i, kb * BK);
+      } else {
+        tma_prefetch_2d(&map_w, kb * BK, ch0);
+      }
+    }
     griddep_wait();                // no global memory is touched before the previous kernel has finished
     for (; first < kb_hi && first < kb_lo + p.stages; ++first) load(first);
   }
