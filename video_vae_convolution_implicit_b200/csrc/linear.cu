@@ -58,8 +58,8 @@ uint32_t pow2(int v) {
 
 // Pair tiles of 256 rows x 256 or 128 columns when there are enough to keep
 // about half of the SM pairs busy, otherwise the rows kernel.  Measured on B200
-// (bf16, GELU, us; pair / rows kernel): 512 x 512 -> 2048 7.6 / 8.1, 256 rows of
-// it 7.5 / 7.3, 1024 x 2048 -> 512 15.7 / 10.6, 1000 x 1024 -> 1024 10.3 / 10.6.
+// (bf16, GELU, us; pair / rows kernel): 512 x 512 -> 2048 7.7 / 8.1, 256 rows of
+// it 7.6 / 6.0, 1024 x 2048 -> 512 15.8 / 10.7, 1000 x 1024 -> 1024 10.3 / 11.1.
 // A round of 128-column tiles takes about 0.65 of a round of 256-column ones
 // (4096 x 512 -> 2048: 18.5 / 12.9; 1024 rows of it: 8.7 / 9.0).
 Plan choose(const Product& P, const Device& dev) {

@@ -15,23 +15,35 @@
 // BN columns, warp-specialised as the convolution is -- TMA producer, one
 // tcgen05.mma issuer (cta_group::2), and epilogue warps over two TMEM
 // accumulators.  At 8 k-blocks a tile the epilogue has about as many issue slots
-// to spend as the tensor cores take for the tile (some 14 instructions a value
-// with GELU and the checkpoint), and a chunk is a long chain of dependent steps
-// (TMEM load, arithmetic, staging, fence, store): 16 warps, four to a scheduler,
-// hide it where 8 left two thirds of the slots empty.  The chunks go out by plain
-// stores through a swizzled buffer of the warp's own, and the residual and the
-// codes come in by cp.async, 16 bytes a thread: as TMA boxes of 32 x 32 values
-// they took 220 cycles each whatever their bytes, 7000 cycles a tile (measured
-// on B200, 512 -> 2048 on 36864 rows: the epilogue alone 63 us, the products 58).  Columns are the
-// fast tile index, so the tiles in flight share rows of A and A is read from
-// HBM about once; w stays in L2.
+// to spend as the tensor cores take for the tile (16 instructions a value with
+// the GELU derivative), and a chunk is a long chain of dependent steps (TMEM load,
+// arithmetic, staging, store): 16 warps, four to a scheduler, hide it where 8
+// left two thirds of the slots empty.  The chunks go out by plain 16-byte stores
+// through a swizzled buffer of the warp's own, and the residual and the codes come
+// in by cp.async, 16 bytes a thread, one chunk ahead.  A warp hands its part of the
+// accumulator back as soon as it is in registers, by an arrival that waits for no
+// global store.  Columns are the fast tile index, so the tiles in flight share rows
+// of A and A is read from HBM about once; w stays in L2.
+//
+// Measured on B200 (bf16, 36864 rows, 512 -> 2048, 77 GFLOP, graph replays): plain
+// 71 us (a plain library product 64), GELU 74, GELU and checkpoint 91, gradient 68,
+// with GELU' from the checkpoint 86; on a chip 5% slower, residual 89, GELU' and the
+// recomputed activation 118.  104448 rows of 2048 -> 512: 174 us, 1260 TFLOP/s
+// (157).  What bounds it: under the plain product the tensor cores are busy 58% of the cycles, with
+// GELU' and the checkpoint 47%, issue slots 47%, the shared-memory data path 41 to
+// 64%, HBM 30%; no unit is full, each tile's 256 KB of operand copies, their reads
+// by the tensor cores and the 130 to 200 KB of staging meet in one shared memory, and
+// the chip runs at its power limit (1.5 to 1.7 GHz).
 //
 // linear_rows_kernel (few rows): one 128-channel x up-to-128-row tile per
 // cluster, transposed (w is the 128-row operand, the rows of x are the N side),
 // with the contraction split over the cluster's CTAs, whose partial sums meet
 // in shared memory: w, the bulk of the bytes, streams through as many SMs as
 // there are pieces, in one launch and without a workspace, and the sum runs in
-// rank order whatever the timing.
+// rank order whatever the timing.  Measured (bf16, GELU, weights from HBM, graph
+// replays): 1 x 512 -> 2048 3.3 us, 1 x 2048 -> 512 4.0, 61 x 1024 -> 1000 4.9, 64
+// x 2048 -> 2048 6.7: latencies one after the other (a first copy 0.6 us, the
+// following k-blocks 0.3 us each, the meeting of the ranks 0.5 to 1.2 us).
 #pragma once
 
 #include "act8.cuh"
@@ -155,9 +167,8 @@ __device__ __forceinline__ uint32_t swz32(uint32_t r, uint32_t h) { return r * 3
 //
 // Resident B: with a short contraction (K <= 512 at BN = 256) a CTA's half of the
 // column tile fits beside the A ring.  A pair then stays with its columns and
-// loads only A, which halves what each tile draws from L2: with both operands
-// streamed that traffic and the stores of a short-K tile together outlast the
-// products.
+// loads only A, which halves what each tile draws from L2 and writes into shared
+// memory.
 template <bool kBF16, bool kBwd, int kAct, bool kQ, bool kValue = false>
 __global__ void __launch_bounds__(kLinThreads, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
