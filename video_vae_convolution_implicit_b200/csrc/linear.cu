@@ -80,7 +80,7 @@ Plan choose(const Product& P, const Device& dev) {
   if (L.pair) {
     L.split = 1;
     const bool q = P.codes != nullptr;
-    const size_t epi = kLinEpiWarps * (kLinOutBytes + (q && (P.bwd || P.residual) ? kLinCodeBytes : 0) +
+    const size_t epi = kLinEpiWarps * (lin_out_chunks(P.bwd, q, P.value != nullptr) * kLinOutBytes + (q && (P.bwd || P.residual) ? kLinCodeBytes : 0) +
                                        (P.bwd ? 0 : kLinBiasBytes));
     const size_t room = dev.max_smem_optin - 64 - kReserve - epi;
     const size_t b_bytes = static_cast<size_t>(L.BN / 2) * BK * 2;

@@ -58,6 +58,12 @@ constexpr int kLinThreads = 64 + 32 * kLinEpiWarps;   // producer, issuer, epilo
 constexpr int kLinRowsThreads = 64 + 32 * 16, kLinFewThreads = 64 + 32 * 4;
 constexpr uint32_t kLinABytes = BM * BK * 2;           // one CTA's A rows of a k-block
 constexpr uint32_t kLinOutBytes = 32 * 32 * 2;         // a 32 x 32 chunk of 16-bit values
+// Chunks in an epilogue warp's output buffer: two where it writes twice, the codes
+// or the recomputed activation beside the values (104448 rows, 512 -> 2048: GELU' and
+// the activation 301 us, 345 with one; 36864 rows, GELU and checkpoint 90.6, 91.8);
+// elsewhere a pipeline stage is worth more (36864 rows, plain: 71 us with one, 76 with
+// two).
+__host__ __device__ constexpr int lin_out_chunks(bool bwd, bool q, bool value) { return value || (q && !bwd) ? 2 : 1; }
 constexpr uint32_t kLinCodeBytes = 32 * 32;            // the same chunk's codes
 constexpr uint32_t kLinBiasBytes = 64 * 4;             // the biases of a warp's (at most two) chunks
 
@@ -193,11 +199,12 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const uint32_t b_ring = a_ring + p.stages * kLinABytes;      // or the whole half tile, by k-block
   const uint32_t out_buf = b_ring + (p.resident ? p.kblocks : p.stages) * b_bytes;
   const bool has_res = !kBwd && p.residual != nullptr;
-  // codes: a buffer of their own where the other is taken when they are staged
+  constexpr uint32_t kOutBytes = lin_out_chunks(kBwd, kQ, kValue) * kLinOutBytes;
+  // codes: a buffer of their own, or the second chunk's place before its values come
   const bool own_codes = kQ && (kBwd || has_res);
-  const uint32_t code_buf = own_codes ? out_buf + kLinEpiWarps * kLinOutBytes : out_buf;
-  const uint32_t code_step = own_codes ? kLinCodeBytes : kLinOutBytes;
-  const uint32_t bias_buf = out_buf + kLinEpiWarps * (kLinOutBytes + (own_codes ? kLinCodeBytes : 0));
+  const uint32_t code_buf = out_buf + (own_codes ? kLinEpiWarps * kOutBytes : kLinOutBytes);
+  const uint32_t code_step = own_codes ? kLinCodeBytes : kOutBytes;
+  const uint32_t bias_buf = out_buf + kLinEpiWarps * (kOutBytes + (own_codes ? kLinCodeBytes : 0));
   const uint32_t bars = bias_buf + (kBwd ? 0 : kLinEpiWarps * kLinBiasBytes);
   const uint32_t full_bar = bars;
   const uint32_t empty_bar = full_bar + 8 * p.stages;
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     const uint32_t ew = warp - 2;
     const int share = static_cast<int>(ew) / 4;
     const int nj = p.BN / 128;                                 // chunks per warp and tile
-    const uint32_t ob = out_buf + ew * kLinOutBytes;
+    const uint32_t ob = out_buf + ew * kOutBytes;
     const uint32_t cb = code_buf + ew * code_step;
     const uint32_t bb = bias_buf + ew * kLinBiasBytes;
     // this lane's 16 bytes of a chunk's rows in the row-contiguous order of
@@ -370,10 +377,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     here.nt = unit % p.tiles_n;
     here.row0 = (unit / p.tiles_n) * 2 * BM + static_cast<int>(rank) * BM + static_cast<int>(quarter) * 32;
     here.col0 = here.nt * p.BN + share * nj * 32;
-    // The residual or the codes of the warp's next chunk are always under way:
-    // the load is issued when the buffer is free (the residual's is the output
-    // buffer, in which the sum replaces it), for the next live chunk, of this tile
-    // or a later one, and a chunk's exponent byte is fetched with it.
+    constexpr bool kTwo = lin_out_chunks(kBwd, kQ, kValue) == 2;
+    // Place of 16-byte piece c of row r of the warp's chunk j.  (Two chunks' pieces of a
+    // row lie in different banks.)
+    auto slot = [&](int j, int r, int c) {
+      const uint32_t at = swz64(static_cast<uint32_t>(r), static_cast<uint32_t>(c));
+      return ob + (!kTwo || j == 0 ? at : kLinOutBytes + (at ^ 64u));
+    };
+    // What the warp's next live chunk reads, of this tile or a later one, is always
+    // under way: its codes, and its exponent byte with them, as soon as the chunk
+    // before it has been decoded; its residual (in a buffer of two chunks, the next
+    // tile's) as soon as the output buffer is free, in which the sum replaces it.
     Place next = here;
     int next_j = 0;
     uint32_t next_eb = 0;
@@ -384,8 +398,8 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       }
       if (next.t >= p.num_tiles) return;
       const int row0 = next.row0;
-      const int col = next.col0 + 32 * next_j;
       if constexpr (kLoadCodes) {
+        const int col = next.col0 + 32 * next_j;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = crow + 16 * i;
@@ -393,20 +407,23 @@ __global__ void __launch_bounds__(kLinThreads, 1)
             lin_copy16(cb + swz32(r, cpart),
                        p.codes + (static_cast<size_t>(row0 + r) * p.blocks + col / 32) * 32 + cpart * 16);
         }
-      } else if (col + vpart * 8 < p.N) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = vrow + 8 * i;
-          if (row0 + r < p.M)
-            lin_copy16(ob + swz64(r, vpart), p.residual + static_cast<size_t>(row0 + r) * p.N + col + vpart * 8);
-        }
-      }
-      lin_copy_commit();
-      if constexpr (kLoadCodes) {
         const int row = row0 + static_cast<int>(lane);
         next_eb = row < p.M ? __ldg(p.exponents + static_cast<size_t>(row) * p.blocks + col / 32) : 0u;
+        ++next_j;
+      } else {
+        do {
+          const int col = next.col0 + 32 * next_j;
+          if (col + vpart * 8 < p.N) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = vrow + 8 * i;
+              if (row0 + r < p.M)
+                lin_copy16(slot(next_j, r, vpart), p.residual + static_cast<size_t>(row0 + r) * p.N + col + vpart * 8);
+            }
+          }
+        } while (++next_j < live_chunks(next) && kTwo);
       }
-      ++next_j;
+      lin_copy_commit();
     };
     if (loads) ask();
     int local = 0;
@@ -539,7 +556,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               float2 f[4];
-              T::unpack8(ld_shared_v4(ob + swz64(lane, g)), f);
+              T::unpack8(ld_shared_v4(slot(j, lane, g)), f);
 #pragma unroll
               for (int e = 0; e < 4; ++e) v[4 * g + e] = add2(v[4 * g + e], f[e]);
             }
@@ -547,22 +564,49 @@ __global__ void __launch_bounds__(kLinThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) packed[e] = T::pack(v[e].x, v[e].y);
         }
-        auto put = [&](uint16_t* to, const uint32_t* w) {
+        // Into the output buffer, and out of it in whole rows: 64 bytes of each, or 128
+        // of two chunks together (four lines a store instead of eight: the stores share
+        // the data path of shared memory)
+        auto stage = [&](int place, const uint32_t* w) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) st_shared_v4(ob + swz64(lane, g), w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
-          __syncwarp();
-          if (col + vpart * 8 < p.N) {
-            uint16_t* dst = to + static_cast<size_t>(row0 + vrow) * p.N + col + vpart * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (row0 + vrow + 8 * i < p.M)
-                *reinterpret_cast<uint4*>(dst + static_cast<size_t>(8 * i) * p.N) = ld_shared_v4(ob + swz64(vrow + 8 * i, vpart));
-          }
-          __syncwarp();   // the buffer is free again
+          for (int g = 0; g < 4; ++g) st_shared_v4(slot(place, lane, g), w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
         };
-        put(p.out, packed);
-        if constexpr (kValue) put(p.value, packed_value);
-        if (has_res) ask();
+        auto put = [&](int place, uint16_t* to) {
+          if (col + vpart * 8 >= p.N) return;
+          uint16_t* dst = to + static_cast<size_t>(row0 + vrow) * p.N + col + vpart * 8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row0 + vrow + 8 * i < p.M)
+              *reinterpret_cast<uint4*>(dst + static_cast<size_t>(8 * i) * p.N) = ld_shared_v4(slot(place, vrow + 8 * i, vpart));
+        };
+        if constexpr (kValue) {
+          stage(0, packed);
+          stage(1, packed_value);
+          __syncwarp();
+          put(0, p.out);
+          put(1, p.value);
+          __syncwarp();   // the buffer is free again
+        } else {
+          stage(j, packed);
+          if (!kTwo || j + 1 == live) {
+            __syncwarp();
+            if (!kTwo || live == 1) {
+              put(0, p.out);
+            } else {
+              const int wrow = static_cast<int>(lane >> 3), wpart = static_cast<int>(lane & 7);
+              if (col0 + wpart * 8 < p.N) {
+                uint16_t* dst = p.out + static_cast<size_t>(row0 + wrow) * p.N + col0 + wpart * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (row0 + wrow + 4 * i < p.M)
+                    *reinterpret_cast<uint4*>(dst + static_cast<size_t>(4 * i) * p.N) =
+                        ld_shared_v4(slot(wpart >> 2, wrow + 4 * i, wpart & 3));
+              }
+            }
+            __syncwarp();   // the buffer is free again
+            if (has_res) ask();
+          }
+        }
       }
     }
     lin_copy_wait();
