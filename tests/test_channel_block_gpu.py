@@ -404,6 +404,24 @@ def test_product_kernels_time_out_and_recover(variant, monkeypatch, _disarm):
     check_linear(p, BF, 2, True, True, y, a)
 
 
+@pytest.mark.parametrize("variant", sorted(STALLS))
+def test_gradient_kernels_time_out_and_recover(variant, monkeypatch, _disarm):
+    for k, v in STALLS[variant].items():
+        monkeypatch.setenv(k, v)
+    dy, w, pre = rand((700, 264), 39, 0), rand((264, 512), 39, 1, 0.05), ckpt(700, 512, 39)
+    want = c3.linear_bwd_data(dy, w, pre, c3.ACT_GELU, with_x=True)
+    sync_ok()
+    c3.test_arm_stall(1, 50)
+    t0 = time.perf_counter()
+    c3.linear_bwd_data(dy, w, pre, c3.ACT_GELU, with_x=True)
+    status = c3.poll_status()
+    assert status == c3.Status.TIMEOUT, c3.status_string(status)
+    assert time.perf_counter() - t0 < 5.0
+    again = c3.linear_bwd_data(dy, w, pre, c3.ACT_GELU, with_x=True)
+    sync_ok()
+    assert all(torch.equal(a, b) for a, b in zip(again, want))
+
+
 @pytest.mark.parametrize("splits", ["1", "2"])
 def test_weight_gradient_kernel_times_out_and_recovers(splits, monkeypatch, _disarm):
     monkeypatch.setenv("CONV3D_LINEAR_WGRAD_SPLITS", splits)
@@ -432,7 +450,8 @@ def test_resident_and_streamed_weight_agree(M, K, N, monkeypatch):
         monkeypatch.setenv("CONV3D_LINEAR_RESIDENT", resident)
         y, a = run_linear(p, 2, True, True, True)
         dx = c3.linear_bwd_data(dy, rand((K, N), 37, 8, K ** -0.5), pre, c3.ACT_SILU)
+        both = c3.linear_bwd_data(dy, rand((K, N), 37, 8, K ** -0.5), pre, c3.ACT_SILU, with_x=True)
         sync_ok()
-        out.append((y, a.codes, a.exponents, dx))
+        out.append((y, a.codes, a.exponents, dx, *both))
     check_linear(p, BF, 2, True, True, out[0][0], c3.Act8(out[0][1], out[0][2], N))
     assert all(torch.equal(a, b) for a, b in zip(*out))

@@ -396,6 +396,49 @@ def test_linear_data_gradient(M, K, N, dtype, kernel, monkeypatch):
             assert torch.equal(again, dx) and torch.equal(x, c3.act8_unpack(pre, dt, act=act))
 
 
+@pytest.mark.parametrize("rows", ["16", "32", "64", "128"])
+@pytest.mark.parametrize("split", ["1", "2", "3", "5", "6", "7", "8"])
+def test_linear_few_rows_in_any_pieces(split, rows, monkeypatch):
+    """Every number of pieces hands every row to one rank, whatever the rows per tile; the same bits again."""
+    monkeypatch.setenv("CONV3D_LINEAR", "1")
+    monkeypatch.setenv("CONV3D_LINEAR_SPLIT", split)
+    monkeypatch.setenv("CONV3D_LINEAR_ROWS", rows)
+    for M, K, N in ((1, 136, 712), (5, 264, 512), (61, 72, 1000), (131, 136, 520)):
+        p = product_case(M, N, K, torch.bfloat16, 19)              # forward: [M, N] -> [M, K]
+        out = run_linear(p, 1, True, True, True)
+        again = run_linear(p, 1, True, True, True)
+        check_linear(p, torch.bfloat16, 1, True, True, *out)
+        assert torch.equal(out[0], again[0]) and torch.equal(out[1].codes, again[1].codes)
+        dy, w = rand((M, N), 19, 4), rand((N, K), 19, 5, K ** -0.5)
+        pre = ckpt(M, K, 19, 1.5)
+        dx, x = c3.linear_bwd_data(dy, w, pre, 2, with_x=True)
+        sync_ok()
+        v = ref.decode(pre)
+        s = ref.slope(v, 2)
+        plain = dy.double() @ w.double()
+        off = (N + 8) * 2.0 ** -23 * (dy.double().abs() @ w.double().abs())
+        want = plain * s
+        bound = off * (s.abs() + ref.slope_error(v, 2)) + plain.abs() * ref.slope_error(v, 2)
+        ref.check(dx, want, ref.rounding(want, dx.dtype) * 1.01 + bound + 2.0 ** -23 * want.abs(), "dx")
+        assert torch.equal(x, c3.act8_unpack(pre, dx.dtype, act=2))
+
+
+@pytest.mark.parametrize("kernel", ["1", "128", "256"])
+@pytest.mark.parametrize("M,K,N", [(1, 8, 64), (61, 1000, 72), (300, 520, 136)])
+def test_linear_gradient_writes_nothing_outside(M, K, N, kernel, monkeypatch):
+    monkeypatch.setenv("CONV3D_LINEAR", kernel)
+    dy, w, pre = rand((M, N), 20, 0), rand((N, K), 20, 1, K ** -0.5), ckpt(M, K, 20, 1.5)
+    d, d_ok = guarded(M * K, torch.bfloat16)
+    x, x_ok = guarded(M * K, torch.bfloat16)
+    assert c3.linear_bwd_data_ptr(dy.data_ptr(), w.data_ptr(), pre.codes.data_ptr(), pre.exponents.data_ptr(), 1, d.data_ptr(),
+                                  x.data_ptr(), M, K, N, c3.BF16, torch.cuda.current_stream().cuda_stream) == c3.Status.OK
+    sync_ok()
+    d_ok()
+    x_ok()
+    assert torch.equal(d.view(M, K), c3.linear_bwd_data(dy, w, pre, 1))
+    assert torch.equal(x.view(M, K), c3.act8_unpack(pre, torch.bfloat16, act=1))
+
+
 @pytest.mark.parametrize("act", [1, 2])
 @pytest.mark.parametrize("M", [37, 700])
 def test_linear_data_gradient_recomputes_any_checkpoint(M, act):
