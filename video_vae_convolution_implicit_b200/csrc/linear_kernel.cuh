@@ -696,9 +696,12 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
     }
     mbar_init(tfull_bar, 1);
     fence_mbar_init();
-    // the weight's way from HBM to L2 may overlap the previous kernel (L2 stays
-    // coherent should that write it)
-    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+    // With a token or a few, the way of the weight's first stages from HBM to L2 may
+    // overlap the previous kernel (L2 stays coherent should that write them): 1 x 512
+    // -> 2048 3.25 us, 3.43 without, 1 x 4096 -> 4096 9.2 and 9.7; 3.22 and 3.14 where
+    // the weight is in L2 already.  All of a long contraction would pass this SM's copy
+    // engine twice (1 x 8192 -> 8192 32.8 us, 26.2 with the first stages only).
+    for (int kb = kb_lo; p.BN <= 32 && kb < kb_hi && kb < kb_lo + p.stages; ++kb) {
       if constexpr (kBwd) {
         for (int i = 0; i < BM / 64; ++i) tma_prefetch_2d(&map_w, ch0 + 64 * i, kb * BK);
       } else {
