@@ -373,10 +373,10 @@ CONV3D_API conv3d_status_t conv3d_bwd_weight_cached(const void* x, const void* p
  * [rows, C], one row a pixel (rows = N*D*H*W of an NDHWC tensor) or token, and
  * C (or K and N) a multiple of 8; 16-bit tensors, fp32 statistics and sums, one
  * round-to-nearest-even to the dtype.  Any number of rows from 1 up (the products:
- * below 2^31 - 65536).  The pages
- * name the operators next to their convolutions (Metal FlashAttention post:
- * GEMM and layer norm shaders with backward passes; LoRA post: training on
- * device, where activation memory is short); the interface is this library's.
+ * below 2^31 - 65536).  The pages name the operators next to their convolutions
+ * (Metal FlashAttention post: GEMM and layer norm shaders with backward passes;
+ * LoRA post: training on device, where activation memory is short); the interface
+ * is this library's.
  *
  * 8-bit activation checkpoint.  A training step keeps activations for its
  * backward pass; a checkpoint keeps one in 1.03 bytes a value.  Blocks of 32
@@ -418,7 +418,8 @@ CONV3D_API conv3d_status_t conv3d_layernorm_fwd(const void* x, const void* gamma
  * dgamma and dbeta ([C]) may each be NULL.  dx may be exactly dy, x or dres.
  * Partial sums in the workspace (conv3d_layernorm_bwd_workspace_bytes(), device,
  * 256-byte aligned, not needed without dgamma and dbeta) are added in a fixed
- * order: the same inputs give the same bits.
+ * order: the same inputs give the same bits.  A workspace, here and below, serves
+ * one call at a time: calls or graphs that may overlap need one each.
  */
 CONV3D_API conv3d_status_t conv3d_layernorm_bwd(const void* dy, const void* x, const float* mean,
                                                 const void* codes, const void* exponents,
