@@ -322,6 +322,42 @@ def test_linear_forward(M, K, N, dtype, kernel, monkeypatch):
         check_linear(p, dt, act, bias, residual, y, a)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 2, 3, 4])
+def test_linear_of_a_token_or_a_few(M, dtype, monkeypatch):
+    """The dot products, chosen and by force: odd sizes, one and two shares of the contraction, contractions that are
+    too long for them (another kernel takes those), guarded outputs, the same bits with and without a checkpoint."""
+    dt = DT[dtype]
+    for K, N in ((8, 8), (24, 40), (512, 2048), (1000, 136), (1024, 520), (1032, 72), (2048, 264), (4096, 64), (4104, 1000),
+                 (8192, 32), (20000, 96), (72, 5000)):
+        p = product_case(M, K, N, dt, 21)
+        for kernel in ("0", "2"):
+            monkeypatch.setenv("CONV3D_LINEAR", kernel)
+            for act, bias, residual in ((0, False, False), (1, True, True), (2, True, False)):
+                y, a = run_linear(p, act, bias, residual, True)
+                plain = run_linear(p, act, bias, residual, False)
+                sync_ok()
+                check_linear(p, dt, act, bias, residual, y, a)
+                assert torch.equal(y, plain)
+    monkeypatch.setenv("CONV3D_LINEAR", "2")
+    K, N = 520, 200
+    p = product_case(M, K, N, dt, 22)
+    y, y_ok = guarded(M * N, dt)
+    q, q_ok = guarded(M * 224, torch.int8)
+    e, e_ok = guarded(M * 7, torch.uint8)
+    y.copy_(p["residual"].flatten())
+    code = c3.BF16 if dt == torch.bfloat16 else c3.F16
+    assert c3.linear_fwd_ptr(p["x"].data_ptr(), p["w"].data_ptr(), p["bias"].data_ptr(), y.data_ptr(), y.data_ptr(),
+                             q.data_ptr(), e.data_ptr(), M, K, N, 2, code, torch.cuda.current_stream().cuda_stream) == c3.Status.OK
+    sync_ok()
+    check_linear(p, dt, 2, True, True, y.view(M, N), c3.Act8(q.view(M, -1), e.view(M, 7), N))
+    for ok in (y_ok, q_ok, e_ok):
+        ok()
+    p["x"][M - 1, 3] = float("nan")                     # a row of NaN leaves the others alone
+    z, a = run_linear(p, 2, True, True, True)
+    assert torch.equal(z[:M - 1], y.view(M, N)[:M - 1]) and torch.isnan(z[M - 1]).all() and (a.exponents[M - 1] == 255).all()
+
+
 @pytest.mark.parametrize("split", ["1", "2", "3", "8"])
 def test_linear_split_along_the_contraction(split, monkeypatch):
     monkeypatch.setenv("CONV3D_LINEAR", "1")

@@ -1,5 +1,5 @@
 // linear.cu -- host side of the channel product (linear_kernel.cuh): argument
-// checks, the choice between the two kernels, tensor maps and launches.
+// checks, the choice between the kernels, tensor maps and launches.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -150,6 +150,35 @@ conv3d_status_t allow_smem(K kern, std::atomic<unsigned long long>& done, int by
   return CONV3D_OK;
 }
 
+// Dot products for one to four rows (forward), where their arithmetic and the
+// blocks' waves cost less than the few-row kernel's latencies.  Measured on B200
+// (bf16, GELU, weights from HBM, us; dot / few rows): 1 x 512 -> 2048 2.1 / 3.3, 1 x
+// 2048 -> 512 3.2 / 4.1, 1 x 4096 -> 4096 8.1 / 9.4, 1 x 8192 -> 1024 8.7 / 8.7, 2 x
+// 2048 -> 2048 4.6 / 5.0, 3 x 1024 -> 1000 3.8 / 3.9, 4 x 512 -> 2048 3.2 / 3.4; but 2 x
+// 4096 -> 4096 9.8 / 9.6, 4 x 1024 -> 1000 4.2 / 3.9 and, in several waves of blocks,
+// 1 x 4096 -> 14336 28.7 / 25.0, 3 x 512 of it 7.6 / 6.1 (1 x 512 of it 5.0 / 6.0).
+bool choose_dot(const Product& P, const Device& dev) {
+  if (P.bwd || P.M > kDotMaxRows || static_cast<long long>(P.M) * P.K * 2 > kDotMaxBytes) return false;
+  const int forced = env_int("CONV3D_LINEAR");   // tuning and tests: 2 wherever it can, 1, 128 and 256 not
+  if (forced != 0) return forced == 2;
+  return (P.M - 1) * P.K <= 2048 && ((P.N + 31) / 32 <= dev.num_sms || (P.K <= 1024 && P.M <= 2));
+}
+
+template <bool kBF16, int kAct, bool kQ>
+conv3d_status_t run_dot(const Product& P, const LinearParams& p, cudaStream_t stream) {
+  const uint16_t* x = static_cast<const uint16_t*>(P.a);
+  const uint16_t* w = static_cast<const uint16_t*>(P.w);
+  const unsigned blocks = static_cast<unsigned>(p.blocks);
+  const size_t smem = static_cast<size_t>(P.M) * P.K * 2;
+  const unsigned threads = P.K > 1024 ? kDotThreads * kDotShares : kDotThreads;
+  if (plan_log())
+    fprintf(stderr, "libconv3d: channel product forward dot products, %d x %d x %d, %u blocks\n", P.M, P.N, P.K, blocks);
+  const cudaError_t e = P.M == 1   ? launch(linear_dot_kernel<kBF16, kAct, kQ, 1>, blocks, threads, smem, 1, stream, x, w, P.K, p)
+                        : P.M == 2 ? launch(linear_dot_kernel<kBF16, kAct, kQ, 2>, blocks, threads, smem, 1, stream, x, w, P.K, p)
+                                   : launch(linear_dot_kernel<kBF16, kAct, kQ, 4>, blocks, threads, smem, 1, stream, x, w, P.K, p);
+  return e == cudaSuccess ? CONV3D_OK : cuda_fail(e, "channel product launch");
+}
+
 template <bool kBF16, bool kBwd, int kAct, bool kQ, bool kValue = false>
 conv3d_status_t run(const Product& P, cudaStream_t stream) {
   Device dev;
@@ -177,6 +206,8 @@ conv3d_status_t run(const Product& P, cudaStream_t stream) {
   p.blocks = (P.N + 31) / 32;
   p.status = dev.status;
   p.timeout_ns = wait_limit_ns();
+  if constexpr (!kBwd)
+    if (choose_dot(P, dev)) return run_dot<kBF16, kAct, kQ>(P, p, stream);
   p.test_stall = take_stall(p.timeout_ns) ? 1 : 0;
   CUtensorMap map_a, map_w;
   if (plan_log())

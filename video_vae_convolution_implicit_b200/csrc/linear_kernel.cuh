@@ -41,9 +41,12 @@
 // in shared memory: w, the bulk of the bytes, streams through as many SMs as
 // there are pieces, in one launch and without a workspace, and the sum runs in
 // rank order whatever the timing.  Measured (bf16, GELU, weights from HBM, graph
-// replays): 1 x 512 -> 2048 3.3 us, 1 x 2048 -> 512 4.0, 61 x 1024 -> 1000 4.9, 64
-// x 2048 -> 2048 6.7: latencies one after the other (a first copy 0.6 us, the
-// following k-blocks 0.3 us each, the meeting of the ranks 0.5 to 1.2 us).
+// replays): 8 x 512 -> 2048 3.5 us, 61 x 1024 -> 1000 4.9, 64 x 2048 -> 2048 6.8:
+// latencies one after the other (a first copy 0.6 us, the following k-blocks 0.3 us
+// each, the meeting of the ranks 0.5 to 1.2 us).
+//
+// linear_dot_kernel (forward, one to four rows): dot products on the ordinary
+// units, for the latency of a token.
 #pragma once
 
 #include "act8.cuh"
@@ -871,6 +874,125 @@ __global__ void __launch_bounds__(kLinRowsThreads, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+// ------------------------------------------------------------------ one to four rows
+
+// Forward with M <= R rows: dot products.  A matrix instruction would have 124 of
+// its 128 rows idle, and what a call of a token costs is latency: here there is no
+// tensor map to fetch, no tensor memory and no cluster to meet.  A block takes 32
+// channels (one checkpoint block), a warp two of them, its lanes their contraction,
+// 16 bytes a load and kUnroll loads of each channel in flight; twice the warps share
+// a contraction of more than 1024.  x lies in shared memory as it came.  fp32 sums
+// per lane, then over the lanes in a fixed tree, then the shares.  Measured (graph
+// replays): 1 x 512 -> 2048 2.1 us (1.9 with the weight in L2; a layer norm of the
+// row takes 1.6), 1 x 4096 -> 4096 8.1 us (4.1 TB/s): loads' latency, in one batch up
+// to a contraction of 2048 and one after the other beyond.
+constexpr int kDotThreads = 512;                       // per share of the contraction
+constexpr int kDotShares = 2;                          // at most, each with its own warps
+constexpr int kDotMaxRows = 4;
+constexpr int kDotMaxBytes = 32 * 1024;                // of x in shared memory
+
+template <bool kBF16, int kAct, bool kQ, int R>
+__global__ void __launch_bounds__(kDotThreads * kDotShares, 1)
+    linear_dot_kernel(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w, const int K, const LinearParams p) {
+  using T = Val16<kBF16>;
+  constexpr int kUnroll = 4;
+  extern __shared__ __align__(16) uint8_t dot_x[];
+  __shared__ float sums[kDotShares][R][32];
+  const int share = threadIdx.x / kDotThreads, shares = blockDim.x / kDotThreads;
+  const int warp = threadIdx.x % kDotThreads / 32, lane = threadIdx.x % 32;
+  const int ch0 = blockIdx.x * 32;
+  const int vecs = K / 8;
+  const int c0 = ch0 + 2 * warp;
+  const bool live = c0 < p.N;                          // N is even: both channels or none
+  const int lo = share * vecs / shares, hi = (share + 1) * vecs / shares;   // this share's vectors
+  const uint4* wa = reinterpret_cast<const uint4*>(w + static_cast<size_t>(live ? c0 : 0) * K);
+  const uint4* wb = wa + vecs;
+  const uint32_t xs = smem_addr(dot_x);
+  // into L2 while the previous kernel ends (L2 stays coherent should that write it)
+#pragma unroll
+  for (int i = 0; i < kUnroll; ++i) {
+    const int v = lo + lane + 32 * i;
+    if (live && v < hi && (lane & 7) == 0) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(wa + v) : "memory");
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(wb + v) : "memory");
+    }
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  uint4 a[kUnroll], b[kUnroll];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int v = base + lane + 32 * i;
+      a[i] = b[i] = make_uint4(0, 0, 0, 0);
+      if (live && v < hi) {
+        a[i] = __ldg(wa + v);
+        b[i] = __ldg(wb + v);
+      }
+    }
+  };
+  load(lo);
+  for (int i = threadIdx.x; i < p.M * vecs; i += blockDim.x) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(x) + i);
+    st_shared_v4(xs + i * 16u, q.x, q.y, q.z, q.w);
+  }
+  __syncthreads();
+  float2 acc[R][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = both(0.0f);
+  for (int base = lo; live && base < hi; base += 32 * kUnroll) {
+    if (base != lo) load(base);
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int v = base + lane + 32 * i;
+      if (v < hi) {
+        float2 fa[4], fb[4];
+        T::unpack8(a[i], fa);
+        T::unpack8(b[i], fb);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (r < p.M) {
+            float2 fx[4];
+            T::unpack8(ld_shared_v4(xs + (r * vecs + v) * 16u), fx);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              acc[r][0] = fma2(fa[e], fx[e], acc[r][0]);
+              acc[r][1] = fma2(fb[e], fx[e], acc[r][1]);
+            }
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float v = acc[r][c].x + acc[r][c].y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+      if (lane == 0) sums[share][r][2 * warp + c] = v;
+    }
+  __syncthreads();
+  if (share != 0 || warp >= p.M) return;               // a warp finishes a row, a lane a channel
+  const int ch = ch0 + lane;
+  const size_t row = warp;
+  float y = sums[0][warp][lane];
+  for (int s = 1; s < shares; ++s) y += sums[s][warp][lane];
+  if (p.bias != nullptr && ch < p.N) y += T::lo(__ldg(p.bias + ch));
+  if constexpr (kQ) {
+    const uint32_t eb = a8_exponent(__reduce_max_sync(0xFFFFFFFFu, a8_mag(y)));
+    p.codes[row * p.blocks * 32 + ch] =
+        static_cast<uint8_t>(a8_code4(make_float2(y, 0.0f), both(0.0f), a8_inv_step(eb)) & 0xFFu);
+    if (lane == 0) p.exponents[row * p.blocks + blockIdx.x] = static_cast<uint8_t>(eb);
+  }
+  y = act_value<kAct>(y);
+  if (ch < p.N) {
+    y += p.residual != nullptr ? T::lo(p.residual[row * p.N + ch]) : 0.0f;
+    p.out[row * p.N + ch] = static_cast<uint16_t>(T::pack(y, 0.0f) & 0xFFFFu);
   }
 }
 
