@@ -810,6 +810,11 @@ __global__ void __launch_bounds__((kFeat & FEAT_GN)     ? GN_THREADS
     const uint32_t rbar = rfull_bar + ew * 16;
     uint32_t rphase[2] = {0, 0};
     bool rpending[2] = {false, false};   // a residual copy into buffer b is in flight
+    // Stores issued by this warp, over all of its tiles: the next chunk's buffer is
+    // the one the store before the last left.  (Counted per tile, a tile with an odd
+    // number of chunks would hand the next one the buffer of the store just issued,
+    // which the wait below lets go on reading.)
+    uint32_t stored = 0;
     int local = 0;
     const uint4* bias4 = reinterpret_cast<const uint4*>(p.bias);
     const int chunks = p.BN / 32;
@@ -920,7 +925,7 @@ __global__ void __launch_bounds__((kFeat & FEAT_GN)     ? GN_THREADS
             }
             if (lane == 0) bulk_wait_group_read<kYBufs - 1>();
             __syncwarp();
-            const uint32_t yb = ybuf + (m & (kYBufs - 1)) * ybytes;
+            const uint32_t yb = ybuf + (stored & (kYBufs - 1)) * ybytes;
             if (f32_tile) {
               // fp32 rows of 32 channels (128 bytes, 128-byte swizzle): this
               // thread's channel is 4-byte word (lane & 3) of 16-byte chunk lane >> 2
@@ -983,6 +988,7 @@ __global__ void __launch_bounds__((kFeat & FEAT_GN)     ? GN_THREADS
                             pix0 + 64 * kJStep, tl.frame_out);
               }
             }
+            if (!kScatter || f32_tile) ++stored;
             if (refill) rpending[b] = true;
           }
         }
@@ -1091,10 +1097,10 @@ __global__ void __launch_bounds__((kFeat & FEAT_GN)     ? GN_THREADS
               v[8 * g + 6] += C::lo(q.w); v[8 * g + 7] += C::hi(q.w);
             }
           }
-          // the store issued from this buffer two chunks ago must have read it
+          // the last store but one issued from this buffer: it must have read it
           if (lane == 0) bulk_wait_group_read<kYBufs - 1>();
           __syncwarp();
-          const uint32_t yb = ybuf + (m & (kYBufs - 1)) * ybytes;
+          const uint32_t yb = ybuf + (stored & (kYBufs - 1)) * ybytes;
           if (f32_tile) {
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -1162,6 +1168,7 @@ __global__ void __launch_bounds__((kFeat & FEAT_GN)     ? GN_THREADS
                           row_base, tl.frame_out);
             }
           }
+          if (!kScatter || f32_tile) ++stored;
           if (refill) rpending[b] = true;
         }
       }
