@@ -8,8 +8,10 @@
 // the exception class that the package hands over (set_error_class).
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAException.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/utils/pybind.h>
 
 #include <climits>
@@ -108,8 +110,13 @@ Act8 checkpoint(const char* name, const Tensor& codes, const Tensor& exponents, 
 
 // The call's device and stream, which become the current ones while it lasts, so
 // that what it allocates belongs to the stream its kernels run on: a temporary
-// freed at its end is not handed to other streams before they have.  (1 and 2 are
-// CUDA's names for the default streams, which torch's allocator does not know.)
+// freed at its end is not handed to other streams before they have.
+//
+// CUDA's own handles of the default streams: 1 is the legacy one, which torch
+// knows as 0; 2 is the calling thread's, which torch's allocator cannot keep
+// blocks for (one handle, another stream in every thread).  Memory comes from the
+// current stream there, whose earlier work the thread's stream waits for (it may
+// still use a block), and whose later work waits for the call (it may get one).
 struct On {
   c10::cuda::CUDAGuard device;
   c10::cuda::OptionalCUDAStreamGuard current;
@@ -119,8 +126,37 @@ struct On {
       stream = c10::cuda::getCurrentCUDAStream(d.index()).stream();
       return;
     }
-    stream = reinterpret_cast<CUstream_st*>(*s);
-    if (*s != 1 && *s != 2) current.reset_stream(c10::cuda::getStreamFromExternal(stream, d.index()));
+    stream = *s == 1 ? nullptr : reinterpret_cast<CUstream_st*>(*s);
+    if (stream == cudaStreamPerThread) {
+      CUstream_st* const memory = c10::cuda::getCurrentCUDAStream(d.index()).stream();
+      C10_CUDA_CHECK(follow(stream, memory));
+      lender = memory;
+      lends = true;
+    } else {
+      current.reset_stream(c10::cuda::getStreamFromExternal(stream, d.index()));
+    }
+  }
+  On(const On&) = delete;
+  ~On() {
+    if (lends && follow(lender, stream) != cudaSuccess) {
+      // the order cannot be had on the device: have it here
+      cudaGetLastError();
+      cudaStreamSynchronize(stream);
+    }
+  }
+
+ private:
+  CUstream_st* lender = nullptr;   // the stream whose memory a call on handle 2 uses,
+  bool lends = false;              // and whether there is one
+  // What `later` is given from now on waits for what `earlier` was given before.
+  static cudaError_t follow(cudaStream_t later, cudaStream_t earlier) {
+    cudaEvent_t event;
+    cudaError_t e = cudaEventCreateWithFlags(&event, cudaEventDisableTiming);
+    if (e != cudaSuccess) return e;
+    e = cudaEventRecord(event, earlier);
+    if (e == cudaSuccess) e = cudaStreamWaitEvent(later, event, 0);
+    cudaEventDestroy(event);   // its resources go when it has completed
+    return e;
   }
 };
 
@@ -201,6 +237,7 @@ std::tuple<Tensor, OptTensor, OptTensor> layernorm_bwd(const Tensor& dy, const O
                                                        const OptTensor& dres, bool with_params, const OptTensor& dx,
                                                        const OptTensor& workspace, const OptStream& stream) {
   const Lead l("dy", dy);
+  Tensor ws;   // outlives `on`, which sees to it that its next owner waits
   const On on(l.device, stream);
   const void* r = operand("rstd", rstd, l.device, at::kFloat, l.lead());
   const void *xp = nullptr, *m = nullptr;
@@ -217,7 +254,7 @@ std::tuple<Tensor, OptTensor, OptTensor> layernorm_bwd(const Tensor& dy, const O
   const void* s = operand("dres", dres, l, dy.sizes());
   operand("dx", dx, l, dy.sizes());
   Tensor out = dx.has_value() ? *dx : l.empty(dy.sizes());
-  Tensor dgamma, dbeta, ws;
+  Tensor dgamma, dbeta;
   size_t ws_bytes = 0;
   if (with_params) {
     dgamma = l.empty({l.C});
@@ -297,11 +334,12 @@ std::tuple<Tensor, OptTensor> linear_bwd_data(const Tensor& dy, const Tensor& w,
 std::tuple<Tensor, OptTensor> linear_bwd_weight(const Tensor& x, const Tensor& dy, bool with_bias,
                                                 const OptTensor& workspace, const OptStream& stream) {
   const Lead l("x", x);
+  Tensor ws;   // outlives `on`, which sees to it that its next owner waits
   const On on(l.device, stream);
   TORCH_CHECK_VALUE(dy.dim() >= 1, "dy must be [..., N]");
   const int N = Lead::narrow(dy.size(-1));
   const void* d = operand("dy", dy, l.device, l.type, l.with(N));
-  Tensor dw = l.empty({N, l.C}), db, ws;
+  Tensor dw = l.empty({N, l.C}), db;
   if (with_bias) db = l.empty({N});
   if (workspace.has_value()) {
     TORCH_CHECK_VALUE(workspace->device() == l.device && workspace->is_contiguous(),
