@@ -317,21 +317,27 @@ bool lo8_enabled() {
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
 PFN_cuTensorMapEncodeIm2col_v12000 g_encode_im2col = nullptr;
+PFN_cuCtxGetCurrent_v4000 g_ctx_get_current = nullptr;
 std::once_flag g_entry_once;
 cudaError_t g_entry_err = cudaSuccess;
 
 conv3d_status_t load_entry_points() {
   std::call_once(g_entry_once, [] {
-    cudaDriverEntryPointQueryResult q1, q2;
+    cudaDriverEntryPointQueryResult q1, q2, q3;
     void* p1 = nullptr;
     void* p2 = nullptr;
+    void* p3 = nullptr;
     cudaError_t e1 = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p1, cudaEnableDefault, &q1);
     cudaError_t e2 = cudaGetDriverEntryPoint("cuTensorMapEncodeIm2col", &p2, cudaEnableDefault, &q2);
+    cudaError_t e3 = cudaGetDriverEntryPoint("cuCtxGetCurrent", &p3, cudaEnableDefault, &q3);
     if (e1 != cudaSuccess || q1 != cudaDriverEntryPointSuccess || !p1) {
       g_entry_err = e1 != cudaSuccess ? e1 : cudaErrorNotSupported;
     } else if (e2 != cudaSuccess || q2 != cudaDriverEntryPointSuccess || !p2) {
       g_entry_err = e2 != cudaSuccess ? e2 : cudaErrorNotSupported;
+    } else if (e3 != cudaSuccess || q3 != cudaDriverEntryPointSuccess || !p3) {
+      g_entry_err = e3 != cudaSuccess ? e3 : cudaErrorNotSupported;
     } else {
+      g_ctx_get_current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(p3);
       g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p1);
       g_encode_im2col = reinterpret_cast<PFN_cuTensorMapEncodeIm2col_v12000>(p2);
     }
@@ -474,13 +480,16 @@ conv3d_status_t device_state(DeviceState*& out, int& dev) {
     set_error("device ordinal %d out of range", dev);
     return CONV3D_ERR_CUDA;
   }
-  // A thread that has made no CUDA call yet (autograd's, a user's worker) has no
-  // current context, which the tensor-map encoder needs; cudaSetDevice makes it so.
-  static thread_local int bound = -1;
-  if (bound != dev) {
-    if ((e = cudaSetDevice(dev)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
-    bound = dev;
-  }
+  // The tensor-map encoder needs a current context.  A thread that has made no CUDA
+  // call yet (autograd's, a user's worker), or has left its context, has none:
+  // cudaSetDevice makes the device's own one current.  One that the caller has made
+  // current stays.
+  const conv3d_status_t st = load_entry_points();
+  if (st != CONV3D_OK) return st;
+  CUcontext current = nullptr;
+  if ((g_ctx_get_current(&current) != CUDA_SUCCESS || current == nullptr) &&
+      (e = cudaSetDevice(dev)) != cudaSuccess)
+    return cuda_fail(e, "cudaSetDevice");
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState& s = g_dev[dev];
   if (!s.init) {
