@@ -84,11 +84,24 @@ if not os.path.exists(lib_path):
     raise ImportError(f"{lib_path} is missing: build it with "
                       "`python video_vae_convolution_implicit_b200/build.py` (nvcc, sm_100a)")
 _lib = ctypes.CDLL(lib_path)
+
+
+class _NoBinding:
+    """Stands in for the native binding where it does not load (not built, or built
+    against another torch): the calls that need it say so, the others do without."""
+
+    def __init__(self, cause: ImportError):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError("the native binding _channel.so is missing or does not load: build it with "
+                          "`python video_vae_convolution_implicit_b200/build.py`") from self._cause
+
+
 try:
     from . import _channel   # the native calls of the channel-wise operators (csrc/binding.cpp)
 except ImportError as e:
-    raise ImportError("the native binding _channel.so is missing or does not load: build it with "
-                      "`python video_vae_convolution_implicit_b200/build.py`") from e
+    _channel = _NoBinding(e)
 
 _i3 = ctypes.c_int * 3
 _vp = ctypes.c_void_p
@@ -165,7 +178,8 @@ _lib.conv3d_linear_bwd_weight.argtypes = [_vp] * 4 + [_ll, _c, _c, _c, _vp, ctyp
 _lib.conv3d_linear_bwd_weight_workspace_bytes.restype = ctypes.c_size_t
 _lib.conv3d_linear_bwd_weight_workspace_bytes.argtypes = [_ll, _c, _c]
 
-_channel.set_error_class(Conv3dError)
+if not isinstance(_channel, _NoBinding):
+    _channel.set_error_class(Conv3dError)
 
 
 def raw_library() -> ctypes.CDLL:

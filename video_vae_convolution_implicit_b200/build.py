@@ -2,7 +2,8 @@
 
 The translation units are compiled side by side into build/ (one object each,
 recompiled when it or a header is newer) and linked; then the native Python
-binding of the channel-wise operators, _channel.so, against torch's headers.
+binding of the channel-wise operators, _channel.so, against torch's headers
+(again when torch or Python is another one than it was built for).
 """
 from __future__ import annotations
 
@@ -16,6 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(ROOT, "build")
 LIB = os.path.join(PKG, "libconv3d.so")
 BINDING = os.path.join(PKG, "_channel.so")
+BUILT_FOR = os.path.join(OBJ, "_channel.built_for")
 SOURCES = [os.path.join(CSRC, f) for f in ("conv3d_api.cu", "groupnorm.cu", "channel_ops.cu", "linear.cu")]
 # the headers that each unit includes (besides the public one)
 HEADERS = {
@@ -53,6 +55,20 @@ def binding_command() -> list[str]:
             "-L", PKG, "-l:libconv3d.so", "-Wl,-rpath,$ORIGIN"]
 
 
+def binding_target() -> str:
+    """What the binding is built for: it fits no other torch or Python."""
+    from importlib.metadata import version
+    return f"torch {version('torch')}, Python {sys.version.split()[0]}\n"
+
+
+def binding_stale() -> bool:
+    deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "conv3d.h")]
+    if _newer(deps, BINDING) or not os.path.exists(BUILT_FOR):
+        return True
+    with open(BUILT_FOR) as f:
+        return f.read() != binding_target()
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if force or _newer([d for s in SOURCES for d in _deps(s)], LIB):
         os.makedirs(OBJ, exist_ok=True)
@@ -69,9 +85,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise subprocess.CalledProcessError(1, failed[0])
         subprocess.run(["nvcc", "-gencode", "arch=compute_100a,code=sm_100a", "--shared", "-o", LIB, *objects],
                        check=True)
-    binding_deps = [os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "conv3d.h")]
-    if force or _newer(binding_deps, BINDING):
+    if force or binding_stale():
         subprocess.run(binding_command(), check=True)
+        os.makedirs(OBJ, exist_ok=True)
+        with open(BUILT_FOR, "w") as f:
+            f.write(binding_target())
     return LIB
 
 
