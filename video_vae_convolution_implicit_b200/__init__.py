@@ -564,11 +564,13 @@ class Conv3dFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, residual, stride, pad, tpad, checkpoint8=False):
         y = conv3d(x, w, bias, residual, stride, pad, tpad)
-        if checkpoint8:
+        if not checkpoint8:
+            ctx.save_for_backward(w, x)
+        elif ctx.needs_input_grad[1] or (bias is not None and ctx.needs_input_grad[2]):
             a = act8_pack(x)
             ctx.save_for_backward(w, a.codes, a.exponents)
         else:
-            ctx.save_for_backward(w, x)
+            ctx.save_for_backward(w)   # nothing will read x
         ctx.conf = (tuple(stride), tuple(pad), tpad, bias is not None, residual is not None)
         ctx.x_shape = tuple(x.shape)
         return y
@@ -597,8 +599,10 @@ class Conv3dFunction(torch.autograd.Function):
 def conv3d_autograd(x, w, bias=None, residual=None, stride=(1, 1, 1), pad=(0, 1, 1),
                     tpad=TPAD_CAUSAL_REPLICATE, checkpoint8=False):
     """y = conv3d(x, w) + bias + residual with gradients for x, w, bias and residual.
-    checkpoint8: keep x for the weight gradient in 8 bits (1.03 bytes a value)."""
-    return Conv3dFunction.apply(x, w, bias, residual, tuple(stride), tuple(pad), tpad, checkpoint8)
+    checkpoint8: keep x for the weight gradient in 8 bits (1.03 bytes a value); where neither
+    w nor bias needs a gradient, or none is recorded, nothing is kept of x."""
+    return Conv3dFunction.apply(x, w, bias, residual, tuple(stride), tuple(pad), tpad,
+                                checkpoint8 and torch.is_grad_enabled())
 
 
 # ---------------------------------------------------------------- channel-wise operators
