@@ -47,3 +47,35 @@ def test_conv3d_keeps_no_checkpoint_that_nothing_reads():
     _, db = c3.conv3d_bwd_weight(x, dy, (3, 3, 3))
     torch.testing.assert_close(grads[2].float(), db.float(), rtol=2.0 ** -7, atol=0)
     assert c3.poll_status() == c3.Status.OK
+
+
+def _calls():
+    x, w, b = rand((64, 64), 10), rand((64, 64), 11, 0.125), rand((64,), 12)
+    clip, kernel = rand((1, 2, 8, 8, 64), 13), rand((64, 3, 3, 3, 64), 14, 0.025)
+    return {
+        "layernorm": (c3.layernorm_autograd, (x, b, b)),
+        "layernorm checkpoint": (lambda *t: c3.layernorm_autograd(*t, checkpoint8=True), (x, b, b)),
+        "linear": (c3.linear_autograd, (x, w, b)),
+        "linear gelu": (lambda *t: c3.linear_autograd(*t, act=c3.ACT_GELU), (x, w, b)),
+        "mlp": (c3.channel_mlp_autograd, (x, b, b, w, b, w, b)),
+        "conv3d": (c3.conv3d_autograd, (clip, kernel, b)),
+    }
+
+
+@pytest.mark.parametrize("name", ["layernorm", "layernorm checkpoint", "linear", "linear gelu", "mlp", "conv3d"])
+def test_second_derivatives_are_refused(name):
+    """The gradients of these calls carry no graph: a loss with a gradient in it would
+    lose that term without a word."""
+    call, tensors = _calls()[name]
+    leaves = [t.clone().requires_grad_() for t in tensors]
+    y = call(*leaves)
+    dy = rand(tuple(y.shape), 15)
+    plain = torch.autograd.grad(y, leaves, dy, retain_graph=True)
+    grads = torch.autograd.grad(y, leaves, dy, create_graph=True)
+    for g, p in zip(grads, plain):
+        # (the convolution's weight gradient adds its parts in any order)
+        torch.testing.assert_close(g, p, rtol=0 if name != "conv3d" else 2.0 ** -7, atol=0 if name != "conv3d" else 1e-3)
+    for g in grads:
+        with pytest.raises(RuntimeError, match="differentiable once"):   # whatever dy depends on
+            g.float().square().sum().backward(retain_graph=True)
+    assert c3.poll_status() == c3.Status.OK

@@ -24,6 +24,7 @@ linear_bwd_data, linear_bwd_weight) and the channel MLP block made of them
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -554,12 +555,40 @@ def conv3d_bwd_weight_cached(x: torch.Tensor, prev: torch.Tensor | None, dy: tor
     return dw, db
 
 
+class _NoSecondDerivative(torch.autograd.Function):
+    """Passes gradients on and refuses to be differentiated."""
+
+    @staticmethod
+    def forward(ctx, anchor, *grads):
+        return tuple(g if g is None else g.detach() for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("libconv3d's gradients are differentiable once: they carry no graph of their own")
+
+
+def _differentiable_once(backward):
+    """A Function's backward whose results refuse to be differentiated again.  (torch's
+    once_differentiable lets them pass as constants where the upstream gradient is one,
+    although they depend on the call's inputs too.)"""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, dy):
+        with torch.no_grad():
+            grads = backward(ctx, dy)
+        if not torch.is_grad_enabled():          # not within create_graph=True
+            return grads
+        return _NoSecondDerivative.apply(dy.new_empty(0).requires_grad_(), *grads)
+    return wrapped
+
+
 class Conv3dFunction(torch.autograd.Function):
     """torch.autograd wrapper: forward through conv3d_fwd, backward through
     conv3d_bwd_data (dx; temporal stride 1) and conv3d_bwd_weight (dw, dbias).
     The residual's gradient is dy itself.  With checkpoint8 the input is kept as
     an 8-bit checkpoint (Act8), which only dw reads.  Marshalling only: every
-    product runs in the library's kernels, none in torch."""
+    product runs in the library's kernels, none in torch.  Differentiable once, as
+    all of these wrappers are: a second derivative is refused."""
 
     @staticmethod
     def forward(ctx, x, w, bias, residual, stride, pad, tpad, checkpoint8=False):
@@ -576,6 +605,7 @@ class Conv3dFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, dy):
         w, *saved = ctx.saved_tensors
         stride, pad, tpad, has_bias, has_res = ctx.conf
@@ -808,6 +838,7 @@ class LayerNormFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, dy):
         gamma, rstd, s0, s1 = ctx.saved_tensors
         checkpoint8, C = ctx.conf
@@ -838,6 +869,7 @@ class LinearFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, dy):
         x, w, *a = ctx.saved_tensors
         act, has_bias, has_res = ctx.conf
@@ -872,6 +904,7 @@ class ChannelMlpFunction(torch.autograd.Function):
         return y
 
     @staticmethod
+    @_differentiable_once
     def backward(ctx, dy):
         gamma, beta, w1, w2, qc, qe, rstd, pc, pe = ctx.saved_tensors
         act, C, H, has_b1, has_b2 = ctx.conf
