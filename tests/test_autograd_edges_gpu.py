@@ -79,3 +79,42 @@ def test_second_derivatives_are_refused(name):
         with pytest.raises(RuntimeError, match="differentiable once"):   # whatever dy depends on
             g.float().square().sum().backward(retain_graph=True)
     assert c3.poll_status() == c3.Status.OK
+
+
+def _in_place_calls():
+    """name: (a tensor that a call will overwrite, the call)"""
+    x, w, b = rand((64, 64), 20), rand((64, 64), 21, 0.125), rand((64,), 22)
+    clip, kernel = rand((1, 2, 8, 8, 64), 23), rand((64, 1, 1, 1, 64), 24, 0.125)
+    a8 = c3.act8_pack(x)
+    _, mean, rstd = c3.layernorm(x, with_stats=True)
+    stats = c3.groupnorm_stats(clip, 8)
+    flat = dict(pad=(0, 0, 0), tpad=c3.TPAD_ZERO)
+    return {
+        "layernorm": (x, lambda t: c3.layernorm(t, y=t)),
+        "layernorm_bwd": (x, lambda t: c3.layernorm_bwd(t, x, rstd, mean, dx=t)),
+        "act8_unpack": (x, lambda t: c3.act8_unpack(a8, BF, y=t)),
+        "act8_bwd": (x, lambda t: c3.act8_bwd(t, a8, c3.ACT_SILU, dx=t)),
+        "linear": (x, lambda t: c3.linear(x, w, b, t, y=t)),
+        "linear_bwd_data": (x, lambda t: c3.linear_bwd_data(x, w, dx=t)),
+        "conv3d_fwd": (clip, lambda t: c3.conv3d_fwd(clip, kernel, b, None, t, **flat)),
+        "conv3d_gn": (clip, lambda t: c3.conv3d_gn(clip, None, None, None, kernel, y=t, **flat)),
+        "groupnorm_silu": (clip, lambda t: c3.groupnorm_silu(t, stats, y=t)),
+        "groupnorm_stats": (stats, lambda t: c3.groupnorm_stats(clip, 8, stats=t)),
+        "conv3d_bwd_data": (clip, lambda t: c3.conv3d_bwd_data(clip, kernel, clip.shape, dx=t, **flat)),
+    }
+
+
+@pytest.mark.parametrize("name", [
+    "layernorm", "layernorm_bwd", "act8_unpack", "act8_bwd", "linear", "linear_bwd_data", "conv3d_fwd", "conv3d_gn",
+    "groupnorm_silu", "groupnorm_stats", "conv3d_bwd_data"])
+def test_autograd_notices_an_overwritten_tensor(name):
+    tensor, call = _in_place_calls()[name]
+    t = tensor.clone()
+    leaf = torch.ones_like(t).requires_grad_()
+    z = (leaf * t).sum()              # saves t
+    call(t)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        z.backward()
+    with torch.inference_mode():      # tensors without a version
+        call(tensor.clone())
+    assert c3.poll_status() == c3.Status.OK

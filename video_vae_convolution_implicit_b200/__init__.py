@@ -267,6 +267,14 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _overwritten(*tensors) -> None:
+    """Tensors of the caller's that a call writes: autograd is told, as torch's own in-place
+    operators tell it, so that a backward pass which saved one of them notices."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def conv3d_fwd(x: torch.Tensor, w: torch.Tensor, bias, residual, y: torch.Tensor,
                stride=(1, 1, 1), pad=(0, 1, 1), tpad=TPAD_CAUSAL_REPLICATE, stream=None,
                workspace: torch.Tensor | None = None, prev: torch.Tensor | None = None
@@ -319,6 +327,7 @@ def conv3d_fwd(x: torch.Tensor, w: torch.Tensor, bias, residual, y: torch.Tensor
                                H, W, Cout, (kt, kh, kw), stride, pad, tpad, code,
                                _ptr(workspace), workspace.numel() * workspace.element_size(), s)
     _check(st)
+    _overwritten(y)
     return y
 
 
@@ -369,6 +378,7 @@ def conv3d_gn(x: torch.Tensor, stats, gamma, beta, w: torch.Tensor, bias=None,
                          y.data_ptr(), N, Cin, D, H, W, Cout, (kt, kh, kw), stride, pad, tpad,
                          _dtype_code(x.dtype), _stream_handle(stream), _ptr(out_stats), out_groups,
                          out_eps))
+    _overwritten(y)
     return (y, out_stats) if out_stats is not None else y
 
 
@@ -420,6 +430,7 @@ def groupnorm_stats(x: torch.Tensor, groups: int, eps: float = 1e-6, per_frame: 
         raise ValueError(f"stats must be float64 {(sets, groups, 2)}")
     _check(groupnorm_stats_ptr(x.data_ptr(), N, D, H, W, C, groups, per_frame, eps,
                                _dtype_code(x.dtype), stats.data_ptr(), _stream_handle(stream)))
+    _overwritten(stats)
     return stats
 
 
@@ -440,6 +451,7 @@ def groupnorm_silu(x: torch.Tensor, stats: torch.Tensor, gamma=None, beta=None, 
     _check(groupnorm_silu_ptr(x.data_ptr(), stats.data_ptr(), _ptr(gamma), _ptr(beta),
                               y.data_ptr(), N, D, H, W, C, groups, per_frame, apply_silu,
                               _dtype_code(x.dtype), _stream_handle(stream)))
+    _overwritten(y)
     return y
 
 
@@ -474,6 +486,7 @@ def conv3d_bwd_data(dy: torch.Tensor, w: torch.Tensor, x_shape, pad=(0, 1, 1),
     _check(conv3d_bwd_data_ptr(dy.data_ptr(), w.data_ptr(), dx.data_ptr(), N, Cin, D, H, W, Cout,
                                (kt, kh, kw), tuple(stride), pad, tpad, _dtype_code(dy.dtype),
                                workspace.data_ptr(), workspace.numel(), _stream_handle(stream)))
+    _overwritten(dx)
     return dx
 
 

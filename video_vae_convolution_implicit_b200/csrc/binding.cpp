@@ -92,6 +92,12 @@ void* operand(const char* name, const OptTensor& t, const Lead& l, at::IntArrayR
   return t.has_value() ? operand(name, *t, l.device, l.type, shape) : nullptr;
 }
 
+// A tensor of the caller's that the call writes: autograd is told, as torch's own
+// in-place operators tell it, so that a backward pass which saved it notices.
+void overwritten(const OptTensor& t) {
+  if (t.has_value() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 struct Act8 {
   void* codes;
   void* exponents;
@@ -192,6 +198,7 @@ Tensor act8_unpack(const Tensor& codes, const Tensor& exponents, int64_t channel
   const void* b = beta.has_value() ? operand("beta", *beta, device, type, {channels}) : nullptr;
   check_status(conv3d_act8_unpack(a.codes, a.exponents, g, b, act_of(act), out.data_ptr(), C > 0 ? out.numel() / C : 0,
                                   C, code, on.stream));
+  overwritten(y);
   return out;
 }
 
@@ -204,6 +211,7 @@ Tensor act8_bwd(const Tensor& dy, const Tensor& codes, const Tensor& exponents, 
   Tensor out = dx.has_value() ? *dx : l.empty(dy.sizes());
   check_status(conv3d_act8_bwd(dy.data_ptr(), a.codes, a.exponents, act_of(act), out.data_ptr(), l.rows, l.C, l.code,
                                on.stream));
+  overwritten(dx);
   return out;
 }
 
@@ -225,6 +233,7 @@ py::object layernorm(const Tensor& x, const OptTensor& gamma, const OptTensor& b
       x.data_ptr(), g, b, out.data_ptr(), with_stats ? mean.data_ptr<float>() : nullptr,
       with_stats || checkpoint8 ? rstd.data_ptr<float>() : nullptr, checkpoint8 ? codes.data_ptr() : nullptr,
       checkpoint8 ? exponents.data_ptr() : nullptr, l.rows, l.C, static_cast<float>(eps), l.code, on.stream));
+  overwritten(y);
   if (checkpoint8) return py::make_tuple(out, codes, exponents, rstd);
   if (with_stats) return py::make_tuple(out, mean, rstd);
   return py::cast(out);
@@ -272,6 +281,7 @@ std::tuple<Tensor, OptTensor, OptTensor> layernorm_bwd(const Tensor& dy, const O
                                     static_cast<const float*>(r), g, s, out.data_ptr(),
                                     with_params ? dgamma.data_ptr() : nullptr, with_params ? dbeta.data_ptr() : nullptr,
                                     l.rows, l.C, l.code, with_params ? ws.data_ptr() : nullptr, ws_bytes, on.stream));
+  overwritten(dx);
   if (!with_params) return {out, std::nullopt, std::nullopt};
   return {out, dgamma, dbeta};
 }
@@ -302,6 +312,7 @@ py::object linear(const Tensor& x, const Tensor& w, const OptTensor& bias, const
   check_status(conv3d_linear_fwd(x.data_ptr(), wp, b, r, out.data_ptr(), checkpoint8 ? codes.data_ptr() : nullptr,
                                  checkpoint8 ? exponents.data_ptr() : nullptr, l.rows, l.C, N, act_of(act), l.code,
                                  on.stream));
+  overwritten(y);
   if (checkpoint8) return py::make_tuple(out, codes, exponents);
   return py::cast(out);
 }
@@ -327,6 +338,7 @@ std::tuple<Tensor, OptTensor> linear_bwd_data(const Tensor& dy, const Tensor& w,
   if (with_x) x = l.empty(shape);
   check_status(conv3d_linear_bwd_data(dy.data_ptr(), wp, a.codes, a.exponents, act_of(act), out.data_ptr(),
                                       with_x ? x.data_ptr() : nullptr, l.rows, K, l.C, l.code, on.stream));
+  overwritten(dx);
   if (!with_x) return {out, std::nullopt};
   return {out, x};
 }
