@@ -93,113 +93,90 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // ------------------------------------------------------------------ activations
 
-// One special-function operation per activation: the hardware tanh, whose
-// error is about 2^-11 of a result of magnitude at most 1.  silu(v) = h + h
-// tanh(h), h = v/2; gelu(v) = h + h tanh(u(v)), u = sqrt(2/pi) (v + 0.044715
-// v^3).  The absolute error is at most |v| 2^-12, under half a bf16 step of v.
-__device__ __forceinline__ float tanh_hw(float x) {
-  float t;
-  asm("tanh.approx.f32 %0, %1;" : "=f"(t) : "f"(x));
-  return t;
+// silu(v) = v s(v), gelu(v) = v s(2 u(v)) with s(x) = 1 / (1 + e^-x) and u = sqrt(2/pi)
+// (v + 0.044715 v^3): two special-function operations, 2^w and a reciprocal, w =
+// -log2(e) times the argument of s.  Both are relative approximations, and w is off by
+// a few 2^-24 of itself, so the relative error stays below 2^-15 out to the smallest
+// results (h + h tanh(h), h = v/2, needs one operation, but the hardware tanh's error
+// of 2^-11 is relative to v and not to the result: silu(-8) = -0.0027 could be off by
+// 0.0020).  s below 2^-126 is 0, in both places that can find it so: 2^w is infinite
+// from w = 128 on, and the reciprocal flushes what lies below the normal numbers.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
 
-constexpr float kGeluA = 0.7978845608028654f;             // sqrt(2 / pi)
-constexpr float kGeluC = 0.7978845608028654f * 0.044715f;
+constexpr double kLog2e = 1.4426950408889634, kGeluA = 0.7978845608028654;   // sqrt(2 / pi)
+constexpr float kSiluW = static_cast<float>(-kLog2e);
+constexpr float kGeluW1 = static_cast<float>(-2.0 * kGeluA * kLog2e);
+constexpr float kGeluW3 = static_cast<float>(-2.0 * kGeluA * kLog2e * 0.044715);
+// 2 u'(v) = kGeluD0 + kGeluD2 v^2
+constexpr float kGeluD0 = static_cast<float>(2.0 * kGeluA), kGeluD2 = static_cast<float>(6.0 * kGeluA * 0.044715);
 
+// w of v, and of v = 2 h: the same bits (the constants differ by powers of two).
 template <int kAct>
-__device__ __forceinline__ float act_value(float v) {
-  if constexpr (kAct == kActSilu) {
-    const float h = 0.5f * v;
-    return fmaf(h, tanh_hw(h), h);
-  } else if constexpr (kAct == kActGelu) {
-    const float u = v * fmaf(kGeluC, v * v, kGeluA);
-    const float h = 0.5f * v;
-    return fmaf(h, tanh_hw(u), h);
-  } else {
-    return v;
-  }
+__device__ __forceinline__ float2 act_exponent(float2 v) {
+  if constexpr (kAct == kActSilu) return mul2(v, both(kSiluW));
+  return mul2(v, fma2(both(kGeluW3), mul2(v, v), both(kGeluW1)));
 }
-
-// silu'(v) = s + v s (1 - s) with s = (1 + t)/2, t = tanh(v/2):
-//   = (1 + t)/2 + (v/4) (1 - t^2).
-// gelu'(v) = (1 + t)/2 + (v/2) (1 - t^2) u'(v), t = tanh(u(v)).
 template <int kAct>
-__device__ __forceinline__ float act_slope(float v) {
-  if constexpr (kAct == kActSilu) {
-    const float t = tanh_hw(0.5f * v);
-    const float c = 0.25f * v;
-    return fmaf(c, fmaf(-t, t, 1.0f), fmaf(0.5f, t, 0.5f));
-  } else if constexpr (kAct == kActGelu) {
-    const float v2 = v * v;
-    const float t = tanh_hw(v * fmaf(kGeluC, v2, kGeluA));
-    const float c = 0.5f * v * fmaf(3.0f * kGeluC, v2, kGeluA);
-    return fmaf(c, fmaf(-t, t, 1.0f), fmaf(0.5f, t, 0.5f));
-  } else {
-    return 1.0f;
-  }
+__device__ __forceinline__ float2 act_exponent_of_half(float2 h, float2 h2) {
+  if constexpr (kAct == kActSilu) return mul2(h, both(2.0f * kSiluW));
+  return mul2(h, fma2(both(8.0f * kGeluW3), h2, both(2.0f * kGeluW1)));
 }
-
-// The same for a pair: all but the two tanh in packed operations.
-__device__ __forceinline__ float2 tanh_hw2(float2 x) { return make_float2(tanh_hw(x.x), tanh_hw(x.y)); }
 
 template <int kAct>
 __device__ __forceinline__ float2 act_value(float2 v) {
-  if constexpr (kAct == kActSilu) {
-    const float2 h = mul2(both(0.5f), v);
-    return fma2(h, tanh_hw2(h), h);
-  } else if constexpr (kAct == kActGelu) {
-    const float2 u = mul2(v, fma2(both(kGeluC), mul2(v, v), both(kGeluA)));
-    const float2 h = mul2(both(0.5f), v);
-    return fma2(h, tanh_hw2(u), h);
-  } else {
-    return v;
-  }
+  if constexpr (kAct == kActNone) return v;
+  return mul2(v, rcp(add2(ex2(act_exponent<kAct>(v)), both(1.0f))));
+}
+template <int kAct>
+__device__ __forceinline__ float act_value(float v) {
+  return act_value<kAct>(both(v)).x;
 }
 
-// The derivative in terms of h = v/2, which the checkpoint's values are decoded
-// to (half the step): with q = t^2 - 1,
-//   silu'(v) = (1 + t)/2 - (h/2) q,                      t = tanh(h)
-//   gelu'(v) = (1 + t)/2 - h (a + 12 c h^2) q,           t = tanh(h (2a + 8 c h^2)),
-// a = sqrt(2/pi), c = 0.044715 a.
+// Both derivatives are s + c s (1 - s) = s (1 + c (1 - s)), 1 - s = 2^w s, with c = v
+// (silu) or 2 v u'(v) (gelu).  Beyond |v| = 88 and 10.03, where w passes +-126.9, s is
+// 0 or 1 exactly (and 2^w still finite); v^3 may overflow there, which would leave
+// infinity times zero: such arguments are brought back to these bounds.
+template <int kAct>
+__host__ __device__ constexpr float act_half_bound() {
+  return kAct == kActSilu ? 44.0f : 5.015f;
+}
+
+// The derivative at v = 2 h (the checkpoint's values are decoded to their halves), and
+// the value there from the same s; `whole` is h before it was brought within the bound,
+// which the value goes on growing with.
+template <int kAct>
+__device__ __forceinline__ float2 act_slope_and_value(float2 whole, float2 h, float2& value) {
+  const float2 h2 = kAct == kActGelu ? mul2(h, h) : h;
+  const float2 e = ex2(act_exponent_of_half<kAct>(h, h2));
+  const float2 s = rcp(add2(e, both(1.0f)));
+  value = mul2(add2(whole, whole), s);
+  const float2 c = kAct == kActGelu ? mul2(h, fma2(both(8.0f * kGeluD2), h2, both(2.0f * kGeluD0))) : add2(h, h);
+  return mul2(s, fma2(c, mul2(e, s), both(1.0f)));
+}
 template <int kAct>
 __device__ __forceinline__ float2 act_slope_of_half(float2 h) {
-  if constexpr (kAct == kActSilu) {
-    const float2 t = tanh_hw2(h);
-    return fma2(mul2(h, both(-0.5f)), fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
-  } else if constexpr (kAct == kActGelu) {
-    const float2 h2 = mul2(h, h);
-    const float2 t = tanh_hw2(mul2(h, fma2(both(8.0f * kGeluC), h2, both(2.0f * kGeluA))));
-    const float2 c = mul2(h, fma2(both(-12.0f * kGeluC), h2, both(-kGeluA)));
-    return fma2(c, fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
-  } else {
-    return both(1.0f);
-  }
+  if constexpr (kAct == kActNone) return both(1.0f);
+  float2 value;
+  return act_slope_and_value<kAct>(h, h, value);
 }
 
-// The derivative and the value, h + h t, from one tanh.  `hc` is h brought back
-// to +-32 (the same h where the block's step keeps it there).
-template <int kAct>
-__device__ __forceinline__ float2 act_slope_and_value(float2 h, float2 hc, float2& value) {
-  if constexpr (kAct == kActSilu) {
-    const float2 t = tanh_hw2(hc);
-    value = fma2(h, t, h);
-    return fma2(mul2(hc, both(-0.5f)), fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
-  } else {
-    const float2 h2 = mul2(hc, hc);
-    const float2 t = tanh_hw2(mul2(hc, fma2(both(8.0f * kGeluC), h2, both(2.0f * kGeluA))));
-    value = fma2(h, t, h);
-    const float2 c = mul2(hc, fma2(both(-12.0f * kGeluC), h2, both(-kGeluA)));
-    return fma2(c, fma2(t, t, both(-1.0f)), fma2(both(0.5f), t, both(0.5f)));
-  }
-}
-
-// Beyond |v| = 64 both derivatives are 0 or 1, t has long been -1 or 1 exactly,
-// and v^3 may overflow, which would leave infinity times zero: such arguments
-// are brought back to +-64.  (NaN stays: fminf and fmaxf would drop it.)
+// The same at any v.  (NaN stays: fminf and fmaxf would drop it.)
 template <int kAct>
 __device__ __forceinline__ float act_slope_safe(float v) {
   if constexpr (kAct == kActNone) return 1.0f;
-  const float s = act_slope<kAct>(fminf(fmaxf(v, -64.0f), 64.0f));
+  constexpr float kBound = act_half_bound<kAct>();
+  const float s = act_slope_of_half<kAct>(both(fminf(fmaxf(0.5f * v, -kBound), kBound))).x;
   return v == v ? s : v;
 }
 
@@ -274,24 +251,32 @@ __device__ __forceinline__ void a8_decode4(uint32_t w, float step, float2* v) {
   v[1] = mul2(add2(make_float2(f[2], f[3]), both(-8388736.0f)), both(step));
 }
 
-// Whether halves of values under exponent byte b can lie outside +-32: not with a
-// step of at most 1/2, nor in a block marked as not finite (NaN step).
-__device__ __forceinline__ bool a8_wide(float half) { return half > 0.25f; }
+// Whether halves of values (at most 127 half steps) can lie outside act_half_bound: with
+// a step above 1/2 (silu) or 1/16 (gelu), and not in a block marked as not finite (NaN
+// step).
+template <int kAct>
+__device__ __forceinline__ bool a8_wide(float half) {
+  constexpr float kMost = kAct == kActSilu ? 0.25f : 0.03125f;
+  static_assert(127.0f * kMost <= act_half_bound<kAct>(), "blocks of smaller steps need no narrowing");
+  return half > kMost;
+}
+template <int kAct>
 __device__ __forceinline__ float2 a8_narrow(float2 h) {
-  return make_float2(fminf(fmaxf(h.x, -32.0f), 32.0f), fminf(fmaxf(h.y, -32.0f), 32.0f));
+  constexpr float kBound = act_half_bound<kAct>();
+  return make_float2(fminf(fmaxf(h.x, -kBound), kBound), fminf(fmaxf(h.y, -kBound), kBound));
 }
 
-// Halves of the values of 4 N codes, `half` the half step, brought back to +-32
-// (see act_slope_safe) if kNarrow.  Where the step is at most 1/2 the subtraction and
-// the product are one exact fused operation; NaN steps go the same way and stay NaN.
-template <bool kNarrow, int N>
+// Halves of the values of 4 N codes, `half` the half step, brought back to the bound
+// (see act_half_bound) if kNarrow.  Where the step is small the subtraction and the
+// product are one exact fused operation; NaN steps go the same way and stay NaN.
+template <int kAct, bool kNarrow, int N>
 __device__ __forceinline__ void a8_decode_halves(const uint32_t (&w)[N], float half, float2 (&h)[2 * N]) {
-  if (a8_wide(half)) {
+  if (a8_wide<kAct>(half)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) a8_decode4(w[i], half, h + 2 * i);
     if constexpr (kNarrow)
 #pragma unroll
-      for (int e = 0; e < 2 * N; ++e) h[e] = a8_narrow(h[e]);
+      for (int e = 0; e < 2 * N; ++e) h[e] = a8_narrow<kAct>(h[e]);
     return;
   }
   const float off = -8388736.0f * half;

@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, kMode == Read::kGrad ? 3 : 4) act8_r
         T::unpack8(d[j], dy);
         if constexpr (kAct != kActNone) {
           const uint32_t w[2] = {k[j].x, k[j].y};
-          a8_decode_halves<true>(w, 0.5f * a8_step(eb[j]), v);
+          a8_decode_halves<kAct, true>(w, 0.5f * a8_step(eb[j]), v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = mul2(dy[e], act_slope_of_half<kAct>(v[e]));
         } else {

@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           for (int h = 0; h < 2; ++h) {
             float2 v[8];
             const float half = 0.5f * a8_step(eb);
-            a8_decode_halves<!kValue>(h ? kb : ka, half, v);
+            a8_decode_halves<kAct, !kValue>(h ? kb : ka, half, v);
             auto multiply = [&](int e, float2 slope) {
               const float2 d = mul2(slope, make_float2(__uint_as_float(raw[16 * h + 2 * e]),
                                                        __uint_as_float(raw[16 * h + 2 * e + 1])));
@@ -488,9 +488,9 @@ __global__ void __launch_bounds__(kLinThreads, 1)
                 multiply(e, act_slope_and_value<kAct>(v[e], narrowed, value));
                 packed_value[8 * h + e] = T::pack(value.x, value.y);
               };
-              if (a8_wide(half)) {
+              if (a8_wide<kAct>(half)) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) both_of(e, a8_narrow(v[e]));
+                for (int e = 0; e < 8; ++e) both_of(e, a8_narrow<kAct>(v[e]));
               } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) both_of(e, v[e]);
