@@ -828,7 +828,10 @@ def channel_mlp_bwd(dy: torch.Tensor, saved: ChannelMlpSaved, gamma, beta, w1: t
     checkpoints: the activation by the product dy w2, whose epilogue reads them for
     act' (:func:`linear_bwd_data`), the normalised input by a pass of its own.  The
     skip connection's gradient rides in the layer norm's.
-    While the call runs it holds the activation and its gradient, 4 H bytes a row.
+    While the call runs it holds the activation and its gradient, 4 H bytes a row, then the
+    gradient and the normalised input, whose place dx takes, 2 H + 2 C: at most max(4 H, 2 H +
+    2 C) bytes a row, the weight gradients, and a workspace of :func:`linear_bwd_weight`
+    (linear_bwd_weight_workspace_bytes).
     """
     x, pre = saved.xhat, saved.pre
     return _channel.channel_mlp_bwd(dy, x[0], x[1], x[2], saved.rstd, pre[0], pre[1], pre[2], gamma, beta, w1, w2, act,
