@@ -123,11 +123,15 @@ def load_peaks():
     return FALLBACK_PEAKS, "fallback"
 
 
+# The convolution kernel's device code: its file and every header of csrc/ it includes.
+KERNEL_SOURCES = ("conv3d_kernel.cuh", "pipeline.cuh", "ptx.cuh")
+
+
 def kernel_source_hash():
     """Fingerprint of the device code the ncu counters were taken on."""
     h = hashlib.sha256()
-    for rel in ("csrc/conv3d_kernel.cuh", "csrc/ptx.cuh"):
-        with open(os.path.join(ROOT, "video_vae_convolution_implicit_b200", rel), "rb") as f:
+    for name in KERNEL_SOURCES:
+        with open(os.path.join(ROOT, "video_vae_convolution_implicit_b200", "csrc", name), "rb") as f:
             h.update(f.read())
     return h.hexdigest()[:16]
 
