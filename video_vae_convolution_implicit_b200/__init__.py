@@ -222,6 +222,44 @@ def _stream_handle(stream) -> int:
     return int(stream)
 
 
+class _CallOn:
+    """The stream a call is given, current while the call lasts, so that what it allocates
+    belongs to the stream its kernels run on and is not handed to another one before they
+    have run.  Enters as the stream to run on (None: the current one).
+
+    CUDA's handle 1 is the legacy default stream, torch's 0.  Handle 2 is the calling
+    thread's, which torch's allocator cannot keep memory for: the current stream's is used,
+    and the two streams wait for each other around the call."""
+
+    def __init__(self, stream):
+        self._stream, self._guard, self._lender = stream, None, None
+
+    def __enter__(self):
+        if self._stream is None:
+            return None
+        handle = _stream_handle(self._stream)
+        if handle == 2:
+            lender = torch.cuda.current_stream()
+            torch.cuda.ExternalStream(2).wait_stream(lender)
+            self._lender = lender
+            return handle
+        if handle in (0, 1):
+            handle, stream = 0, torch.cuda.default_stream()
+        elif isinstance(self._stream, torch.cuda.Stream):
+            stream = self._stream
+        else:
+            stream = torch.cuda.ExternalStream(handle)
+        self._guard = torch.cuda.stream(stream)
+        self._guard.__enter__()
+        return handle
+
+    def __exit__(self, *error):
+        if self._lender is not None:
+            self._lender.wait_stream(torch.cuda.ExternalStream(2))
+        if self._guard is not None:
+            self._guard.__exit__(*error)
+
+
 def output_shape(D, H, W, kernel, stride=(1, 1, 1), pad=(0, 1, 1), tpad=TPAD_CAUSAL_REPLICATE):
     out = _i3()
     _check(_lib.conv3d_output_shape(D, H, W, _i3(*kernel), _i3(*stride), _i3(*pad), tpad, out))
@@ -334,11 +372,12 @@ def conv3d_fwd(x: torch.Tensor, w: torch.Tensor, bias, residual, y: torch.Tensor
 def conv3d(x: torch.Tensor, w: torch.Tensor, bias=None, residual=None, stride=(1, 1, 1),
            pad=(0, 1, 1), tpad=TPAD_CAUSAL_REPLICATE, stream=None, prev=None) -> torch.Tensor:
     """Allocate y (torch) and run :func:`conv3d_fwd`."""
-    N, D, H, W, _ = x.shape
-    Cout, kt, kh, kw, _ = w.shape
-    out = output_shape(D, H, W, (kt, kh, kw), stride, pad, tpad)
-    y = torch.empty((N, *out, Cout), dtype=x.dtype, device=x.device)
-    return conv3d_fwd(x, w, bias, residual, y, stride, pad, tpad, stream, prev=prev)
+    with _CallOn(stream) as s:
+        N, D, H, W, _ = x.shape
+        Cout, kt, kh, kw, _ = w.shape
+        out = output_shape(D, H, W, (kt, kh, kw), stride, pad, tpad)
+        y = torch.empty((N, *out, Cout), dtype=x.dtype, device=x.device)
+        return conv3d_fwd(x, w, bias, residual, y, stride, pad, tpad, s, prev=prev)
 
 
 def conv3d_gn_ptr(x, stats, gamma, beta, groups, per_frame, apply_silu, w, bias, residual, y, N,
@@ -360,26 +399,27 @@ def conv3d_gn(x: torch.Tensor, stats, gamma, beta, w: torch.Tensor, bias=None,
     applied as the convolution reads x (``stats`` from groupnorm_stats over x, or
     None for plain x).  With ``out_groups`` > 0 also returns the per-sample
     GroupNorm statistics of y ([N, out_groups, 2] float64): (y, out_stats)."""
-    N, D, H, W, Cin = x.shape
-    Cout, kt, kh, kw, _ = w.shape
-    groups = (stats.shape[1] if stats is not None else 1) if groups is None else groups
-    if y is None:
-        out = output_shape(D, H, W, (kt, kh, kw), stride, pad, tpad)
-        y = torch.empty((N, *out, Cout), dtype=x.dtype, device=x.device)
-    for name, t in (("x", x), ("w", w), ("y", y)):
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of x's dtype")
-    if stats is not None and (stats.dtype != torch.float64 or not stats.is_cuda):
-        raise ValueError("stats must be a float64 CUDA tensor")
-    out_stats = (torch.empty((N, out_groups, 2), dtype=torch.float64, device=x.device)
-                 if out_groups > 0 else None)
-    _check(conv3d_gn_ptr(x.data_ptr(), _ptr(stats), _ptr(gamma), _ptr(beta), groups,
-                         per_frame, apply_silu, w.data_ptr(), _ptr(bias), _ptr(residual),
-                         y.data_ptr(), N, Cin, D, H, W, Cout, (kt, kh, kw), stride, pad, tpad,
-                         _dtype_code(x.dtype), _stream_handle(stream), _ptr(out_stats), out_groups,
-                         out_eps))
-    _overwritten(y)
-    return (y, out_stats) if out_stats is not None else y
+    with _CallOn(stream) as s:
+        N, D, H, W, Cin = x.shape
+        Cout, kt, kh, kw, _ = w.shape
+        groups = (stats.shape[1] if stats is not None else 1) if groups is None else groups
+        if y is None:
+            out = output_shape(D, H, W, (kt, kh, kw), stride, pad, tpad)
+            y = torch.empty((N, *out, Cout), dtype=x.dtype, device=x.device)
+        for name, t in (("x", x), ("w", w), ("y", y)):
+            if not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype:
+                raise ValueError(f"{name} must be a contiguous CUDA tensor of x's dtype")
+        if stats is not None and (stats.dtype != torch.float64 or not stats.is_cuda):
+            raise ValueError("stats must be a float64 CUDA tensor")
+        out_stats = (torch.empty((N, out_groups, 2), dtype=torch.float64, device=x.device)
+                     if out_groups > 0 else None)
+        _check(conv3d_gn_ptr(x.data_ptr(), _ptr(stats), _ptr(gamma), _ptr(beta), groups,
+                             per_frame, apply_silu, w.data_ptr(), _ptr(bias), _ptr(residual),
+                             y.data_ptr(), N, Cin, D, H, W, Cout, (kt, kh, kw), stride, pad, tpad,
+                             _dtype_code(x.dtype), _stream_handle(s), _ptr(out_stats),
+                             out_groups, out_eps))
+        _overwritten(y)
+        return (y, out_stats) if out_stats is not None else y
 
 
 def poll_status(stream=None) -> int:
@@ -420,18 +460,19 @@ def groupnorm_stats(x: torch.Tensor, groups: int, eps: float = 1e-6, per_frame: 
                     stats: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """{mean, 1/sqrt(var+eps)} per (sample [, frame], group) of an NDHWC tensor, as a
     float64 CUDA tensor [sets, groups, 2] (``stats`` is reused when given)."""
-    if not x.is_cuda or not x.is_contiguous() or x.dim() != 5:
-        raise ValueError("x must be a contiguous CUDA tensor [N, D, H, W, C]")
-    N, D, H, W, C = x.shape
-    sets = N * D if per_frame else N
-    if stats is None:
-        stats = torch.empty((sets, groups, 2), dtype=torch.float64, device=x.device)
-    elif tuple(stats.shape) != (sets, groups, 2) or stats.dtype != torch.float64:
-        raise ValueError(f"stats must be float64 {(sets, groups, 2)}")
-    _check(groupnorm_stats_ptr(x.data_ptr(), N, D, H, W, C, groups, per_frame, eps,
-                               _dtype_code(x.dtype), stats.data_ptr(), _stream_handle(stream)))
-    _overwritten(stats)
-    return stats
+    with _CallOn(stream) as s:
+        if not x.is_cuda or not x.is_contiguous() or x.dim() != 5:
+            raise ValueError("x must be a contiguous CUDA tensor [N, D, H, W, C]")
+        N, D, H, W, C = x.shape
+        sets = N * D if per_frame else N
+        if stats is None:
+            stats = torch.empty((sets, groups, 2), dtype=torch.float64, device=x.device)
+        elif tuple(stats.shape) != (sets, groups, 2) or stats.dtype != torch.float64:
+            raise ValueError(f"stats must be float64 {(sets, groups, 2)}")
+        _check(groupnorm_stats_ptr(x.data_ptr(), N, D, H, W, C, groups, per_frame, eps,
+                                   _dtype_code(x.dtype), stats.data_ptr(), _stream_handle(s)))
+        _overwritten(stats)
+        return stats
 
 
 def groupnorm_silu(x: torch.Tensor, stats: torch.Tensor, gamma=None, beta=None, y=None,
@@ -439,20 +480,21 @@ def groupnorm_silu(x: torch.Tensor, stats: torch.Tensor, gamma=None, beta=None, 
                    stream=None) -> torch.Tensor:
     """y = silu((x - mean) * rstd * gamma + beta) with ``stats`` from groupnorm_stats.
     ``y`` may be ``x`` (in place); it is allocated when None."""
-    if not x.is_cuda or not x.is_contiguous() or x.dim() != 5:
-        raise ValueError("x must be a contiguous CUDA tensor [N, D, H, W, C]")
-    N, D, H, W, C = x.shape
-    groups = stats.shape[1] if groups is None else groups
-    if y is None:
-        y = torch.empty_like(x)
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None and (tuple(t.shape) != (C,) or t.dtype != x.dtype or not t.is_cuda):
-            raise ValueError(f"{name} must be a CUDA [C] tensor of x's dtype")
-    _check(groupnorm_silu_ptr(x.data_ptr(), stats.data_ptr(), _ptr(gamma), _ptr(beta),
-                              y.data_ptr(), N, D, H, W, C, groups, per_frame, apply_silu,
-                              _dtype_code(x.dtype), _stream_handle(stream)))
-    _overwritten(y)
-    return y
+    with _CallOn(stream) as s:
+        if not x.is_cuda or not x.is_contiguous() or x.dim() != 5:
+            raise ValueError("x must be a contiguous CUDA tensor [N, D, H, W, C]")
+        N, D, H, W, C = x.shape
+        groups = stats.shape[1] if groups is None else groups
+        if y is None:
+            y = torch.empty_like(x)
+        for name, t in (("gamma", gamma), ("beta", beta)):
+            if t is not None and (tuple(t.shape) != (C,) or t.dtype != x.dtype or not t.is_cuda):
+                raise ValueError(f"{name} must be a CUDA [C] tensor of x's dtype")
+        _check(groupnorm_silu_ptr(x.data_ptr(), stats.data_ptr(), _ptr(gamma), _ptr(beta),
+                                  y.data_ptr(), N, D, H, W, C, groups, per_frame, apply_silu,
+                                  _dtype_code(x.dtype), _stream_handle(s)))
+        _overwritten(y)
+        return y
 
 
 def conv3d_bwd_data_ptr(dy, w, dx, N, Cin, D, H, W, Cout, kernel, stride, pad, tpad, dtype,
@@ -473,21 +515,22 @@ def conv3d_bwd_data(dy: torch.Tensor, w: torch.Tensor, x_shape, pad=(0, 1, 1),
                     stride=(1, 1, 1)) -> torch.Tensor:
     """dx for the forward problem x [x_shape] -> y (dy has y's shape); temporal
     stride 1, spatial strides up to 8."""
-    N, D, H, W, Cin = x_shape
-    Cout, kt, kh, kw, _ = w.shape
-    if dx is None:
-        dx = torch.empty(tuple(x_shape), dtype=dy.dtype, device=dy.device)
-    need = bwd_data_workspace_bytes(N, Cin, D, H, W, Cout, (kt, kh, kw), pad, tpad)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dy.device)
-    for name, t in (("dy", dy), ("w", w), ("dx", dx)):
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != dy.dtype:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of dy's dtype")
-    _check(conv3d_bwd_data_ptr(dy.data_ptr(), w.data_ptr(), dx.data_ptr(), N, Cin, D, H, W, Cout,
-                               (kt, kh, kw), tuple(stride), pad, tpad, _dtype_code(dy.dtype),
-                               workspace.data_ptr(), workspace.numel(), _stream_handle(stream)))
-    _overwritten(dx)
-    return dx
+    with _CallOn(stream) as s:
+        N, D, H, W, Cin = x_shape
+        Cout, kt, kh, kw, _ = w.shape
+        if dx is None:
+            dx = torch.empty(tuple(x_shape), dtype=dy.dtype, device=dy.device)
+        need = bwd_data_workspace_bytes(N, Cin, D, H, W, Cout, (kt, kh, kw), pad, tpad)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dy.device)
+        for name, t in (("dy", dy), ("w", w), ("dx", dx)):
+            if not t.is_cuda or not t.is_contiguous() or t.dtype != dy.dtype:
+                raise ValueError(f"{name} must be a contiguous CUDA tensor of dy's dtype")
+        _check(conv3d_bwd_data_ptr(dy.data_ptr(), w.data_ptr(), dx.data_ptr(), N, Cin, D, H, W, Cout,
+                                   (kt, kh, kw), tuple(stride), pad, tpad, _dtype_code(dy.dtype),
+                                   workspace.data_ptr(), workspace.numel(), _stream_handle(s)))
+        _overwritten(dx)
+        return dx
 
 
 def conv3d_bwd_weight_ptr(x, dy, dw, dbias, N, Cin, D, H, W, Cout, kernel, stride, pad, tpad,
@@ -506,21 +549,22 @@ def conv3d_bwd_weight(x: torch.Tensor, dy: torch.Tensor, kernel, stride=(1, 1, 1
                       tpad=TPAD_CAUSAL_REPLICATE, with_bias: bool = True,
                       workspace: torch.Tensor | None = None, stream=None):
     """(dw, dbias) for the forward problem x -> y with upstream gradient dy."""
-    N, D, H, W, Cin = x.shape
-    Cout = dy.shape[-1]
-    dw = torch.empty((Cout, *kernel, Cin), dtype=x.dtype, device=x.device)
-    db = torch.empty((Cout,), dtype=x.dtype, device=x.device) if with_bias else None
-    need = bwd_weight_workspace_bytes(Cin, Cout, kernel)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    for name, t in (("x", x), ("dy", dy)):
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of x's dtype")
-    _check(conv3d_bwd_weight_ptr(x.data_ptr(), dy.data_ptr(), dw.data_ptr(), _ptr(db), N, Cin, D,
-                                 H, W, Cout, tuple(kernel), stride, pad, tpad,
-                                 _dtype_code(x.dtype), workspace.data_ptr(), workspace.numel(),
-                                 _stream_handle(stream)))
-    return dw, db
+    with _CallOn(stream) as s:
+        N, D, H, W, Cin = x.shape
+        Cout = dy.shape[-1]
+        dw = torch.empty((Cout, *kernel, Cin), dtype=x.dtype, device=x.device)
+        db = torch.empty((Cout,), dtype=x.dtype, device=x.device) if with_bias else None
+        need = bwd_weight_workspace_bytes(Cin, Cout, kernel)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        for name, t in (("x", x), ("dy", dy)):
+            if not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype:
+                raise ValueError(f"{name} must be a contiguous CUDA tensor of x's dtype")
+        _check(conv3d_bwd_weight_ptr(x.data_ptr(), dy.data_ptr(), dw.data_ptr(), _ptr(db), N, Cin, D,
+                                     H, W, Cout, tuple(kernel), stride, pad, tpad,
+                                     _dtype_code(x.dtype), workspace.data_ptr(), workspace.numel(),
+                                     _stream_handle(s)))
+        return dw, db
 
 
 def conv3d_bwd_data_cached(dy: torch.Tensor, w: torch.Tensor, x_shape, pad=(0, 1, 1),
@@ -528,44 +572,46 @@ def conv3d_bwd_data_cached(dy: torch.Tensor, w: torch.Tensor, x_shape, pad=(0, 1
                            stream=None):
     """(dx, dprev) for one chunk of the cached-frames mode (stride 1): dprev is
     the gradient of the kt-1 cached frames (None when with_prev is false)."""
-    N, D, H, W, Cin = x_shape
-    Cout, kt, kh, kw, _ = w.shape
-    dx = torch.empty(tuple(x_shape), dtype=dy.dtype, device=dy.device)
-    dprev = (torch.empty((N, kt - 1, H, W, Cin), dtype=dy.dtype, device=dy.device)
-             if with_prev and kt > 1 else None)
-    need = bwd_data_workspace_bytes(N, Cin, D, H, W, Cout, (kt, kh, kw), pad, TPAD_CAUSAL_CACHED)
-    if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dy.device)
-    for name, t in (("dy", dy), ("w", w)):
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != dy.dtype:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of dy's dtype")
-    _check(_lib.conv3d_bwd_data_cached(dy.data_ptr(), w.data_ptr(), dx.data_ptr(), _ptr(dprev), N,
-                                       Cin, D, H, W, Cout, _i3(kt, kh, kw), _i3(1, 1, 1),
-                                       _i3(*pad), _dtype_code(dy.dtype), workspace.data_ptr(),
-                                       workspace.numel(), _stream_handle(stream)))
-    return dx, dprev
+    with _CallOn(stream) as s:
+        N, D, H, W, Cin = x_shape
+        Cout, kt, kh, kw, _ = w.shape
+        dx = torch.empty(tuple(x_shape), dtype=dy.dtype, device=dy.device)
+        dprev = (torch.empty((N, kt - 1, H, W, Cin), dtype=dy.dtype, device=dy.device)
+                 if with_prev and kt > 1 else None)
+        need = bwd_data_workspace_bytes(N, Cin, D, H, W, Cout, (kt, kh, kw), pad, TPAD_CAUSAL_CACHED)
+        if workspace is None:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dy.device)
+        for name, t in (("dy", dy), ("w", w)):
+            if not t.is_cuda or not t.is_contiguous() or t.dtype != dy.dtype:
+                raise ValueError(f"{name} must be a contiguous CUDA tensor of dy's dtype")
+        _check(_lib.conv3d_bwd_data_cached(dy.data_ptr(), w.data_ptr(), dx.data_ptr(), _ptr(dprev), N,
+                                           Cin, D, H, W, Cout, _i3(kt, kh, kw), _i3(1, 1, 1),
+                                           _i3(*pad), _dtype_code(dy.dtype), workspace.data_ptr(),
+                                           workspace.numel(), _stream_handle(s)))
+        return dx, dprev
 
 
 def conv3d_bwd_weight_cached(x: torch.Tensor, prev: torch.Tensor | None, dy: torch.Tensor, kernel,
                              stride=(1, 1, 1), pad=(0, 1, 1), with_bias: bool = True,
                              workspace: torch.Tensor | None = None, stream=None):
     """(dw, dbias) for one chunk of the cached-frames mode; prev: the cached frames."""
-    N, D, H, W, Cin = x.shape
-    Cout = dy.shape[-1]
-    dw = torch.empty((Cout, *kernel, Cin), dtype=x.dtype, device=x.device)
-    db = torch.empty((Cout,), dtype=x.dtype, device=x.device) if with_bias else None
-    need = bwd_weight_workspace_bytes(Cin, Cout, kernel)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    for name, t in (("x", x), ("dy", dy), ("prev", prev)):
-        if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of x's dtype")
-    _check(_lib.conv3d_bwd_weight_cached(x.data_ptr(), _ptr(prev), dy.data_ptr(), dw.data_ptr(),
-                                         _ptr(db), N, Cin, D, H, W, Cout, _i3(*kernel),
-                                         _i3(*stride), _i3(*pad), _dtype_code(x.dtype),
-                                         workspace.data_ptr(), workspace.numel(),
-                                         _stream_handle(stream)))
-    return dw, db
+    with _CallOn(stream) as s:
+        N, D, H, W, Cin = x.shape
+        Cout = dy.shape[-1]
+        dw = torch.empty((Cout, *kernel, Cin), dtype=x.dtype, device=x.device)
+        db = torch.empty((Cout,), dtype=x.dtype, device=x.device) if with_bias else None
+        need = bwd_weight_workspace_bytes(Cin, Cout, kernel)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        for name, t in (("x", x), ("dy", dy), ("prev", prev)):
+            if t is not None and (not t.is_cuda or not t.is_contiguous() or t.dtype != x.dtype):
+                raise ValueError(f"{name} must be a contiguous CUDA tensor of x's dtype")
+        _check(_lib.conv3d_bwd_weight_cached(x.data_ptr(), _ptr(prev), dy.data_ptr(), dw.data_ptr(),
+                                             _ptr(db), N, Cin, D, H, W, Cout, _i3(*kernel),
+                                             _i3(*stride), _i3(*pad), _dtype_code(x.dtype),
+                                             workspace.data_ptr(), workspace.numel(),
+                                             _stream_handle(s)))
+        return dw, db
 
 
 class _NoSecondDerivative(torch.autograd.Function):
