@@ -878,6 +878,10 @@ def channel_mlp_bwd(dy: torch.Tensor, saved: ChannelMlpSaved, gamma, beta, w1: t
     gradient and the normalised input, whose place dx takes, 2 H + 2 C: at most max(4 H, 2 H +
     2 C) bytes a row, the weight gradients, and a workspace of :func:`linear_bwd_weight`
     (linear_bwd_weight_workspace_bytes).
+
+    What goes into the products is rounded to 16 bits: the two recomputed inputs, the hidden
+    activation's gradient and the normalised input's.  From the same checkpoints the bf16
+    results are off by about 0.003 of their norm, their own rounding being 0.0017 of it.
     """
     x, pre = saved.xhat, saved.pre
     return _channel.channel_mlp_bwd(dy, x[0], x[1], x[2], saved.rstd, pre[0], pre[1], pre[2], gamma, beta, w1, w2, act,
@@ -949,7 +953,9 @@ class LinearFunction(torch.autograd.Function):
 
 
 def linear_autograd(x, w, bias=None, residual=None, act: int = ACT_NONE):
-    """y = act(x w^T + bias) + residual with gradients for x, w, bias and residual."""
+    """y = act(x w^T + bias) + residual with gradients for x, w, bias and residual.
+    With an activation act' is taken at the 8-bit checkpoint of x w^T + bias (off by at most
+    1/64 of the largest magnitude in its block of 32 channels), which is what is kept of it."""
     return LinearFunction.apply(x, w, bias, residual, act)
 
 
@@ -978,5 +984,7 @@ class ChannelMlpFunction(torch.autograd.Function):
 
 
 def channel_mlp_autograd(x, gamma, beta, w1, b1, w2, b2, act: int = ACT_GELU, eps: float = 1e-6):
-    """channel_mlp with gradients for x, gamma, beta, w1, b1, w2 and b2."""
+    """channel_mlp with gradients for x, gamma, beta, w1, b1, w2 and b2, taken at the 8-bit
+    checkpoints of the normalised input and the pre-activation (each value off by at most 1/64
+    of the largest magnitude in its block of 32 channels): see :func:`channel_mlp_bwd`."""
     return ChannelMlpFunction.apply(x, gamma, beta, w1, b1, w2, b2, act, eps)

@@ -592,8 +592,10 @@ struct UnitWalk {
 constexpr int kUnroll = 4;   // units in flight per thread
 
 // Measured on B200 (bf16, graph replays): 36864 x 2048 written 36 us (6.3 TB/s), read
-// 39 (5.9), read through GELU 42 (5.5), through gamma, beta and SiLU 47 (4.9), dy
-// times GELU' 65 (5.8); 1000 x 136 2 us.  Bound by HBM; the affine read by issue too.
+// 39 (5.9), read through SiLU 48 (4.8), through GELU 50 (4.6), through gamma, beta and
+// SiLU 54 (4.2), dy times GELU' 72 (5.3); 1000 x 136 2 us.  Bound by HBM, under an
+// activation also by its two special functions a value (34 us of that unit's time here)
+// and by issue.
 
 template <bool kBF16>
 __global__ void __launch_bounds__(kThreads) act8_pack_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ q,

@@ -15,25 +15,29 @@
 // BN columns, warp-specialised as the convolution is -- TMA producer, one
 // tcgen05.mma issuer (cta_group::2), and epilogue warps over two TMEM
 // accumulators.  At 8 k-blocks a tile the epilogue has about as many issue slots
-// to spend as the tensor cores take for the tile (16 instructions a value with
-// the GELU derivative), and a chunk is a long chain of dependent steps (TMEM load,
-// arithmetic, staging, store): 16 warps, four to a scheduler, hide it where 8
-// left two thirds of the slots empty.  The chunks go out by plain 16-byte stores
-// through a swizzled buffer of the warp's own, and the residual and the codes come
-// in by cp.async, 16 bytes a thread, one chunk ahead.  A warp hands its part of the
-// accumulator back as soon as it is in registers, by an arrival that waits for no
-// global store.  Columns are the fast tile index, so the tiles in flight share rows
-// of A and A is read from HBM about once; w stays in L2.
+// to spend as the tensor cores take for the tile (17 instructions a value with the
+// GELU derivative, two of them special functions), and a chunk is a long chain of
+// dependent steps (TMEM load, arithmetic, staging, store): 16 warps, four to a
+// scheduler, hide it where 8 left two thirds of the slots empty.  The chunks go out by
+// plain 16-byte stores through a swizzled buffer of the warp's own, and the residual and
+// the codes come in by cp.async, 16 bytes a thread, one chunk ahead.  A warp hands its
+// part of the accumulator back as soon as it is in registers, by an arrival that waits
+// for no global store.  Columns are the fast tile index, so the tiles in flight share
+// rows of A and A is read from HBM about once; w stays in L2.
 //
-// Measured on B200 (bf16, 36864 rows, 512 -> 2048, 77 GFLOP, graph replays): plain
-// 71 us (a plain library product 64), GELU 74, GELU and checkpoint 91, gradient 68,
-// with GELU' from the checkpoint 86; on a chip 5% slower, residual 89, GELU' and the
-// recomputed activation 118.  104448 rows of 2048 -> 512: 174 us, 1260 TFLOP/s
-// (157).  What bounds it: under the plain product the tensor cores are busy 58% of the cycles, with
-// GELU' and the checkpoint 47%, issue slots 47%, the shared-memory data path 41 to
-// 64%, HBM 30%; no unit is full, each tile's 256 KB of operand copies, their reads
-// by the tensor cores and the 130 to 200 KB of staging meet in one shared memory, and
-// the chip runs at its power limit (1.5 to 1.7 GHz).
+// Measured on B200 (bf16, 36864 rows, 512 -> 2048, 77 GFLOP, graph replays, us: a
+// burst of eight after a rest / replayed for a second, at the power limit, which takes
+// the clock from 1.97 to between 1.3 and 1.5 GHz): plain 73 / 85 (a plain library
+// product 72 / 80), SiLU 81 / 90, GELU 81 / 94, GELU and checkpoint 96 / 112, residual
+// 85 / 105, gradient 71 / 83, with GELU' from the checkpoint 92 / 108, and the
+// recomputed activation 118 / 139.  104448 rows: 2048 -> 512 175 / 210 (157 / 198),
+// 512 -> 2048 197 / 236 (186 / 222).  Whether the operands lie in L2 or come from HBM
+// changes none of these by more than 1%; the clock does.  What bounds it: under the
+// plain product the tensor cores are busy 56% of the cycles, with an activation and its
+// checkpoint 43 to 46%, issue slots 50%, the special functions' unit 46%, the
+// shared-memory data path 42 to 50%, HBM 30%; no unit is full, each tile's 256 KB of
+// operand copies, their reads by the tensor cores and the 130 to 200 KB of staging meet
+// in one shared memory, and the chip runs at its power limit.
 //
 // linear_rows_kernel (few rows): one 128-channel x up-to-128-row tile per
 // cluster, transposed (w is the 128-row operand, the rows of x are the N side),
@@ -41,7 +45,8 @@
 // in shared memory: w, the bulk of the bytes, streams through as many SMs as
 // there are pieces, in one launch and without a workspace, and the sum runs in
 // rank order whatever the timing.  Measured (bf16, GELU, weights from HBM, graph
-// replays): 8 x 512 -> 2048 3.5 us, 61 x 1024 -> 1000 4.9, 64 x 2048 -> 2048 6.8:
+// replays): 8 x 512 -> 2048 3.6 us, 61 x 1024 -> 1000 5.2, 64 x 2048 -> 2048 7.1; the
+// gradient with GELU' of the same sizes 4.4, 5.1 and 7.2, of 1 x 512 -> 2048 4.1:
 // latencies one after the other (a first copy 0.6 us, the following k-blocks 0.3 us
 // each, the meeting of the ranks 0.5 to 1.2 us).
 //
@@ -63,7 +68,8 @@ constexpr uint32_t kLinABytes = BM * BK * 2;           // one CTA's A rows of a 
 constexpr uint32_t kLinOutBytes = 32 * 32 * 2;         // a 32 x 32 chunk of 16-bit values
 // Chunks in an epilogue warp's output buffer: two where it writes twice, the codes
 // or the recomputed activation beside the values (104448 rows, 512 -> 2048: GELU' and
-// the activation 301 us, 345 with one; 36864 rows, GELU and checkpoint 90.6, 91.8);
+// the activation 301 us, 345 with one; 36864 rows, GELU and checkpoint 90.6, 91.8; both
+// measured with a cheaper activation);
 // elsewhere a pipeline stage is worth more (36864 rows, plain: 71 us with one, 76 with
 // two).
 __host__ __device__ constexpr int lin_out_chunks(bool bwd, bool q, bool value) { return value || (q && !bwd) ? 2 : 1; }

@@ -19,8 +19,8 @@
 //
 // Measured (bf16 with dbias; the 1x1x1 convolution's kernel in brackets): 104448
 // rows, 512 -> 2048 187 us (263) and 2048 -> 512 180 us (218), 1170 and 1220
-// TFLOP/s: the tensor cores are busy 65 to 68% of the cycles, under the chip's power
-// limit; stages of 64 rows, twice as many, took 235 and 208.  540672 rows of 512 ->
+// TFLOP/s (in bursts; replayed for a second, at the chip's power limit and 1.3 GHz, 231
+// us each): the tensor cores are busy 65 to 68% of the cycles; stages of 64 rows, twice as many, took 235 and 208.  540672 rows of 512 ->
 // 256 135 us (195), 6.1 TB/s: the rows' reads.  10000 rows of 128 x 128 12 us (13),
 // 61 rows of 1000 x 1024 9 us (20): launches and latency.
 #pragma once
